@@ -12,4 +12,9 @@ from .api import (  # noqa: F401
     segment_begin, version, SparseAllReduce, sparse_all_reduce, topk_count, SPARSE_MODES,
     occupancy_caps,
 )
+from .steps import (  # noqa: F401
+    Checkpoint, CheckpointPack, CheckpointUnpack, Embedding, EmbeddingGrad, LayerNorm, LayerNormGrad, TokenLogprobs,
+    TokenLogprobsGrad, checkpoint_pack, checkpoint_unpack, embedding, embedding_grad, layer_norm, layer_norm_grad,
+    token_logprobs, token_logprobs_grad,
+)
 from ._lib import RsxError  # noqa: F401

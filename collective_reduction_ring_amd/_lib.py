@@ -22,6 +22,8 @@ RSX_SPARSE_THRESHOLD, RSX_SPARSE_TOPK = 0, 1
 RSX_MAX_RANKS = 16
 RSX_NAIVE_MAX_BYTES = 32768
 RSX_FUSE_BATCH = 248
+RSX_TOP_MAX = 64
+RSX_CHECKPOINT_BLOCK = 32
 RSX_FUSION_THRESHOLD_DEFAULT = 64 * 1024 * 1024   # Horovod's default tensor_fusion_threshold
 
 STATUS = {
@@ -56,6 +58,18 @@ SIGNATURES = {
                                    _P, _P, _SZ, _P]),
     "rsx_sparse_all_reduce_noalloc": (_I, [_PP, _PP, _PP, _I, _SZ, _I, ctypes.c_float, _SZ, _PP, _PP,
                                            _SZ, _P, _P]),
+    "rsx_embedding": (_I, [_P, _SZ, _SZ, _SZ, _I, _P, _SZ, _I, ctypes.c_int64, ctypes.c_float, _P, _SZ, _I, _P]),
+    "rsx_embedding_grad_workspace_size": (_SZ, [_SZ, _SZ]),
+    "rsx_embedding_grad": (_I, [_P, _SZ, _I, _P, _SZ, _I, ctypes.c_int64, ctypes.c_float, _P, _SZ, _SZ, _SZ, _I, _I,
+                                _P, _SZ, _P]),
+    "rsx_layer_norm": (_I, [_P, _SZ, _P, _P, _P, _SZ, _P, _P, _P, _P, _SZ, _SZ, ctypes.c_float, _I, _I, _P]),
+    "rsx_layer_norm_grad_workspace_size": (_SZ, [_SZ, _SZ]),
+    "rsx_layer_norm_grad": (_I, [_P, _SZ, _P, _SZ, _P, _P, _P, _P, _P, _P, _SZ, _P, _P, _SZ, _SZ, _I, _I, _P, _SZ, _P]),
+    "rsx_checkpoint_pack": (_I, [_P, _SZ, _P, _P, _SZ, _SZ, _I, _P]),
+    "rsx_checkpoint_unpack": (_I, [_P, _P, _P, _SZ, _SZ, _SZ, _I, _P]),
+    "rsx_token_logprobs_workspace_size": (_SZ, [_SZ, _SZ, _I]),
+    "rsx_token_logprobs": (_I, [_P, _SZ, _I, _P, _I, _SZ, _SZ, _I, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "rsx_token_logprobs_grad": (_I, [_P, _SZ, _I, _P, _I, _P, _P, _P, _P, _P, _SZ, _SZ, _SZ, _P]),
     "rsx_segment_begin": (_SZ, [_SZ, _I, _I]),
     "rsx_dtype_size": (_SZ, [_I]),
     "rsx_status_string": (ctypes.c_char_p, [_I]),

@@ -26,12 +26,16 @@ namespace {
 
 thread_local char g_hip_error[256] = "HIP error";
 
+}  // namespace
+
 rsx_status_t hip_status(hipError_t e) {
   if (e == hipSuccess) return RSX_SUCCESS;
   snprintf(g_hip_error, sizeof(g_hip_error), "HIP error %d: %s", static_cast<int>(e),
            hipGetErrorString(e));
   return RSX_ERR_HIP;
 }
+
+namespace {
 
 size_t esize_of(int dtype) {
   switch (dtype) {

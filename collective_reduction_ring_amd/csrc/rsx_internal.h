@@ -9,6 +9,9 @@
 
 namespace rsx {
 
+// Status of a HIP call; a failure's text is kept for rsx_status_string.
+rsx_status_t hip_status(hipError_t e);
+
 constexpr int kBlock = 256;        // threads per workgroup: 4 wave64s
 constexpr int kVecBytes = 16;      // one dwordx4 per lane per source
 

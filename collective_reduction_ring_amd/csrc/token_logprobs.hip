@@ -1,0 +1,416 @@
+// Log probabilities of given tokens, with the entropy and the most likely
+// alternatives, and their gradient.
+//
+//   lse = log sum exp z,  log p_j = z_j - lse,
+//   logprob = log p_token,  entropy H = -sum p_j log p_j,
+//   dz_j = g (delta(j, token) - p_j) - h p_j (log p_j + H)
+//   for gradients g of the log probability and h of the entropy.
+//
+// The forward pass reads a row once: each lane keeps a running maximum m, the
+// sum s of 2^u and the sum t of 2^u u, u = (z - m) log2 e, all in fp32.  Then
+// lse = m + ln s and H = ln s - t ln 2 / s, a sum of two terms that are not
+// negative, so nothing cancels.  A masked logit (-inf) adds nothing; a row of
+// nothing else has lse = -inf, log probabilities of -inf, entropy 0 and a
+// gradient of 0.  A row with a NaN or +inf has NaN for lse, log probabilities,
+// entropy and gradient.  A token outside the row has log probability 0 and no
+// gradient through it.
+#include "step_device.h"
+
+namespace rsx {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ uint64_t token_at(const void* tokens, uint64_t i, int wide) {
+  return wide ? static_cast<uint64_t>(static_cast<const int64_t*>(tokens)[i])
+              : static_cast<uint64_t>(static_cast<int64_t>(static_cast<const int32_t*>(tokens)[i]));
+}
+
+// ------------------------------------------------------- softmax statistics
+struct Stats {
+  float m, s, t;
+};
+constexpr float kLeast = -1e30f;  // stands in for u = -inf where u is a factor
+
+// The maximum that u is taken against: 0 while there is none.
+__device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// `a` against the larger maximum m.
+__device__ __forceinline__ Stats rebase(const Stats& a, float m) {
+  const float d = (a.m - reference(m)) * kLog2e;
+  const float f = __builtin_amdgcn_exp2f(d);
+  const float dd = fmaxf(d, kLeast);
+  return {m, a.s * f, (a.t + dd * a.s) * f};
+}
+__device__ __forceinline__ Stats merge(const Stats& a, const Stats& b) {
+  const float m = fmaxf(a.m, b.m);
+  const Stats x = rebase(a, m), y = rebase(b, m);
+  return {m, x.s + y.s, x.t + y.t};
+}
+__device__ __forceinline__ Stats wave_merge(Stats a) {
+  const float m = wave_max(a.m);
+  const Stats x = rebase(a, m);
+  return {m, wave_sum(x.s), wave_sum(x.t)};
+}
+
+// --------------------------------------------------------- top alternatives
+// A candidate as one integer: its value in order (a NaN below every number,
+// -0 equal to +0) in the high half, the complement of its index in the low
+// half, so that of equal values the lower index is the larger candidate.  0
+// is no candidate.
+__device__ __forceinline__ uint32_t value_order(float z) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, z + 0.0f);
+  const uint32_t o = b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+  return z == z ? o : 1u;
+}
+__device__ __forceinline__ float order_value(uint32_t o) {
+  const uint32_t b = o ^ ((o >> 31) ? 0x80000000u : 0xffffffffu);
+  return o == 1u ? __builtin_bit_cast(float, 0x7fc00000u) : __builtin_bit_cast(float, b);
+}
+__device__ __forceinline__ uint64_t candidate(uint32_t order, uint32_t index) {
+  return (static_cast<uint64_t>(order) << 32) | (0xffffffffu - index);
+}
+__device__ __forceinline__ uint64_t lane_value64(uint64_t v, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(v), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(v >> 32), lane);
+  return (static_cast<uint64_t>(hi) << 32) | lo;
+}
+
+// A wave's best candidates, one a lane, largest first; `least` is the top-th.
+struct Best {
+  uint64_t mine, floor, least;  // least = the larger of the top-th and of `floor`, a bound known to be passed
+};
+__device__ __forceinline__ void insert(Best& b, uint64_t c, uint32_t lane, uint32_t top) {
+  const uint32_t at = static_cast<uint32_t>(__popcll(__ballot(b.mine > c)));
+  // lane i takes lane i - 1's
+  const uint32_t lo = __builtin_amdgcn_mov_dpp(static_cast<int>(b.mine), 0x138, 0xf, 0xf, true);
+  const uint32_t hi = __builtin_amdgcn_mov_dpp(static_cast<int>(b.mine >> 32), 0x138, 0xf, 0xf, true);
+  if (lane > at) b.mine = (static_cast<uint64_t>(hi) << 32) | lo;
+  if (lane == at) b.mine = c;
+  const uint64_t last = lane_value64(b.mine, static_cast<int>(top) - 1);
+  b.least = last > b.floor ? last : b.floor;
+}
+// The top-th largest of the lanes' values, one bit at a time.
+__device__ __forceinline__ uint32_t lanes_nth(uint32_t v, uint32_t top) {
+  uint64_t alive = ~0ull;
+  uint32_t found = 0, need = top;
+#pragma unroll
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint64_t set = __ballot((v >> bit) & 1u) & alive;
+    const uint32_t c = static_cast<uint32_t>(__popcll(set));
+    if (c >= need) {
+      alive = set;
+      found |= 1u << bit;
+    } else {
+      need -= c;
+      alive &= ~set;
+    }
+  }
+  return found;
+}
+
+// ---------------------------------------------------------------- forward
+constexpr int kUnroll = 4;  // vectors a lane has in flight
+
+struct Partial {
+  float m, s, t, pad;
+};
+
+__device__ __forceinline__ float finish_row(const LogprobArgs& a, uint64_t row, const Stats& st) {
+  const bool none = st.s == 0.0f && st.m == -INFINITY;  // every logit masked
+  const float ln_s = logf(st.s);
+  const float lse = none ? -INFINITY : st.m + ln_s;
+  const uint64_t tok = token_at(a.tokens, row, a.wide);
+  float z = 0.0f, lp = 0.0f;
+  if (tok < a.vocab) {
+    const uint64_t at = row * a.stride + tok;
+    z = a.type == RSX_FLOAT32    ? static_cast<const float*>(a.logits)[at]
+        : a.type == RSX_BFLOAT16 ? static_cast<float>(static_cast<const bf16_t*>(a.logits)[at])
+                                 : static_cast<float>(static_cast<const f16_t*>(a.logits)[at]);
+    // (z - m) - ln s keeps more digits than z - lse where the maximum is large
+    lp = none ? -INFINITY : (z - st.m) - ln_s;
+  }
+  a.logprob[row] = lp;
+  a.lse[row] = lse;
+  if (a.entropy != nullptr) a.entropy[row] = none ? 0.0f : ln_s - st.t * kLn2 / st.s;
+  return lse;
+}
+
+// Workgroup (row, slice): the statistics and best candidates of `slice`
+// elements; with one slice to a row, the row's results.
+template <class T, bool TOP>
+__global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs a, uint32_t slices, uint32_t slice,
+                                                           Partial* partial, uint64_t* best_out) {
+  constexpr int E = 16 / sizeof(T);
+  typedef Vec<T, E> X;
+  __shared__ Stats wave_stats[kWaves];
+  __shared__ uint64_t wave_best[TOP ? kWaves * RSX_TOP_MAX : 1];
+  __shared__ float row_lse;
+  const uint64_t block = block_id();
+  const uint64_t row = block / slices;
+  if (row >= a.rows) return;
+  const uint32_t part = static_cast<uint32_t>(block - row * slices);
+  const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const uint32_t begin = part * slice;
+  const uint32_t end = min(begin + slice, static_cast<uint32_t>(a.vocab));
+  const T* z = static_cast<const T*>(a.logits) + row * a.stride;
+  const uint32_t top = a.top;
+
+  Stats st = {-INFINITY, 0.0f, 0.0f};
+  Best best = {0ull, 0ull, 0ull};
+  bool seeded = false;
+  constexpr uint32_t kSpan = 64 * E;             // elements of one vector across a wave
+  constexpr uint32_t kGroup = kSpan * kUnroll;   // of a wave's step
+  for (uint32_t base = begin + wave * kGroup; base < end; base += kWaves * kGroup) {
+    typename X::wide f[kUnroll];
+    const bool full = base + kGroup <= end;  // the same for the wave
+    if (full) {
+      typename X::type raw[kUnroll];
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) raw[j] = load_once<T, E>(z + base + j * kSpan + lane * E);
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) f[j] = widen<T, E>(raw[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) {
+        const uint32_t e = base + j * kSpan + lane * E;
+        f[j] = widen<T, E>(load_row<T, E>(z, e, end));
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          if (e + i >= end) f[j][i] = -INFINITY;
+      }
+    }
+    float most = f[0][0];
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j)
+#pragma unroll
+      for (int i = 0; i < E; ++i) most = fmaxf(most, f[j][i]);
+    if (most > st.m) st = rebase(st, most);
+    const float ref = reference(st.m);
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j)
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float u = (f[j][i] - ref) * kLog2e;
+        const float p = __builtin_amdgcn_exp2f(u);
+        st.s += p;
+        st.t = fmaf(p, fmaxf(u, kLeast), st.t);
+      }
+    if constexpr (TOP) {
+      const uint32_t mine = value_order(most);
+      if (!seeded) {
+        // The top-th largest of the lanes' maxima, 64 elements of their own,
+        // is a lower bound of the top-th largest: few candidates pass it.
+        // A maximum of -inf may stand for NaNs (which fmaxf passes over) or for
+        // the fill past the slice's end, and counts as the lowest order; lanes
+        // that are past the end altogether have no element.
+        const uint32_t sure = most > -INFINITY ? mine : 1u;
+        const uint32_t bound = lanes_nth(base + lane * E < end ? sure : 0u, top);
+        best.floor = bound == 0u ? 0ull : candidate(bound, 0xffffffffu) - 1;
+        best.least = best.floor;
+        seeded = true;
+      }
+      if (__ballot(candidate(mine, base) > best.least)) {
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j)
+#pragma unroll
+          for (int i = 0; i < E; ++i) {
+            const uint32_t e = base + j * kSpan + lane * E + i;
+            const uint64_t c = e < end ? candidate(value_order(f[j][i]), e) : 0ull;
+            uint64_t who = __ballot(c > best.least);
+            while (who) {
+              const int l = __builtin_ctzll(who);
+              insert(best, lane_value64(c, l), lane, top);
+              who = __ballot(c > best.least) & ~((2ull << l) - 1);
+            }
+          }
+      }
+    }
+  }
+
+  st = wave_merge(st);
+  if (lane == 0) wave_stats[wave] = st;
+  if constexpr (TOP) {
+    if (lane < top) wave_best[wave * top + lane] = best.mine;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    Stats all = wave_stats[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) all = merge(all, wave_stats[w]);
+    if (slices == 1)
+      row_lse = finish_row(a, row, all);
+    else
+      partial[block] = {all.m, all.s, all.t, 0.0f};
+  }
+  if constexpr (TOP) {
+    __syncthreads();
+    const float lse = row_lse;
+    // A candidate's rank is the number of larger ones; all are different but
+    // for 0, which is none.
+    for (uint32_t i = threadIdx.x; i < kWaves * top; i += kThreads) {
+      const uint64_t c = wave_best[i];
+      uint32_t rank = 0;
+      for (uint32_t j = 0; j < kWaves * top; ++j) rank += wave_best[j] > c ? 1u : 0u;
+      if (slices == 1) {
+        if (c != 0 && rank < top) {
+          const float v = order_value(static_cast<uint32_t>(c >> 32));
+          a.top_token[row * top + rank] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(c));
+          a.top_logprob[row * top + rank] = lse == -INFINITY ? -INFINITY : v - lse;
+        }
+      } else if (c != 0 && rank < top) {
+        best_out[block * top + rank] = c;
+      }
+    }
+    if (slices > 1) {
+      // Fewer candidates than `top` in this slice: the rest is none.
+      uint32_t found = 0;
+      for (uint32_t j = 0; j < kWaves * top; ++j) found += wave_best[j] != 0 ? 1u : 0u;
+      for (uint32_t i = threadIdx.x; i < top; i += kThreads)
+        if (i >= found) best_out[block * top + i] = 0ull;
+    }
+  }
+}
+
+// A row's slices joined in order.
+__global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs a, uint32_t slices, const Partial* partial,
+                                                                const uint64_t* best) {
+  extern __shared__ uint64_t cand[];
+  __shared__ Stats wave_stats[kWaves];
+  __shared__ float row_lse;
+  const uint64_t row = block_id();
+  if (row >= a.rows) return;
+  const uint32_t top = a.top, n = slices * top;
+  for (uint32_t i = threadIdx.x; i < n; i += kThreads) cand[i] = best[row * n + i];
+  Stats st = {-INFINITY, 0.0f, 0.0f};
+  for (uint32_t i = threadIdx.x; i < slices; i += kThreads) {
+    const Partial p = partial[row * slices + i];
+    st = merge(st, {p.m, p.s, p.t});
+  }
+  st = wave_merge(st);
+  if (threadIdx.x % 64 == 0) wave_stats[threadIdx.x / 64] = st;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    Stats all = wave_stats[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) all = merge(all, wave_stats[w]);
+    row_lse = finish_row(a, row, all);
+  }
+  if (top == 0) return;
+  __syncthreads();
+  const float lse = row_lse;
+  for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
+    const uint64_t c = cand[i];
+    if (c == 0) continue;
+    uint32_t rank = 0;
+    for (uint32_t j = 0; j < n; ++j) rank += cand[j] > c ? 1u : 0u;
+    if (rank < top) {
+      a.top_token[row * top + rank] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(c));
+      a.top_logprob[row * top + rank] =
+          lse == -INFINITY ? -INFINITY : order_value(static_cast<uint32_t>(c >> 32)) - lse;
+    }
+  }
+}
+
+// Slices of a row.  Enough workgroups for the chip, none below one step of its
+// four waves, and no more than the join takes in one go.
+constexpr uint32_t kStepElems = 8192;   // kWaves * 64 lanes * kUnroll vectors of 8
+constexpr uint32_t kWantGroups = 1024;
+constexpr uint32_t kMaxSlices = 64;
+constexpr uint32_t kMaxJoin = 1024;  // candidates, each compared with every other
+struct Slices {
+  uint32_t count, length;
+};
+Slices slices_of(uint64_t rows, uint64_t vocab, uint32_t top) {
+  uint64_t n = rows == 0 ? 1 : (kWantGroups + rows - 1) / rows;
+  const uint64_t most = (vocab + kStepElems - 1) / kStepElems;
+  n = n < most ? n : most;
+  const uint64_t room = top > kMaxJoin / kMaxSlices ? kMaxJoin / top : kMaxSlices;
+  n = n < room ? n : room;
+  n = n > 0 ? n : 1;
+  uint64_t length = (vocab + n - 1) / n;
+  length = (length + kStepElems - 1) / kStepElems * kStepElems;
+  return {static_cast<uint32_t>((vocab + length - 1) / length), static_cast<uint32_t>(length)};
+}
+
+template <class T>
+hipError_t logprobs(const LogprobArgs& a, hipStream_t s) {
+  const Slices sl = slices_of(a.rows, a.vocab, a.top);
+  const uint64_t grid = a.rows * sl.count;
+  Partial* partial = static_cast<Partial*>(a.ws);
+  uint64_t* best = reinterpret_cast<uint64_t*>(static_cast<char*>(a.ws) + (grid * sizeof(Partial) + 255) / 256 * 256);
+  const dim3 g = grid_of(grid);
+  const hipError_t e = launch(a.top != 0 ? logprob_kernel<T, true> : logprob_kernel<T, false>, g, kThreads, 0, s, a,
+                              sl.count, sl.length, partial, best);
+  if (e != hipSuccess || sl.count == 1) return e;
+  return launch(logprob_join_kernel, grid_of(a.rows), kThreads, sl.count * a.top * sizeof(uint64_t), s, a, sl.count,
+                partial, best);
+}
+
+// --------------------------------------------------------------- gradient
+// Workgroup (row, tile) of kThreads * kUnroll vectors.
+template <class T>
+__global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs a, uint32_t tiles) {
+  constexpr int E = 16 / sizeof(T);
+  typedef Vec<T, E> X;
+  constexpr uint32_t kSpan = kThreads * E;
+  const uint64_t block = block_id();
+  const uint64_t row = block / tiles;
+  if (row >= a.rows) return;
+  const uint32_t base = static_cast<uint32_t>(block - row * tiles) * (kSpan * kUnroll) + threadIdx.x * E;
+  const uint32_t vocab = static_cast<uint32_t>(a.vocab);
+  const T* z = static_cast<const T*>(a.logits) + row * a.stride;
+  T* dz = static_cast<T*>(a.dlogits) + row * a.dstride;
+  const float lse = a.lse[row];
+  const uint64_t tok = token_at(a.tokens, row, a.wide);
+  const uint32_t mine = tok < a.vocab ? static_cast<uint32_t>(tok) : 0xffffffffu;  // no element's index
+  const float g = tok < a.vocab ? a.dlogprob[row] : 0.0f;
+  const float h = a.dentropy != nullptr ? a.dentropy[row] : 0.0f;
+  const float c = a.dentropy != nullptr ? fmaf(h, a.entropy[row], g) : g;  // dz_j = -p_j (c + h log p_j)
+  const bool none = lse == -INFINITY;
+  typename X::type raw[kUnroll];
+#pragma unroll
+  for (int j = 0; j < kUnroll; ++j) raw[j] = load_row<T, E>(z, base + j * kSpan, vocab);
+#pragma unroll
+  for (int j = 0; j < kUnroll; ++j) {
+    const uint32_t e = base + j * kSpan;
+    typename X::wide f = widen<T, E>(raw[j]);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const float lp = f[i] - lse;
+      const float p = __builtin_amdgcn_exp2f(lp * kLog2e);
+      f[i] = none ? 0.0f : -p * fmaf(h, fmaxf(lp, kLeast), c);
+      if (mine == e + i) f[i] += none ? 0.0f : g;
+    }
+    store_row<T, E>(dz, e, vocab, narrow<T, E>(f));
+  }
+}
+
+template <class T>
+hipError_t logprobs_grad(const LogprobGradArgs& a, hipStream_t s) {
+  const uint64_t per = kThreads * kUnroll * (16 / sizeof(T));
+  const uint64_t tiles = (a.vocab + per - 1) / per;
+  return launch(logprob_grad_kernel<T>, grid_of(a.rows * tiles), kThreads, 0, s, a, static_cast<uint32_t>(tiles));
+}
+
+}  // namespace
+
+uint64_t token_logprobs_ws(uint64_t rows, uint64_t vocab, uint32_t top) {
+  const Slices sl = slices_of(rows, vocab, top);
+  if (sl.count <= 1) return 0;
+  return (rows * sl.count * sizeof(Partial) + 255) / 256 * 256 + rows * sl.count * top * sizeof(uint64_t);
+}
+
+hipError_t launch_token_logprobs(const LogprobArgs& a, hipStream_t s) {
+  if (a.type == RSX_FLOAT32) return logprobs<float>(a, s);
+  return a.type == RSX_BFLOAT16 ? logprobs<bf16_t>(a, s) : logprobs<f16_t>(a, s);
+}
+hipError_t launch_token_logprobs_grad(const LogprobGradArgs& a, hipStream_t s) {
+  if (a.type == RSX_FLOAT32) return logprobs_grad<float>(a, s);
+  return a.type == RSX_BFLOAT16 ? logprobs_grad<bf16_t>(a, s) : logprobs_grad<f16_t>(a, s);
+}
+
+}  // namespace rsx

@@ -61,10 +61,11 @@
 extern "C" {
 #endif
 
-#define RSX_VERSION 110          /* 1.1.0 */
+#define RSX_VERSION 120          /* 1.2.0 */
 #define RSX_MAX_RANKS 16         /* largest W a call accepts */
 #define RSX_NAIVE_MAX_BYTES 32768 /* RSX_ALGO_AUTO picks naive at or below this, per rank [MX] */
 #define RSX_FUSE_BATCH 248       /* tensors per pack/unpack launch */
+#define RSX_TOP_MAX 64           /* most alternatives of rsx_token_logprobs */
 #define RSX_SPARSE_SCRATCH_BYTES 134217728 /* 128 MiB: scratch array of rsx_sparse_all_reduce_noalloc, per GPU */
 
 typedef enum {
@@ -379,6 +380,132 @@ rsx_status_t rsx_sparse_all_reduce_noalloc(const float* const* grads, float* con
  */
 int rsx_fusion_plan(const size_t* counts, const rsx_dtype_t* dtypes, int ntensors,
                     size_t threshold_bytes, int* group_end);
+
+/*
+ * Training-step operators: what makes the gradients that the collectives
+ * above reduce.
+ *
+ * Rows.  A matrix argument is rows of `dim` elements that lie side by side,
+ * `stride` elements from one row's first to the next row's (stride >= dim; a
+ * matrix that is only read may have stride 0, one row standing for all).
+ * Any element-aligned address, stride and length is correct.
+ * Element types are RSX_FLOAT32, RSX_BFLOAT16 and RSX_FLOAT16; sums, norms
+ * and softmax statistics are held in fp32 and rounded once, to nearest even,
+ * at the store.  Token types are RSX_INT32 and RSX_INT64.  Other types:
+ * RSX_ERR_INVALID_TYPE.  Results are the same bits on every run.
+ * Overlap of an output with anything else is RSX_ERR_ALIASING, except for the
+ * in-place forms named; rows of two matrices of one stride in bytes may
+ * interleave.  Sizes: dim, vocab, rows and token counts below 2^31, buffers
+ * below 2^45 bytes, else RSX_ERR_UNSUPPORTED.  A workspace is device memory,
+ * 256-byte aligned, of at least the bytes that its _workspace_size gives
+ * (null is right for 0); its contents are scratch, and two calls that may run
+ * at the same time need two.
+ * Launched, like everything here, on `stream`, with nothing allocated and no
+ * synchronisation; they may be captured into a graph.
+ */
+
+/*
+ * Embedding lookup with scaling: with t = tokens[i] - first,
+ * out[i] = scale * table[t] for 0 <= t < vocab, else a row of zeros.
+ * `first` is the token id of the table's first row: a table cut by rows over
+ * the ranks is looked up part by part, and the sum all-reduce of the outputs
+ * is the whole table's lookup.
+ */
+rsx_status_t rsx_embedding(const void* table, size_t table_stride, size_t vocab, size_t dim,
+                           rsx_dtype_t table_type, const void* tokens, size_t ntokens,
+                           rsx_dtype_t token_type, int64_t first, float scale, void* out,
+                           size_t out_stride, rsx_dtype_t out_type, hipStream_t stream);
+
+/*
+ * Gradient of rsx_embedding in its table:
+ * grad[v] = (accumulate ? grad[v] : 0) + scale * sum of dout[i] over the i
+ * with tokens[i] - first = v.  The tokens are sorted, so that a row's sum is
+ * taken in the order of its positions, in chunks.  Without `accumulate` every
+ * row is written, with it only the rows that occur.
+ */
+size_t rsx_embedding_grad_workspace_size(size_t ntokens, size_t dim);
+rsx_status_t rsx_embedding_grad(const void* dout, size_t dout_stride, rsx_dtype_t dout_type,
+                                const void* tokens, size_t ntokens, rsx_dtype_t token_type,
+                                int64_t first, float scale, void* grad, size_t grad_stride,
+                                size_t vocab, size_t dim, rsx_dtype_t grad_type, int accumulate,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Layer norm: y = (x - mean) * rstd * weight + bias, with each row's
+ * mean = sum x / dim and rstd = (sum (x - mean)^2 / dim + eps)^(-1/2).
+ * weight, bias: `dim` elements of weight_type (x's type or RSX_FLOAT32), or
+ * null (1 and 0).  mean, rstd: `rows` fp32, or null.
+ * codes, scales: null, or an 8-bit checkpoint of x written on the way, as
+ * rsx_checkpoint_pack does.  y == x with one stride is allowed.
+ */
+rsx_status_t rsx_layer_norm(const void* x, size_t x_stride, const void* weight, const void* bias,
+                            void* y, size_t y_stride, float* mean, float* rstd, int8_t* codes,
+                            uint8_t* scales, size_t rows, size_t dim, float eps, rsx_dtype_t type,
+                            rsx_dtype_t weight_type, hipStream_t stream);
+
+/*
+ * Gradients of rsx_layer_norm: with xhat = (x - mean) * rstd and g = dy * weight,
+ * dx = rstd * (g - mean(g) - xhat * mean(g * xhat)), dweight = sum over rows of
+ * dy * xhat, dbias = sum over rows of dy (either may be null).
+ * The input is x, or with x null the checkpoint (codes, scales) of it; mean and
+ * rstd are the forward pass's.  dx == dy or dx == x with one stride is allowed.
+ * rows = 0 sets dweight and dbias to 0.
+ */
+size_t rsx_layer_norm_grad_workspace_size(size_t rows, size_t dim);
+rsx_status_t rsx_layer_norm_grad(const void* dy, size_t dy_stride, const void* x, size_t x_stride,
+                                 const int8_t* codes, const uint8_t* scales, const float* mean,
+                                 const float* rstd, const void* weight, void* dx, size_t dx_stride,
+                                 void* dweight, void* dbias, size_t rows, size_t dim,
+                                 rsx_dtype_t type, rsx_dtype_t weight_type, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Activation checkpoints in 8 bits.  Each row is cut into blocks of
+ * RSX_CHECKPOINT_BLOCK elements (the last may be shorter).  With 2^E <= m <
+ * 2^(E+1) the block's largest magnitude, x is kept as the int8 code
+ * q = rint(x / 2^(E-6)), clamped to [-127, 127], and comes back as
+ * q * 2^(E-6), rounded to the output's type.  scales holds E - 6 + 127 (0 for
+ * blocks below 2^-120); a block with an infinity or a NaN has 255 and comes
+ * back as NaN throughout.
+ * codes: [rows][dim]; scales: [rows][ceil(dim / RSX_CHECKPOINT_BLOCK)].
+ */
+#define RSX_CHECKPOINT_BLOCK 32
+rsx_status_t rsx_checkpoint_pack(const void* x, size_t x_stride, int8_t* codes, uint8_t* scales,
+                                 size_t rows, size_t dim, rsx_dtype_t type, hipStream_t stream);
+rsx_status_t rsx_checkpoint_unpack(const int8_t* codes, const uint8_t* scales, void* out,
+                                   size_t out_stride, size_t rows, size_t dim, rsx_dtype_t type,
+                                   hipStream_t stream);
+
+/*
+ * Log probabilities of given tokens.  For each row of logits:
+ * lse = log sum exp z; logprob = z[token] - lse (0 for a token outside
+ * [0, vocab)); entropy = -sum p log p (may be null); and the `top` largest
+ * logits, in order, of equal ones the lower index first (a NaN ranks below
+ * every number): top_token[row][k] and top_logprob[row][k] = z - lse.
+ * top: 0..min(vocab, RSX_TOP_MAX); with 0 the two arrays may be null.
+ * A logit of -inf is masked.  A row with nothing else has lse = -inf, log
+ * probabilities of -inf and entropy 0; a row with a NaN or +inf has NaN.
+ */
+size_t rsx_token_logprobs_workspace_size(size_t rows, size_t vocab, int top);
+rsx_status_t rsx_token_logprobs(const void* logits, size_t stride, rsx_dtype_t type,
+                                const void* tokens, rsx_dtype_t token_type, size_t rows,
+                                size_t vocab, int top, float* logprob, float* entropy, float* lse,
+                                float* top_logprob, int32_t* top_token, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradient of the log probability and of the entropy in the logits:
+ * dlogits[j] = dlogprob * (delta(j, token) - p_j) - dentropy * p_j * (log p_j + entropy),
+ * rounded to the logits' type.  lse and entropy are the forward pass's;
+ * dentropy may be null (then entropy may be too).  A token outside [0, vocab)
+ * has no gradient through its log probability; a row of masked logits alone
+ * has a gradient of 0.  dlogits == logits with one stride is allowed.
+ */
+rsx_status_t rsx_token_logprobs_grad(const void* logits, size_t stride, rsx_dtype_t type,
+                                     const void* tokens, rsx_dtype_t token_type, const float* lse,
+                                     const float* entropy, const float* dlogprob,
+                                     const float* dentropy, void* dlogits, size_t dlogits_stride,
+                                     size_t rows, size_t vocab, hipStream_t stream);
 
 /*
  * First element of segment k in RSX_ALGO_RING all-reduce of `count`
