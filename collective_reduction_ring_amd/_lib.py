@@ -59,7 +59,7 @@ SIGNATURES = {
     "rsx_sparse_all_reduce_noalloc": (_I, [_PP, _PP, _PP, _I, _SZ, _I, ctypes.c_float, _SZ, _PP, _PP,
                                            _SZ, _P, _P]),
     "rsx_embedding": (_I, [_P, _SZ, _SZ, _SZ, _I, _P, _SZ, _I, ctypes.c_int64, ctypes.c_float, _P, _SZ, _I, _P]),
-    "rsx_embedding_grad_workspace_size": (_SZ, [_SZ, _SZ]),
+    "rsx_embedding_grad_workspace_size": (_SZ, [_SZ, _SZ, _SZ]),
     "rsx_embedding_grad": (_I, [_P, _SZ, _I, _P, _SZ, _I, ctypes.c_int64, ctypes.c_float, _P, _SZ, _SZ, _SZ, _I, _I,
                                 _P, _SZ, _P]),
     "rsx_layer_norm": (_I, [_P, _SZ, _P, _P, _P, _SZ, _P, _P, _P, _P, _SZ, _SZ, ctypes.c_float, _I, _I, _P]),

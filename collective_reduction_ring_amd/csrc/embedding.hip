@@ -4,6 +4,8 @@
 //   grad[v, :] = (grad[v, :] +) scale * sum of dout[i, :] over the i with t_i = v
 //
 // A token outside [0, vocab) gives a row of zeros and no gradient.
+#include <algorithm>
+
 #include "step_device.h"
 
 namespace rsx {
@@ -26,11 +28,26 @@ __device__ __forceinline__ uint64_t uniform64(uint64_t v) {
   return (static_cast<uint64_t>(hi) << 32) | lo;
 }
 
+// Elements of a vector of the gradient: 16 bytes of the wider type, so that
+// each of a wave's accesses covers one unbroken span on either side.
+template <class T, class U>
+constexpr int kVector = sizeof(T) == 4 || sizeof(U) == 4 ? 4 : 8;
+
+// Lanes that one row of `dim` fills, a power of two up to a wave.
+inline uint32_t lanes_of(uint64_t dim, uint32_t e) {
+  uint32_t lanes = 1;
+  while (lanes < 64 && static_cast<uint64_t>(lanes) * e < dim) lanes *= 2;
+  return lanes;
+}
+
 // ---------------------------------------------------------------- lookup
-// A wave copies V vectors per lane of one row: 64 * V * E elements.
+// A wave copies V vectors per lane of one row: 64 * V * E elements.  A vector
+// has 16 bytes of the output, which is streamed; the table's side goes through
+// the caches, where pieces join (fp32 to bf16, 16384 rows of 4096: 47.4 us; by
+// 16 bytes of the table 49.2).
 template <class T, class U, int V>
 __global__ __launch_bounds__(kThreads) void lookup_kernel(EmbedArgs a, uint32_t chunks) {
-  constexpr int E = sizeof(T) == 4 && sizeof(U) == 4 ? 4 : 8;
+  constexpr int E = 16 / sizeof(U);
   const uint32_t lane = threadIdx.x % 64;
   const uint64_t item = uniform64(block_id() * (kThreads / 64) + threadIdx.x / 64);
   const uint64_t i = item / chunks;
@@ -55,9 +72,25 @@ __global__ __launch_bounds__(kThreads) void lookup_kernel(EmbedArgs a, uint32_t 
   }
 }
 
+// Rows of at most half a wave: `lanes` lanes to a row, 64 / lanes rows to a wave.
+template <class T, class U>
+__global__ __launch_bounds__(kThreads) void lookup_narrow_kernel(EmbedArgs a, uint32_t lanes) {
+  constexpr int E = 16 / sizeof(U);
+  const uint64_t thread = block_id() * kThreads + threadIdx.x;
+  const uint64_t i = thread / lanes;
+  const uint32_t dim = static_cast<uint32_t>(a.dim);
+  const uint32_t e = static_cast<uint32_t>(thread % lanes) * E;
+  if (i >= a.n || e >= dim) return;
+  const uint64_t row = token_row(a.tokens, i, a.first, a.wide);
+  typename Vec<T, E>::wide f = 0.0f;
+  if (row < a.vocab)
+    f = widen<T, E>(load_row<T, E, false>(static_cast<const T*>(a.table) + row * a.table_stride, e, dim)) * a.scale;
+  store_row<U, E>(static_cast<U*>(a.out) + i * a.out_stride, e, dim, narrow<U, E>(f));
+}
+
 template <class T, class U, int V>
 hipError_t lookup_go(const EmbedArgs& a, hipStream_t s) {
-  constexpr int E = sizeof(T) == 4 && sizeof(U) == 4 ? 4 : 8;
+  constexpr int E = 16 / sizeof(U);
   const uint64_t chunks = (a.dim + 64 * V * E - 1) / (64 * V * E);
   const uint64_t grid = (a.n * chunks + kThreads / 64 - 1) / (kThreads / 64);
   return launch(lookup_kernel<T, U, V>, grid_of(grid), kThreads, 0, s, a, static_cast<uint32_t>(chunks));
@@ -65,6 +98,9 @@ hipError_t lookup_go(const EmbedArgs& a, hipStream_t s) {
 
 template <class T, class U>
 hipError_t lookup(const EmbedArgs& a, hipStream_t s) {
+  const uint32_t lanes = lanes_of(a.dim, 16 / sizeof(U));
+  if (lanes < 64)
+    return launch(lookup_narrow_kernel<T, U>, grid_of((a.n * lanes + kThreads - 1) / kThreads), kThreads, 0, s, a, lanes);
   return a.n * a.dim < (1u << 22) ? lookup_go<T, U, 1>(a, s) : lookup_go<T, U, 4>(a, s);
 }
 
@@ -136,13 +172,67 @@ __device__ void scan_counts(uint32_t (*counts)[kBins], uint32_t* totals, const u
   __syncthreads();
 }
 
+// Rows that no token names are zeroed beside the sort and the sums: those have
+// few workgroups or wait for scattered loads, the zeros are nothing but
+// stores, so each hides the other.  A workgroup takes a group of `rows` rows;
+// those that a token names are marked as bits of `named`.
+constexpr uint32_t kNamedWords = kSortWaves * kBins;  // marks that a workgroup holds in LDS
+constexpr uint32_t kScanGroup = 1u << 18;  // bytes of a group that scans
+constexpr uint32_t kZeroGroup = 1u << 15;  // bytes of one that does not
+struct ZeroPlan {
+  const uint32_t* named;  // marks of the whole table; null: not there
+  uint32_t rows, lanes;   // rows of a group; lanes that share a row
+  uint64_t first, end;    // groups of this launch
+};
+// Marks of rows v0 .. v0 + rows in LDS, from a scan of all tokens.
+__device__ void mark_rows(const EmbedGradArgs& a, uint64_t v0, uint32_t rows, uint32_t* named) {
+  const uint32_t n = static_cast<uint32_t>(a.n);
+  for (uint32_t i = threadIdx.x; i < (rows + 31) / 32; i += kSortThreads) named[i] = 0;
+  __syncthreads();
+  constexpr uint32_t kStep = 8 * kSortThreads;
+  for (uint32_t i0 = threadIdx.x; i0 < n; i0 += kStep) {
+    uint64_t r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = token_row(a.tokens, min(i0 + j * kSortThreads, n - 1), a.first, a.wide) - v0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (r[j] < rows) atomicOr(&named[r[j] / 32], 1u << (r[j] % 32));
+  }
+  __syncthreads();
+}
+template <class B>
+__device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, const ZeroPlan& z, uint64_t v0, uint32_t rows,
+                                          const uint32_t* named, uint64_t bit0) {
+  constexpr int E = 16 / sizeof(B);
+  const uint32_t dim = static_cast<uint32_t>(a.dim);
+  const typename Vec<B, E>::type zero = {};
+  for (uint32_t r = threadIdx.x / z.lanes; r < rows; r += blockDim.x / z.lanes) {
+    const uint64_t bit = bit0 + r;
+    if ((named[bit / 32] >> (bit % 32)) & 1u) continue;
+    B* g = static_cast<B*>(a.grad) + (v0 + r) * a.grad_stride;
+    for (uint32_t e = threadIdx.x % z.lanes * E; e < dim; e += z.lanes * E) store_row<B, E>(g, e, dim, zero);
+  }
+}
+// Group z.first + block, from the marks of the table or, without, of its own.
+template <class B>
+__device__ __forceinline__ void zero_group(const EmbedGradArgs& a, const ZeroPlan& z, uint64_t block, uint32_t* lds) {
+  const uint64_t group = z.first + block, v0 = group * z.rows;
+  if (group >= z.end) return;
+  const uint32_t rows = static_cast<uint32_t>(min(static_cast<uint64_t>(z.rows), a.vocab - v0));
+  if (z.named != nullptr) return zero_rows<B>(a, z, v0, rows, z.named, v0);
+  mark_rows(a, v0, rows, lds);
+  zero_rows<B>(a, z, v0, rows, lds, 0);
+}
+
 // The whole sort of at most kSmallSort tokens in one workgroup.
+template <class B>
 __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(EmbedGradArgs a, int bits, uint32_t* keys,
-                                                                  uint32_t* places) {
+                                                                  uint32_t* places, ZeroPlan z) {
   __shared__ uint32_t key[2][kSmallSort];
   __shared__ uint16_t place[2][kSmallSort];
   __shared__ uint32_t counts[kSortWaves][kBins];
   __shared__ uint32_t totals[kBins / 64];
+  if (block_id() != 0) return zero_group<B>(a, z, block_id() - 1, &counts[0][0]);
   const uint32_t n = static_cast<uint32_t>(a.n);
   const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const uint32_t part = ((n + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;  // entries of a wave
@@ -187,10 +277,22 @@ __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(EmbedGradArgs 
   }
 }
 
-// Digit counts of each tile: hist[tile][digit].
+// Digit counts of each tile: hist[tile][digit].  The first pass also marks the
+// named rows (`marks`, `marked` rows to a workgroup), later ones zero groups.
+template <class B>
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(EmbedGradArgs a, const uint32_t* keys_in, int shift,
-                                                                  uint32_t tile, uint32_t* hist) {
-  __shared__ uint32_t counts[kBins];
+                                                                  uint32_t tile, uint32_t tiles, uint32_t* hist,
+                                                                  uint32_t* marks, uint32_t marked, ZeroPlan z) {
+  __shared__ uint32_t counts[kNamedWords];
+  if (block_id() >= tiles) {
+    if (marks == nullptr) return zero_group<B>(a, z, block_id() - tiles, nullptr);
+    const uint64_t v0 = (block_id() - tiles) * marked;
+    if (v0 >= a.vocab) return;
+    const uint32_t rows = static_cast<uint32_t>(min(static_cast<uint64_t>(marked), a.vocab - v0));
+    mark_rows(a, v0, rows, counts);
+    for (uint32_t i = threadIdx.x; i < (rows + 31) / 32; i += kSortThreads) marks[v0 / 32 + i] = counts[i];
+    return;
+  }
   const uint32_t n = static_cast<uint32_t>(a.n);
   if (threadIdx.x < kBins) counts[threadIdx.x] = 0;
   __syncthreads();
@@ -211,20 +313,22 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(EmbedGradArgs 
 
 // One pass: every tile's entries to their places.  Each workgroup adds up the
 // tiles' counts by itself, so a pass is two launches.
+template <class B>
 __global__ __launch_bounds__(kSortThreads) void sort_move_kernel(EmbedGradArgs a, const uint32_t* keys_in,
                                                                  const uint32_t* places_in, int shift, uint32_t tile,
-                                                                 const uint32_t* hist, uint32_t* keys_out,
-                                                                 uint32_t* places_out) {
+                                                                 uint32_t tiles, const uint32_t* hist,
+                                                                 uint32_t* keys_out, uint32_t* places_out, ZeroPlan z) {
   __shared__ uint32_t counts[kSortWaves][kBins];
   __shared__ uint32_t base[kBins];
   __shared__ uint32_t totals[kBins / 64];
+  if (block_id() >= tiles) return zero_group<B>(a, z, block_id() - tiles, nullptr);
   const uint32_t n = static_cast<uint32_t>(a.n), t = threadIdx.x;
   const uint32_t lane = t % 64, wave = t / 64;
   for (uint32_t i = t; i < kSortWaves * kBins; i += kSortThreads) (&counts[0][0])[i] = 0;
   uint32_t before = 0, total = 0;
   if (t < kBins) {
 #pragma unroll 8
-    for (uint32_t b = 0; b < gridDim.x; ++b) {
+    for (uint32_t b = 0; b < tiles; ++b) {
       const uint32_t c = hist[b * kBins + t];
       before += b < blockIdx.x ? c : 0u;
       total += c;
@@ -281,9 +385,12 @@ __global__ __launch_bounds__(kSortThreads) void sort_move_kernel(EmbedGradArgs a
 // goes to head[chunk], the first part of one that goes on to tail[chunk];
 // join_kernel adds a run's tail and the heads after it, in order.  So a
 // frequent token is spread over many waves and the order of its sum is fixed.
-// Rows that no token names are zeroed by the workgroups after those
-// (kZeroRows rows each), unless the gradient accumulates.
 constexpr uint32_t kZeroRows = 64;
+
+// LDS that a workgroup of the sums reserves and does not use: four to a CU
+// leave the memory's pages in better order than eight (330 and 336 us, for the
+// sizes above).
+constexpr uint32_t kSumReserve = 32768;
 
 // Keys are below 2^32 - 1 (vocab < 2^31), so this equals none of them.
 constexpr uint32_t kNoKey = 0xffffffffu;
@@ -305,106 +412,137 @@ __device__ __forceinline__ uint32_t first_at_least(const uint32_t* keys, uint32_
   return lo;
 }
 
+// The same for more tokens than a scan for the marks is worth: which of the
+// rows v0 .. v0 + 63 are named is read off the sorted entries from the first
+// at or past v0, a workgroup's width at a time; where one row fills that
+// width, on to the next.
+template <class U>
+__device__ void zero_sorted_rows(const EmbedGradArgs& a, const uint32_t* keys, uint64_t first_row) {
+  constexpr int E = 16 / sizeof(U);
+  __shared__ uint32_t named[kZeroRows];
+  if (first_row >= a.vocab) return;
+  const uint32_t n = static_cast<uint32_t>(a.n), dim = static_cast<uint32_t>(a.dim);
+  const uint32_t v0 = static_cast<uint32_t>(first_row);
+  uint32_t at = first_at_least(keys, 0, n, v0);
+  if (threadIdx.x < kZeroRows) named[threadIdx.x] = 0;
+  __syncthreads();
+  while (at < n) {  // the same for the whole workgroup
+    const uint32_t i = at + threadIdx.x;
+    const uint32_t k = i < n ? keys[i] : kNoKey;
+    if (k - v0 < kZeroRows) named[k - v0] = 1;
+    const uint32_t last = at + kThreads - 1;
+    if (last >= n) break;
+    const uint32_t kl = keys[last];
+    if (kl - v0 >= kZeroRows) break;
+    at = kl == keys[at] ? first_at_least(keys, last, n, kl + 1) : last + 1;
+  }
+  __syncthreads();
+  const typename Vec<U, E>::type zero = {};
+  for (uint32_t r = threadIdx.x / 64; r < kZeroRows && v0 + r < a.vocab; r += kThreads / 64) {
+    if (named[r]) continue;
+    U* g = static_cast<U*>(a.grad) + (v0 + r) * a.grad_stride;
+    for (uint32_t e = threadIdx.x % 64 * E; e < dim; e += 64 * E) store_row<U, E>(g, e, dim, zero);
+  }
+}
+
 template <class U, int E>
 __device__ __forceinline__ void put_sum(const EmbedGradArgs& a, uint32_t row, uint32_t e, uint32_t dim,
-                                        typename Vec<U, E>::wide sum) {
+                                        typename Vec<float, E>::type sum) {
   U* g = static_cast<U*>(a.grad) + row * a.grad_stride;
   sum *= a.scale;
   if (a.accumulate) sum += widen<U, E>(load_row<U, E>(g, e, dim));
   store_row<U, E>(g, e, dim, narrow<U, E>(sum));
 }
 
-template <class T, class U, int E>
+// A wave's 64 * E columns of a partial row, four floats of each lane at a
+// time, so that its accesses are unbroken; pitch is a multiple of 512.
+template <int E>
+__device__ __forceinline__ void put_part(float* row, uint32_t column, typename Vec<float, E>::type v) {
+  float* p = row + column * (64 * E) + threadIdx.x % 64 * 4;
+#pragma unroll
+  for (int h = 0; h < E / 4; ++h) {
+    typename Vec<float, 4>::type q;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = v[h * 4 + i];
+    *reinterpret_cast<typename Vec<float, 4>::type*>(p + h * 256) = q;
+  }
+}
+template <int E>
+__device__ __forceinline__ typename Vec<float, E>::type get_part(const float* row, uint32_t column) {
+  const float* p = row + column * (64 * E) + threadIdx.x % 64 * 4;
+  typename Vec<float, E>::type v;
+#pragma unroll
+  for (int h = 0; h < E / 4; ++h) {
+    const typename Vec<float, 4>::type q = *reinterpret_cast<const typename Vec<float, 4>::type*>(p + h * 256);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[h * 4 + i] = q[i];
+  }
+  return v;
+}
+
+template <class T, class U>
 __global__ __launch_bounds__(kThreads) void sum_kernel(EmbedGradArgs a, const uint32_t* keys, const uint32_t* places,
                                                        float* head, float* tail, uint32_t chunk, uint32_t chunks,
-                                                       uint32_t columns, uint64_t sum_groups, uint64_t pitch) {
-  __shared__ uint32_t named[kZeroRows];
-  const uint32_t n = static_cast<uint32_t>(a.n), dim = static_cast<uint32_t>(a.dim);
-  const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  typedef typename Vec<T, E>::wide Wide;
+                                                       uint32_t columns, uint64_t sum_groups, uint64_t pitch,
+                                                       ZeroPlan z) {
+  constexpr int E = kVector<T, U>;
   const uint64_t block = block_id();
   if (block >= sum_groups) {
-    // Which of the rows v0 .. v0 + 63 are named: the entries from the first
-    // at or past v0, a workgroup's width at a time; where one row fills that
-    // width, on to the next row.
-    const uint64_t first_row = (block - sum_groups) * kZeroRows;
-    if (first_row >= a.vocab) return;
-    const uint32_t v0 = static_cast<uint32_t>(first_row);
-    uint32_t at = first_at_least(keys, 0, n, v0);
-    if (threadIdx.x < kZeroRows) named[threadIdx.x] = 0;
-    __syncthreads();
-    while (at < n) {  // the same for the whole workgroup
-      const uint32_t i = at + threadIdx.x;
-      const uint32_t k = i < n ? keys[i] : kNoKey;
-      if (k - v0 < kZeroRows) named[k - v0] = 1;
-      const uint32_t last = at + kThreads - 1;
-      if (last >= n) break;
-      const uint32_t kl = keys[last];
-      if (kl - v0 >= kZeroRows) break;
-      at = kl == keys[at] ? first_at_least(keys, last, n, kl + 1) : last + 1;
-    }
-    __syncthreads();
-    const typename Vec<U, E>::type zero = {};
-    for (uint32_t r = wave; r < kZeroRows && v0 + r < a.vocab; r += kThreads / 64) {
-      if (named[r]) continue;
-      U* g = static_cast<U*>(a.grad) + (v0 + r) * a.grad_stride;
-      for (uint32_t e = lane * E; e < dim; e += 64 * E) store_row<U, E>(g, e, dim, zero);
-    }
-    return;
+    if (z.named != nullptr) return zero_group<U>(a, z, block - sum_groups, nullptr);
+    return zero_sorted_rows<U>(a, keys, (block - sum_groups) * kZeroRows);
   }
-
-  const uint64_t item = uniform64(block * (kThreads / 64) + wave);
+  const uint32_t n = static_cast<uint32_t>(a.n), dim = static_cast<uint32_t>(a.dim);
+  const uint32_t lane = threadIdx.x % 64;
+  const uint64_t item = uniform64(block * (kThreads / 64) + threadIdx.x / 64);
   const uint32_t c = static_cast<uint32_t>(item / columns);
-  const uint32_t e = static_cast<uint32_t>(item - static_cast<uint64_t>(c) * columns) * (64 * E) + lane * E;
+  const uint32_t column = static_cast<uint32_t>(item - static_cast<uint64_t>(c) * columns);
+  const uint32_t e = column * (64 * E) + lane * E;
   if (c >= chunks) return;  // whole waves; no barrier follows
-  const uint32_t begin = c * chunk;
-  const uint32_t count = min(n - begin, chunk);
+  const uint32_t begin = c * chunk, end = min(n - begin, chunk) + begin;
   const uint32_t vocab = static_cast<uint32_t>(a.vocab);
-  // Lane i holds entry begin + i, lane 63 the entry before the chunk, lane
-  // `count` the one after it (chunk <= 32).
-  uint32_t k = kNoKey, p = 0;
-  if (lane <= count && begin + lane < n) {
-    k = keys[begin + lane];
-    p = places[begin + lane];
-  }
-  if (lane == 63 && begin != 0) k = keys[begin - 1];
-  const uint32_t key_before = __builtin_amdgcn_readlane(k, 63);
-  const uint32_t key_after = __builtin_amdgcn_readlane(k, count);
+  const uint32_t key_before = begin != 0 ? keys[begin - 1] : kNoKey;
+  const uint32_t key_after = end < n ? keys[end] : kNoKey;
   const T* dout = static_cast<const T*>(a.dout);
 
-  Wide sum = 0.0f;
-  uint32_t run = __builtin_amdgcn_readlane(k, 0);
+  typename Vec<float, E>::type sum = {};
+  uint32_t run = keys[begin];
   bool from_before = run == key_before;
-  constexpr int kAhead = 8;
-  for (uint32_t i0 = 0; i0 < count; i0 += kAhead) {
-    typename Vec<T, E>::type v[kAhead];
+  constexpr int kAhead = 8;  // rows in flight
+  for (uint32_t at = begin; at < end; at += 64) {
+    // Lane i holds entry at + i.
+    const uint32_t count = min(end - at, 64u);
+    const uint32_t mine = at + min(lane, count - 1);
+    const uint32_t k = keys[mine], p = places[mine];
+    for (uint32_t i0 = 0; i0 < count; i0 += kAhead) {
+      typename Vec<T, E>::type v[kAhead];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const uint32_t i = min(i0 + j, count - 1);
-      const uint64_t place = static_cast<uint32_t>(__builtin_amdgcn_readlane(p, i));
-      v[j] = load_row<T, E>(dout + place * a.dout_stride, e, dim);
-    }
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      if (i0 + j >= count) break;
-      const uint32_t key = __builtin_amdgcn_readlane(k, i0 + j);
-      if (key != run) {
-        if (from_before)
-          store_row<float, E>(head + c * pitch, e, dim, sum);
-        else
-          put_sum<U, E>(a, run, e, dim, sum);
-        run = key;
-        from_before = false;
-        sum = 0.0f;
+      for (int j = 0; j < kAhead; ++j) {
+        const uint32_t i = min(i0 + j, count - 1);
+        const uint64_t place = static_cast<uint32_t>(__builtin_amdgcn_readlane(p, i));
+        v[j] = load_row<T, E>(dout + place * a.dout_stride, e, dim);
       }
-      if (run == vocab) return;  // tokens outside the table are last: nothing to sum
-      sum += widen<T, E>(v[j]);
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (i0 + j >= count) break;
+        const uint32_t key = __builtin_amdgcn_readlane(k, i0 + j);
+        if (key != run) {
+          if (from_before)
+            put_part<E>(head + c * pitch, column, sum);
+          else
+            put_sum<U, E>(a, run, e, dim, sum);
+          run = key;
+          from_before = false;
+          sum = 0.0f;
+        }
+        if (run == vocab) return;  // tokens outside the table are last: nothing to sum
+        sum += widen<T, E>(v[j]);
+      }
     }
   }
   if (from_before)
-    store_row<float, E>(head + c * pitch, e, dim, sum);
+    put_part<E>(head + c * pitch, column, sum);
   else if (run == key_after)
-    store_row<float, E>(tail + c * pitch, e, dim, sum);
+    put_part<E>(tail + c * pitch, column, sum);
   else
     put_sum<U, E>(a, run, e, dim, sum);
 }
@@ -435,14 +573,15 @@ __global__ __launch_bounds__(kThreads) void join_kernel(EmbedGradArgs a, const u
     heads += more;
     if (more < 64) break;
   }
-  const uint32_t e = static_cast<uint32_t>(block - static_cast<uint64_t>(c) * columns) * (64 * E) + lane * E;
+  const uint32_t column = static_cast<uint32_t>(block - static_cast<uint64_t>(c) * columns);
+  const uint32_t e = column * (64 * E) + lane * E;
   const uint32_t quarter = (heads + 3) / 4;
   const uint32_t begin = min(wave * quarter, heads), end = min(begin + quarter, heads);
   typename Vec<float, E>::type sum = {};
-  if (wave == 0) sum = load_row<float, E>(tail + c * pitch, e, dim);
-  const float* h = head + (c + 1) * pitch;
+  if (wave == 0) sum = get_part<E>(tail + c * pitch, column);
+  const float* h = head + (static_cast<uint64_t>(c) + 1) * pitch;
 #pragma unroll 8
-  for (uint32_t i = begin; i < end; ++i) sum += load_row<float, E>(h + i * pitch, e, dim);
+  for (uint32_t i = begin; i < end; ++i) sum += get_part<E>(h + i * pitch, column);
 #pragma unroll
   for (int i = 0; i < E; ++i) part[wave][lane * E + i] = sum[i];
   __syncthreads();
@@ -459,19 +598,26 @@ struct GradPlan {
   uint32_t tile, tiles;    // sort
   uint32_t chunk, chunks;  // sums
   uint64_t pitch;          // floats between partial rows
-  uint64_t keys, places, keys2, places2, hist, head, tail, total;  // byte offsets
+  uint64_t keys, places, keys2, places2, hist, marks, head, tail, total;  // byte offsets
 };
-GradPlan grad_plan(uint64_t dim, uint64_t n) {
+// Tokens up to which a scan marks the named rows.
+constexpr uint64_t kScanTokens = 1u << 17;
+
+GradPlan grad_plan(uint64_t vocab, uint64_t dim, uint64_t n) {
   GradPlan p;
   // About 64 tiles, of whole 64-entry steps for each of the 16 waves.
   const uint64_t unit = kSortThreads;
   p.tile = static_cast<uint32_t>(((n + 63) / 64 + unit - 1) / unit * unit);
   if (p.tile == 0) p.tile = unit;
   p.tiles = static_cast<uint32_t>((n + p.tile - 1) / p.tile);
-  // Chunks short enough that a small batch still fills the chip.
-  p.chunk = n >= 32768 ? 32u : n >= 8192 ? 16u : 8u;
+  // Long chunks have few partial rows, short ones fill the chip: about 4096
+  // waves of 512 columns.  A batch of at most 32 is one chunk and needs no join.
+  const uint64_t columns = (dim + 511) / 512;
+  p.chunk = 8;
+  while (p.chunk < 128 && n * columns > static_cast<uint64_t>(p.chunk) * 4096) p.chunk *= 2;
+  if (n <= 32) p.chunk = 32;
   p.chunks = static_cast<uint32_t>((n + p.chunk - 1) / p.chunk);
-  p.pitch = (dim + 15) / 16 * 16;
+  p.pitch = columns * 512;
   uint64_t at = 0;
   auto take = [&](uint64_t bytes) {
     const uint64_t here = at;
@@ -483,52 +629,98 @@ GradPlan grad_plan(uint64_t dim, uint64_t n) {
   p.keys2 = take(n * 4);
   p.places2 = take(n * 4);
   p.hist = take(static_cast<uint64_t>(p.tiles) * kBins * 4);
+  p.marks = take(n > kSmallSort && n <= kScanTokens ? (vocab + 31) / 32 * 4 : 0);
   p.head = take(p.chunks * p.pitch * 4);
   p.tail = take(p.chunks * p.pitch * 4);
   p.total = at;
   return p;
 }
 
-template <class T, class U>
-hipError_t grad(const EmbedGradArgs& a, hipStream_t s) {
-  constexpr int E = sizeof(T) == 4 ? 4 : 8;
-  const GradPlan p = grad_plan(a.dim, a.n);
+// The sort, with zeros of the unnamed rows beside it where z->rows is not 0;
+// z->end is where the sums' launch goes on.
+template <class B>
+hipError_t sort(const EmbedGradArgs& a, const GradPlan& p, ZeroPlan* z, hipStream_t s) {
   char* ws = static_cast<char*>(a.ws);
   uint32_t* keys = reinterpret_cast<uint32_t*>(ws + p.keys);
   uint32_t* places = reinterpret_cast<uint32_t*>(ws + p.places);
   uint32_t* keys2 = reinterpret_cast<uint32_t*>(ws + p.keys2);
   uint32_t* places2 = reinterpret_cast<uint32_t*>(ws + p.places2);
   uint32_t* hist = reinterpret_cast<uint32_t*>(ws + p.hist);
-  float* head = reinterpret_cast<float*>(ws + p.head);
-  float* tail = reinterpret_cast<float*>(ws + p.tail);
+  uint32_t* marks = reinterpret_cast<uint32_t*>(ws + p.marks);
   int bits = 1;
   while (bits < 32 && (a.vocab >> bits) != 0) ++bits;  // rows run up to `vocab` itself
-  hipError_t e = hipSuccess;
-  if (a.n == 0) {
-    // nothing to sort or sum
-  } else if (a.n <= kSmallSort) {
-    e = launch(sort_small_kernel, dim3(1), kSortThreads, 0, s, a, bits, keys, places);
+  const uint64_t groups = z->rows != 0 ? (a.vocab + z->rows - 1) / z->rows : 0;
+  if (a.n <= kSmallSort) {
+    z->end = groups;
+    return launch(sort_small_kernel<B>, grid_of(1 + groups), kSortThreads, 0, s, a, bits, keys, places, *z);
+  }
+  // Marks by one workgroup on each of the CUs that the sort leaves, and 256 KiB
+  // of zeros for each, which are about done with the sort's step.
+  constexpr uint64_t kBeside = 192;
+  uint64_t marked = ((a.vocab + kBeside - 1) / kBeside + 31) / 32 * 32;
+  marked = std::min<uint64_t>(marked, kNamedWords * 32);
+  const uint64_t marking = groups != 0 ? (a.vocab + marked - 1) / marked : 0;
+  const uint64_t beside_groups = kBeside * (kScanGroup / kZeroGroup);
+  const int passes = (bits + kDigit - 1) / kDigit;
+  const uint32_t *kin = nullptr, *pin = nullptr;
+  uint32_t *kout = passes % 2 ? keys : keys2, *pout = passes % 2 ? places : places2;
+  for (int pass = 0; pass < passes; ++pass) {
+    const int shift = pass * kDigit;
+    if (pass != 0) z->end = std::min(groups, z->first + beside_groups);
+    const uint64_t beside = pass == 0 ? marking : z->end - z->first;
+    hipError_t e = launch(sort_count_kernel<B>, grid_of(p.tiles + beside), kSortThreads, 0, s, a, kin, shift, p.tile,
+                          p.tiles, hist, pass == 0 && groups != 0 ? marks : nullptr, static_cast<uint32_t>(marked), *z);
     if (e != hipSuccess) return e;
-  } else {
-    const uint32_t *kin = nullptr, *pin = nullptr;
-    uint32_t *kout = ((bits + kDigit - 1) / kDigit) % 2 ? keys : keys2, *pout = kout == keys ? places : places2;
-    for (int shift = 0; shift < bits; shift += kDigit) {
-      e = launch(sort_count_kernel, dim3(p.tiles), kSortThreads, 0, s, a, kin, shift, p.tile, hist);
-      if (e != hipSuccess) return e;
-      e = launch(sort_move_kernel, dim3(p.tiles), kSortThreads, 0, s, a, kin, pin, shift, p.tile, hist, kout, pout);
-      if (e != hipSuccess) return e;
-      kin = kout;
-      pin = pout;
-      kout = kout == keys ? keys2 : keys;
-      pout = pout == places ? places2 : places;
+    if (groups != 0) z->named = marks;
+    z->first = z->end;
+    z->end = std::min(groups, z->first + beside_groups);
+    e = launch(sort_move_kernel<B>, grid_of(p.tiles + z->end - z->first), kSortThreads, 0, s, a, kin, pin, shift, p.tile,
+               p.tiles, hist, kout, pout, *z);
+    if (e != hipSuccess) return e;
+    z->first = z->end;
+    kin = kout;
+    pin = pout;
+    kout = kout == keys ? keys2 : keys;
+    pout = pout == places ? places2 : places;
+  }
+  return hipSuccess;
+}
+
+template <class T, class U>
+hipError_t grad(const EmbedGradArgs& a, hipStream_t s) {
+  constexpr int E = kVector<T, U>;
+  const GradPlan p = grad_plan(a.vocab, a.dim, a.n);
+  char* ws = static_cast<char*>(a.ws);
+  const uint32_t* keys = reinterpret_cast<const uint32_t*>(ws + p.keys);
+  const uint32_t* places = reinterpret_cast<const uint32_t*>(ws + p.places);
+  float* head = reinterpret_cast<float*>(ws + p.head);
+  float* tail = reinterpret_cast<float*>(ws + p.tail);
+  ZeroPlan z = {nullptr, 0, lanes_of(a.dim, 16 / sizeof(U)), 0, 0};
+  uint64_t zeros = 0;  // workgroups beside the sums
+  if (!a.accumulate && a.n != 0 && a.n <= kScanTokens) {
+    // Where a group scans the tokens by itself, four times what the scan reads
+    // at most.  Else short: groups of 32 KiB sweep the table in order, groups of
+    // 256 KiB are 2048 places that are written at once (336 and 353 us for the
+    // gradient of 65536 rows of 4096 bf16 in a table of 131072).
+    const uint64_t rows = (a.n <= kSmallSort ? kScanGroup : kZeroGroup) / (a.dim * sizeof(U));
+    z.rows = static_cast<uint32_t>(std::max<uint64_t>(1, std::min<uint64_t>(rows, kNamedWords * 32)));
+  } else if (!a.accumulate) {
+    zeros = (a.vocab + kZeroRows - 1) / kZeroRows;
+  }
+  if (a.n != 0) {
+    const hipError_t e = sizeof(U) == 4 ? sort<uint32_t>(a, p, &z, s) : sort<uint16_t>(a, p, &z, s);
+    if (e != hipSuccess) return e;
+    if (z.rows != 0) {
+      z.first = z.end;
+      z.end = (a.vocab + z.rows - 1) / z.rows;
+      zeros = z.end - z.first;
     }
   }
   const uint32_t columns = static_cast<uint32_t>((a.dim + 64 * E - 1) / (64 * E));
   const uint64_t sums = (static_cast<uint64_t>(p.chunks) * columns + kThreads / 64 - 1) / (kThreads / 64);
-  const uint64_t zeros = a.accumulate ? 0 : (a.vocab + kZeroRows - 1) / kZeroRows;
   if (sums + zeros == 0) return hipSuccess;
-  e = launch(sum_kernel<T, U, E>, grid_of(sums + zeros), kThreads, 0, s, a, keys, places, head, tail, p.chunk, p.chunks,
-             columns, sums, p.pitch);
+  const hipError_t e = launch(sum_kernel<T, U>, grid_of(sums + zeros), kThreads, kSumReserve, s, a, keys, places, head, tail, p.chunk,
+                              p.chunks, columns, sums, p.pitch, z);
   if (e != hipSuccess || p.chunks < 2) return e;
   return launch(join_kernel<U, E>, grid_of(static_cast<uint64_t>(p.chunks - 1) * columns), kThreads, 0, s, a, keys, head,
                 tail, p.chunk, columns, p.pitch);
@@ -559,7 +751,7 @@ hipError_t launch_embedding(const EmbedArgs& a, hipStream_t s) {
   }
 }
 
-uint64_t embedding_grad_ws(uint64_t dim, uint64_t n) { return grad_plan(dim, n).total; }
+uint64_t embedding_grad_ws(uint64_t vocab, uint64_t dim, uint64_t n) { return grad_plan(vocab, dim, n).total; }
 
 hipError_t launch_embedding_grad(const EmbedGradArgs& a, hipStream_t s) {
   switch (a.dout_type * 16 + a.grad_type) {

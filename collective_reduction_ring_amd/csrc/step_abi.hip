@@ -111,9 +111,9 @@ rsx_status_t rsx_embedding(const void* table, size_t table_stride, size_t vocab,
                                      stream));
 }
 
-size_t rsx_embedding_grad_workspace_size(size_t ntokens, size_t dim) {
-  if (ntokens > kMaxSize || dim > kMaxSize || ntokens == 0 || dim == 0) return 0;
-  return embedding_grad_ws(dim, ntokens);
+size_t rsx_embedding_grad_workspace_size(size_t ntokens, size_t vocab, size_t dim) {
+  if (ntokens > kMaxSize || vocab > kMaxSize || dim > kMaxSize || ntokens == 0 || dim == 0) return 0;
+  return embedding_grad_ws(vocab, dim, ntokens);
 }
 
 rsx_status_t rsx_embedding_grad(const void* dout, size_t dout_stride, rsx_dtype_t dout_type,
@@ -128,7 +128,7 @@ rsx_status_t rsx_embedding_grad(const void* dout, size_t dout_stride, rsx_dtype_
   m.write(grad, vocab, dim, grad_stride, gs);
   m.read(dout, ntokens, dim, dout_stride, ds);
   m.read_flat(tokens, ntokens, is);
-  m.workspace(workspace, workspace_bytes, rsx_embedding_grad_workspace_size(ntokens, dim));
+  m.workspace(workspace, workspace_bytes, rsx_embedding_grad_workspace_size(ntokens, vocab, dim));
   const rsx_status_t st = m.status();
   if (st != RSX_SUCCESS || vocab == 0 || dim == 0) return st;
   return hip_status(launch_embedding_grad({dout, tokens, grad, dout_stride, grad_stride, ntokens, vocab, dim, first,

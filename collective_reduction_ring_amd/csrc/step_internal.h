@@ -48,7 +48,7 @@ struct EmbedGradArgs {
   void* ws;
 };
 // Workspace of the gradient, in bytes.
-uint64_t embedding_grad_ws(uint64_t dim, uint64_t n);
+uint64_t embedding_grad_ws(uint64_t vocab, uint64_t dim, uint64_t n);
 hipError_t launch_embedding_grad(const EmbedGradArgs& a, hipStream_t s);
 
 // ------------------------------------------------------------ layer norm

@@ -423,7 +423,7 @@ rsx_status_t rsx_embedding(const void* table, size_t table_stride, size_t vocab,
  * taken in the order of its positions, in chunks.  Without `accumulate` every
  * row is written, with it only the rows that occur.
  */
-size_t rsx_embedding_grad_workspace_size(size_t ntokens, size_t dim);
+size_t rsx_embedding_grad_workspace_size(size_t ntokens, size_t vocab, size_t dim);
 rsx_status_t rsx_embedding_grad(const void* dout, size_t dout_stride, rsx_dtype_t dout_type,
                                 const void* tokens, size_t ntokens, rsx_dtype_t token_type,
                                 int64_t first, float scale, void* grad, size_t grad_stride,

@@ -127,12 +127,12 @@ def test_nothing_to_do(fn, kw):
 
 def test_workspace_sizes():
     lib = L.lib()
-    assert lib.rsx_embedding_grad_workspace_size(0, 64) == 0
-    assert lib.rsx_embedding_grad_workspace_size(BIG, 64) == 0
-    # keys and positions twice, and two partial rows of fp32 for each chunk of 32
+    assert lib.rsx_embedding_grad_workspace_size(0, 100, 64) == 0
+    assert lib.rsx_embedding_grad_workspace_size(BIG, 100, 64) == 0
+    # keys and positions twice, and two partial rows of fp32 for each chunk of 128
     n, d = 65536, 4096
-    need = lib.rsx_embedding_grad_workspace_size(n, d)
-    assert 16 * n + 2 * (n // 32) * d * 4 <= need <= 16 * n + 2 * (n // 32) * d * 4 + (1 << 20)
+    need = lib.rsx_embedding_grad_workspace_size(n, 50000, d)
+    assert 16 * n + 2 * (n // 128) * d * 4 <= need <= 16 * n + 2 * (n // 128) * d * 4 + (1 << 20)
     assert lib.rsx_layer_norm_grad_workspace_size(0, 64) == 0
     assert lib.rsx_layer_norm_grad_workspace_size(1, 64) == 2 * 64 * 4
     assert lib.rsx_token_logprobs_workspace_size(4096, 1000, 4) == 0

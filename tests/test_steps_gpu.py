@@ -96,6 +96,10 @@ GRAD = [  # n, vocab, dim, dout, grad, tokens, first, kind, accumulate, pad
     (20000, 100003, 17, F16, F16, torch.int64, 7, "zipf", False, 3), (50001, 300000, 8, BF16, F32, torch.int64, 0, "any", False, 0),
     (40000, 70, 520, BF16, F32, torch.int64, 0, "one", False, 0), (3000, 200, 1030, F32, BF16, torch.int32, 0, "sorted", False, 0),
     (600, 40, 4097, BF16, BF16, torch.int64, 0, "outside", False, 0), (9000, 64, 16, F32, F16, torch.int64, 0, "few", True, 0),
+    (32, 40, 300, BF16, F32, torch.int64, 0, "few", False, 0), (33, 9000, 72, F32, F32, torch.int64, 0, "any", False, 1),
+    (140001, 3001, 24, BF16, F32, torch.int64, 5, "zipf", False, 1), (131073, 520, 9, F32, BF16, torch.int32, 0, "few", False, 0),
+    (131072, 5000, 10, F16, F32, torch.int64, -3, "zipf", False, 0), (10, 70000, 2, F32, BF16, torch.int64, 0, "any", False, 0),
+    (9001, 600000, 1, BF16, BF16, torch.int64, 0, "zipf", False, 0), (70000, 2000, 1100, BF16, BF16, torch.int64, 0, "zipf", False, 0),
 ]
 
 
