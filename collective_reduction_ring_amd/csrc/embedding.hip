@@ -22,12 +22,6 @@ __device__ __forceinline__ uint64_t token_row(const void* tokens, uint64_t i, in
   return wide ? token_row<int64_t>(tokens, i, first) : token_row<int32_t>(tokens, i, first);
 }
 
-__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
-  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<int>(v));
-  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<int>(v >> 32));
-  return (static_cast<uint64_t>(hi) << 32) | lo;
-}
-
 // Elements of a vector of the gradient: 16 bytes of the wider type, so that
 // each of a wave's accesses covers one unbroken span on either side.
 template <class T, class U>

@@ -8,7 +8,9 @@
 // Everything is held in fp32 and rounded once, at the store.  All kernels
 // here are bound by HBM: a row is read once into registers, both its sums are
 // taken there (the variance from the differences, so no digits are lost to a
-// large mean), and the result is written from them.
+// large mean), and the result is written from them.  Measured: 32768 rows of
+// 4096 bf16 forward 91 us (5.9 TB/s), backward 139 us (5.8 TB/s); rows that are
+// no multiple of 16 bytes share cache lines and run at 4.3 to 5 TB/s.
 #include "step_device.h"
 
 namespace rsx {
@@ -25,91 +27,122 @@ __device__ __forceinline__ bool squares_overflow(float sq, float mean, float fac
   return sq == INFINITY && fabsf(mean) < INFINITY && factor == 1.0f;
 }
 
-// G lanes share a row; each holds EPL of its elements, vectors of E at
-// (j * G + lane) * E.  G = 64 puts a row in one wave: no barrier, and four
-// rows in a workgroup.
-template <class T, class W, int G, int EPL>
-__global__ __launch_bounds__(G > kThreads ? G : kThreads) void norm_kernel(NormArgs a) {
+// G lanes share R rows; each holds EPL elements of each, vectors of E at
+// (j * G + lane) * E.  Up to G = 64 a row is in one wave: no barrier, and
+// several groups in a workgroup.  A lane's rows share the weights' loads.
+template <class T, class W, int G, int EPL, int R>
+__global__ __launch_bounds__(G > 64 ? G : kThreads) void norm_kernel(NormArgs a) {
   constexpr int E = 16 / sizeof(T);
   constexpr int V = EPL / E;
-  constexpr int kRows = G >= kThreads ? 1 : kThreads / G;
+  constexpr int kGroups = G > 64 ? 1 : kThreads / G;
   typedef Vec<T, E> X;
-  __shared__ float slots[2][1][16];
-  const uint32_t lane = threadIdx.x % G;
+  __shared__ float slots[2][R][16];
   const uint32_t dim = static_cast<uint32_t>(a.dim);
-  const uint64_t row = block_id() * kRows + (kRows > 1 ? threadIdx.x / G : 0);
-  if (row >= a.rows) return;  // whole waves, and the whole workgroup where it shares a row
-  const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+  const uint64_t row = (block_id() * kGroups + sub_row<G, kGroups * G>()) * R;
+  if (row >= a.rows) return;  // all the lanes of a row
+  const uint32_t lane = threadIdx.x % G;
 
-  typename X::type raw[V];
+  typename X::type raw[R][V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) raw[j] = load_row<T, E>(x, (j * G + lane) * E, dim);
+  for (int k = 0; k < R; ++k) {
+    // Past the last row it once more, with nothing stored.
+    const T* x = static_cast<const T*>(a.x) + min(row + k, a.rows - 1) * a.x_stride;
+#pragma unroll
+    for (int j = 0; j < V; ++j) raw[k][j] = load_in<T, E>(x, (j * G + lane) * E, dim);
+  }
 
   const float inv_dim = 1.0f / static_cast<float>(dim);
-  float sum[1] = {0.0f};
+  float sum[R];
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const typename X::wide f = widen<T, E>(raw[j]);
-#pragma unroll
-    for (int i = 0; i < E; ++i) sum[0] += f[i];
-  }
-  group_sum<G, 1>(sum, slots[0]);
-  const float mean = sum[0] * inv_dim;
-
-  float sq[1], factor = 1.0f;
-  for (int turn = 1;; turn = 0) {
-    sq[0] = 0.0f;
+  for (int k = 0; k < R; ++k) {
+    sum[k] = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const uint32_t e = (j * G + lane) * E;
-      const typename X::wide f = (widen<T, E>(raw[j]) - mean) * factor;
-      if (e + E <= dim) {
+      raw[k][j] = in_place<T, E>(raw[k][j], (j * G + lane) * E, dim);
+      const typename X::wide f = widen<T, E>(raw[k][j]);
 #pragma unroll
-        for (int i = 0; i < E; ++i) sq[0] = fmaf(f[i], f[i], sq[0]);
-      } else {
+      for (int i = 0; i < E; ++i) sum[k] += f[i];
+    }
+  }
+  group_sum<G, R>(sum, slots[0]);
+  float mean[R], sq[R], factor[R];
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-          if (e + i < dim) sq[0] = fmaf(f[i], f[i], sq[0]);
+  for (int k = 0; k < R; ++k) {
+    mean[k] = sum[k] * inv_dim;
+    factor[k] = 1.0f;
+  }
+
+  for (int turn = 1;; turn = 0) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      sq[k] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const uint32_t e = (j * G + lane) * E;
+        const typename X::wide f = (widen<T, E>(raw[k][j]) - mean[k]) * factor[k];
+        if (e + E <= dim) {
+#pragma unroll
+          for (int i = 0; i < E; ++i) sq[k] = fmaf(f[i], f[i], sq[k]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < E; ++i)
+            if (e + i < dim) sq[k] = fmaf(f[i], f[i], sq[k]);
+        }
       }
     }
-    group_sum<G, 1>(sq, slots[turn]);
-    if (!squares_overflow(sq[0], mean, factor)) break;
-    factor = kScaleDown;
+    group_sum<G, R>(sq, slots[turn]);
+    bool over = false;
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      if (squares_overflow(sq[k], mean[k], factor[k])) {
+        factor[k] = kScaleDown;
+        over = true;
+      }
+    if (!over) break;
   }
-  const float rstd = factor / sqrtf(sq[0] * inv_dim + a.eps * factor * factor);
-  if (lane == 0) {
-    if (a.mean != nullptr) a.mean[row] = mean;
-    if (a.rstd != nullptr) a.rstd[row] = rstd;
+  float rstd[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    rstd[k] = factor[k] / sqrtf(sq[k] * inv_dim + a.eps * factor[k] * factor[k]);
+    if (lane == 0 && row + k < a.rows) {
+      if (a.mean != nullptr) a.mean[row + k] = mean[k];
+      if (a.rstd != nullptr) a.rstd[row + k] = rstd[k];
+    }
   }
 
   const W* w = static_cast<const W*>(a.weight);
   const W* b = static_cast<const W*>(a.bias);
-  T* y = static_cast<T*>(a.y) + row * a.y_stride;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const uint32_t e = (j * G + lane) * E;
-    typename X::wide f = widen<T, E>(raw[j]);
-    if (a.codes != nullptr) {
-      float m = 0.0f;
+    typename X::wide weight = 1.0f, bias = 0.0f;
+    if (w != nullptr) weight = widen<W, E>(load_pair<W, E>(w, e, dim));
+    if (b != nullptr) bias = widen<W, E>(load_pair<W, E>(b, e, dim));
 #pragma unroll
-      for (int i = 0; i < E; ++i) m = fmaxf(m, ck_magnitude(f[i]));
-      const uint32_t byte = ck_scale_byte(ck_largest<32 / E>(m));
-      const float inverse = ck_inverse(byte);
-      typename Vec<int8_t, E>::type q;
+    for (int k = 0; k < R; ++k) {
+      if (row + k >= a.rows) break;
+      typename X::wide f = widen<T, E>(raw[k][j]);
+      if (a.codes != nullptr) {
+        float m = 0.0f;
 #pragma unroll
-      for (int i = 0; i < E; ++i) q[i] = ck_code(f[i], inverse);
-      store_row<int8_t, E>(a.codes + row * a.dim, e, dim, q);
-      if (e % kCkBlock == 0 && e < dim) a.scales[row * ck_blocks(a.dim) + e / kCkBlock] = static_cast<uint8_t>(byte);
+        for (int i = 0; i < E; ++i) m = fmaxf(m, ck_magnitude(f[i]));
+        const uint32_t byte = ck_scale_byte(ck_largest<32 / E>(m));
+        const float inverse = ck_inverse(byte);
+        typename Vec<int8_t, E>::type q;
+#pragma unroll
+        for (int i = 0; i < E; ++i) q[i] = ck_code(f[i], inverse);
+        store_row<int8_t, E>(a.codes + (row + k) * a.dim, e, dim, q);
+        if (e % kCkBlock == 0 && e < dim)
+          a.scales[(row + k) * ck_blocks(a.dim) + e / kCkBlock] = static_cast<uint8_t>(byte);
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i) f[i] = (f[i] - mean[k]) * rstd[k] * weight[i] + bias[i];
+      store_row<T, E>(static_cast<T*>(a.y) + (row + k) * a.y_stride, e, dim, narrow<T, E>(f));
     }
-#pragma unroll
-    for (int i = 0; i < E; ++i) f[i] = (f[i] - mean) * rstd;
-    if (w != nullptr) f *= widen<W, E>(load_row<W, E, false>(w, e, dim));
-    if (b != nullptr) f += widen<W, E>(load_row<W, E, false>(b, e, dim));
-    store_row<T, E>(y, e, dim, narrow<T, E>(f));
   }
 }
 
-// Rows too long for the registers: a workgroup reads its row three times,
+// Rows too long for the registers, or too short for a vector: a workgroup reads its row three times,
 // after the first from the caches.
 template <class T, class W>
 __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
@@ -189,15 +222,26 @@ struct Input<T, E, true> {
   typename Vec<int8_t, E>::type q;
   uint32_t scale;
 };
-template <class T, int E, bool CK>
+// IN: rows of at least E elements.
+template <class T, int E, bool CK, bool IN = false>
 __device__ __forceinline__ Input<T, E, CK> load_input(const NormGradArgs& a, uint64_t row, uint32_t e, uint32_t dim) {
   Input<T, E, CK> v;
   if constexpr (CK) {
-    v.q = load_row<int8_t, E>(a.codes + row * a.dim, e, dim);
-    v.scale = e < dim ? a.scales[row * ck_blocks(a.dim) + e / kCkBlock] : 127u;
+    const int8_t* codes = a.codes + row * a.dim;
+    v.q = IN ? load_in<int8_t, E>(codes, e, dim) : load_row<int8_t, E>(codes, e, dim);
+    v.scale = a.scales[row * ck_blocks(a.dim) + min(e, dim - 1) / kCkBlock];
   } else {
-    v.x = load_row<T, E>(static_cast<const T*>(a.x) + row * a.x_stride, e, dim);
+    const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+    v.x = IN ? load_in<T, E>(x, e, dim) : load_row<T, E>(x, e, dim);
   }
+  return v;
+}
+template <class T, int E, bool CK>
+__device__ __forceinline__ Input<T, E, CK> input_in_place(Input<T, E, CK> v, uint32_t e, uint32_t dim) {
+  if constexpr (CK)
+    v.q = in_place<int8_t, E>(v.q, e, dim);
+  else
+    v.x = in_place<T, E>(v.x, e, dim);
   return v;
 }
 template <class T, int E, bool CK>
@@ -213,87 +257,132 @@ __device__ __forceinline__ typename Vec<T, E>::wide input_value(const Input<T, E
 // it takes in registers and writes one partial row of it at the end.
 constexpr uint32_t kGradGroups = 512;
 
-// Each group of G lanes takes every (groups)-th row; its next row is loaded
-// before the current one's sums are exchanged.  dw and db are summed per
-// workgroup over its rows in order, then over workgroups by norm_sum_kernel:
-// a fixed order, whatever the timing.
-template <class T, class W, int G, int EPL, bool CK>
-__global__ __launch_bounds__(G > kThreads ? G : kThreads) void norm_grad_kernel(NormGradArgs a, uint32_t pitch) {
+// Each of the K / G groups of G lanes in a workgroup takes R rows at a time,
+// and loads its next ones before it exchanges the sums of these.  dw and db
+// are summed per workgroup over its rows in order, then over workgroups by
+// norm_sum_kernel: a fixed order, whatever the timing.
+//
+// What bounds it is how much of the rows is on its way while a row's sums are
+// exchanged, and that is a question of registers.  So a lane's rows share its
+// dw, db and weights; rows and weights are held as they came, and what is made
+// of them is made twice; a workgroup of 1024 keeps the weights in LDS, and of
+// fp32 rows the input (8192 rows of 16384: 405 us with 68 bytes of a lane
+// spilled, 302 us so).
+template <class T, class W, int G, int EPL, int K, int R, bool CK>
+__global__ __launch_bounds__(K) void norm_grad_kernel(NormGradArgs a, uint32_t pitch) {
   constexpr int E = 16 / sizeof(T);
   constexpr int V = EPL / E;
-  constexpr int kRows = G >= kThreads ? 1 : kThreads / G;
+  constexpr int kGroups = K / G;
+  constexpr bool kWeightsInLds = K == 1024;
+  constexpr bool kInputInLds = K == 1024 && E == 4 && !CK;
   typedef Vec<T, E> X;
-  __shared__ float slots[2][2][16];
-  __shared__ float join[kRows > 1 ? kRows * G * EPL : 1];
+  __shared__ float slots[2][2 * R][16];
+  __shared__ float join[kGroups > 1 ? K * EPL : 1];
+  __shared__ typename Vec<W, E>::type lds_w[kWeightsInLds ? V : 1][kWeightsInLds ? K : 1];
+  __shared__ Input<T, E, CK> lds_x[kInputInLds ? R * V : 1][kInputInLds ? K : 1];
   const uint32_t lane = threadIdx.x % G;
-  const uint32_t sub = kRows > 1 ? threadIdx.x / G : 0;
+  const uint32_t sub = sub_row<G, K>();
   const uint32_t dim = static_cast<uint32_t>(a.dim);
-  const uint64_t step = static_cast<uint64_t>(gridDim.x) * kRows;
+  const uint64_t step = static_cast<uint64_t>(gridDim.x) * (kGroups * R);
   const T* dy = static_cast<const T*>(a.dy);
   T* dx = static_cast<T*>(a.dx);
   const float inv_dim = 1.0f / static_cast<float>(dim);
+  uint64_t row = (static_cast<uint64_t>(blockIdx.x) * kGroups + sub) * R;
 
-  typename X::wide w[V], dw[V], db[V];
+  typename Vec<W, E>::type held_w[kWeightsInLds ? 1 : V];
+  typename X::wide dw[V], db[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const uint32_t e = (j * G + lane) * E;
-#pragma unroll
-    for (int i = 0; i < E; ++i) w[j][i] = 1.0f;
-    if (a.weight != nullptr) w[j] = widen<W, E>(load_row<W, E, false>(static_cast<const W*>(a.weight), e, dim));
+    typename Vec<W, E>::type w = static_cast<W>(1.0f);
+    if (a.weight != nullptr)
+      w = load_pair<W, E>(static_cast<const W*>(a.weight), (j * G + lane) * E, dim);
+    if constexpr (kWeightsInLds)
+      lds_w[j][threadIdx.x] = w;  // read by this lane alone
+    else
+      held_w[j] = w;
     dw[j] = 0.0f;
     db[j] = 0.0f;
   }
+  auto weight = [&](int j) {
+    if constexpr (kWeightsInLds)
+      return widen<W, E>(lds_w[j][fresh(threadIdx.x)]);
+    else
+      return widen<W, E>(fresh(held_w[j]));
+  };
 
-  uint64_t row = static_cast<uint64_t>(blockIdx.x) * kRows + sub;
-  typename X::type next_dy[V];
-  Input<T, E, CK> next_x[V];
-  float next_mean = 0.0f, next_rstd = 0.0f;
-  if (row < a.rows) {
+  typename X::type next_dy[R][V];
+  Input<T, E, CK> next_x[R][V];
+  float next_mean[R], next_rstd[R];
+  auto load = [&](uint64_t first) {
+    const uint32_t e = fresh(lane * E);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const uint32_t e = (j * G + lane) * E;
-      next_x[j] = load_input<T, E, CK>(a, row, e, dim);
-      next_dy[j] = load_row<T, E>(dy + row * a.dy_stride, e, dim);
-    }
-    next_mean = a.mean[row];
-    next_rstd = a.rstd[row];
-  }
-  uint32_t turn = 0;
-  for (; row < a.rows; row += step, turn ^= 1u) {
-    typename X::wide xhat[V], g[V];
-    const float mean = next_mean, rstd = next_rstd;
-    float s[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const typename X::wide d = widen<T, E>(next_dy[j]);
-      xhat[j] = (input_value<T, E, CK>(next_x[j]) - mean) * rstd;
-      g[j] = d * w[j];
-      db[j] += d;
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        dw[j][i] = fmaf(d[i], xhat[j][i], dw[j][i]);
-        s[0] += g[j][i];
-        s[1] = fmaf(g[j][i], xhat[j][i], s[1]);
-      }
-    }
-    if (row + step < a.rows) {
+    for (int k = 0; k < R; ++k) {
+      const uint64_t r = min(first + k, a.rows - 1);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const uint32_t e = (j * G + lane) * E;
-        next_x[j] = load_input<T, E, CK>(a, row + step, e, dim);
-        next_dy[j] = load_row<T, E>(dy + (row + step) * a.dy_stride, e, dim);
+        next_x[k][j] = load_input<T, E, CK, true>(a, r, e + j * (G * E), dim);
+        next_dy[k][j] = load_in<T, E>(dy + r * a.dy_stride, e + j * (G * E), dim);
       }
-      next_mean = a.mean[row + step];
-      next_rstd = a.rstd[row + step];
+      next_mean[k] = a.mean[r];
+      next_rstd[k] = a.rstd[r];
     }
-    group_sum<G, 2>(s, slots[turn]);
-    const float c1 = s[0] * inv_dim, c2 = s[1] * inv_dim;
+  };
+  // With one row to a workgroup the loop's condition says as much.
+  auto there = [&](int k) { return kGroups * R == 1 || row + k < a.rows; };
+  load(row);
+  uint32_t turn = 0;
+  // The same turns for the whole workgroup: it shares the sums' barrier.
+  for (uint64_t first = row - sub * R; first < a.rows; first += step, row += step, turn ^= 1u) {
+    typename X::type this_dy[R][V];
+    Input<T, E, CK> this_x[R][V];
+    float mean[R], rstd[R], s[2 * R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      mean[k] = next_mean[k];
+      rstd[k] = next_rstd[k];
+      s[2 * k] = s[2 * k + 1] = 0.0f;
+      if (!there(k)) mean[k] = rstd[k] = 0.0f;
+    }
+    const uint32_t e = fresh(lane * E);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      typename X::wide f;
+      const typename X::wide w = weight(j);
 #pragma unroll
-      for (int i = 0; i < E; ++i) f[i] = (g[j][i] - fmaf(xhat[j][i], c2, c1)) * rstd;
-      store_row<T, E>(dx + row * a.dx_stride, (j * G + lane) * E, dim, narrow<T, E>(f));
+      for (int k = 0; k < R; ++k) {
+        this_dy[k][j] = in_place<T, E>(next_dy[k][j], e + j * (G * E), dim);
+        this_x[k][j] = input_in_place<T, E, CK>(next_x[k][j], e + j * (G * E), dim);
+        if (!there(k)) {  // past the last row all is 0, and adds nothing
+          this_dy[k][j] = static_cast<T>(0.0f);
+          this_x[k][j] = {};
+        }
+        if constexpr (kInputInLds) lds_x[k * V + j][threadIdx.x] = this_x[k][j];
+        const typename X::wide d = widen<T, E>(this_dy[k][j]), g = d * w;
+        const typename X::wide xhat = (input_value<T, E, CK>(this_x[k][j]) - mean[k]) * rstd[k];
+        db[j] += d;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          dw[j][i] = fmaf(d[i], xhat[i], dw[j][i]);
+          s[2 * k] += g[i];
+          s[2 * k + 1] = fmaf(g[i], xhat[i], s[2 * k + 1]);
+        }
+      }
+    }
+    if (first + step < a.rows) load(row + step);
+    group_sum<G, 2 * R>(s, slots[turn]);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const typename X::wide w = weight(j);
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        const float c1 = s[2 * k] * inv_dim, c2 = s[2 * k + 1] * inv_dim;
+        if constexpr (kInputInLds) this_x[k][j] = lds_x[k * V + j][fresh(threadIdx.x)];
+        const typename X::wide g = widen<T, E>(fresh(this_dy[k][j])) * w;
+        const typename X::wide xhat = (input_value<T, E, CK>(this_x[k][j]) - mean[k]) * rstd[k];
+        typename X::wide f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) f[i] = (g[i] - fmaf(xhat[i], c2, c1)) * rstd[k];
+        store_row<T, E>(dx + (row + k) * a.dx_stride, e + j * (G * E), there(k) ? dim : 0u, narrow<T, E>(f));
+      }
     }
   }
 
@@ -301,17 +390,20 @@ __global__ __launch_bounds__(G > kThreads ? G : kThreads) void norm_grad_kernel(
   float* part = a.partial + static_cast<uint64_t>(blockIdx.x) * 2 * pitch;
 #pragma unroll
   for (int k = 0; k < 2; ++k, part += pitch) {
-    if constexpr (kRows > 1) {
+    if constexpr (kGroups > 1) {
       __syncthreads();
 #pragma unroll
       for (int j = 0; j < V; ++j)
 #pragma unroll
-        for (int i = 0; i < E; ++i) join[sub * (G * EPL) + (j * G + lane) * E + i] = k == 0 ? dw[j][i] : db[j][i];
+        for (int i = 0; i < E; ++i) {
+          const uint32_t e = (j * G + lane) * E + i;
+          if (e < dim) join[sub * (G * EPL) + e] = k == 0 ? dw[j][i] : db[j][i];
+        }
       __syncthreads();
-      for (uint32_t e = threadIdx.x; e < dim; e += kThreads) {
+      for (uint32_t e = threadIdx.x; e < dim; e += K) {
         float t = 0.0f;
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) t += join[r * (G * EPL) + e];
+        for (int r = 0; r < kGroups; ++r) t += join[r * (G * EPL) + e];
         part[e] = t;
       }
     } else {
@@ -384,28 +476,28 @@ __global__ __launch_bounds__(kThreads) void norm_columns_kernel(NormGradArgs a, 
   store_row<float, E>(part + pitch, e, dim, db);
 }
 
-// dw and db from the workgroups' partial rows: 64 columns a workgroup, wave w
-// takes partial rows w, w + 16, ...; no rows at all give zeros.
+// dw and db from the workgroups' partial rows: 32 columns a workgroup, in 32
+// parts of the rows; no rows at all give zeros.
 template <class W>
 __global__ __launch_bounds__(1024) void norm_sum_kernel(const float* partial, uint32_t pitch, uint32_t parts,
                                                         uint32_t dim, W* dweight, W* dbias) {
-  __shared__ float join[16][64];
+  __shared__ float join[32][33];
   W* out = blockIdx.y == 0 ? dweight : dbias;
   if (out == nullptr) return;
-  const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const uint32_t e = blockIdx.x * 64 + lane;
+  const uint32_t column = threadIdx.x % 32, slice = threadIdx.x / 32;
+  const uint32_t e = blockIdx.x * 32 + column;
   float t = 0.0f;
   if (e < dim) {
     const float* p = partial + blockIdx.y * pitch + e;
-#pragma unroll 8
-    for (uint32_t r = wave; r < parts; r += 16) t += p[static_cast<uint64_t>(r) * 2 * pitch];
+#pragma unroll 16
+    for (uint32_t r = slice; r < parts; r += 32) t += p[static_cast<uint64_t>(r) * 2 * pitch];
   }
-  join[wave][lane] = t;
+  join[slice][column] = t;
   __syncthreads();
-  if (wave == 0 && e < dim) {
+  if (threadIdx.x < 32 && e < dim) {
     float s = 0.0f;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) s += join[r][lane];
+    for (int r = 0; r < 32; ++r) s += join[r][column];
     out[e] = static_cast<W>(s);
   }
 }
@@ -460,27 +552,36 @@ hipError_t checkpoint(const PackArgs& a, bool pack, hipStream_t s) {
 }
 
 // --------------------------------------------------------------- launches
-template <class T, class W, int G, int EPL>
+// Rows from which on two share a group and its weights' loads (32768 rows of
+// 4096 bf16 with fp32 weights: 96 us, one by one 120); fewer leave CUs idle.
+// Rows of more than 4096 are their own group's (16384 rows of 8000 bf16: 96 us,
+// in pairs 111).
+constexpr uint64_t kPairRows = 4096;
+
+template <class T, class W, int G, int EPL, int R = 1>
 hipError_t norm_go(const NormArgs& a, hipStream_t s) {
-  constexpr uint32_t kRows = G >= kThreads ? 1 : kThreads / G;
+  if constexpr (R > 1)
+    if (a.rows < kPairRows) return norm_go<T, W, G, EPL, 1>(a, s);
+  constexpr uint32_t kRows = (G > 64 ? 1 : kThreads / G) * R;
   const uint64_t grid = (a.rows + kRows - 1) / kRows;
-  return launch(norm_kernel<T, W, G, EPL>, grid_of(grid), G > kThreads ? G : kThreads, 0, s, a);
+  return launch(norm_kernel<T, W, G, EPL, R>, grid_of(grid), G > 64 ? G : kThreads, 0, s, a);
 }
 
 template <class T, class W>
 hipError_t norm(const NormArgs& a, hipStream_t s) {
-  // A wave per row where there are rows for every wave slot of the chip's
-  // first fill; with fewer, four waves share a row and it is done sooner.
-  if (a.rows >= 2048) {
-    if (a.dim <= 512) return norm_go<T, W, 64, 8>(a, s);
-    if (a.dim <= 1024) return norm_go<T, W, 64, 16>(a, s);
-    if (a.dim <= 2048) return norm_go<T, W, 64, 32>(a, s);
-    if (a.dim <= 4096) return norm_go<T, W, 64, 64>(a, s);
-  }
-  if (a.dim <= 2048) return norm_go<T, W, 256, 8>(a, s);
-  if (a.dim <= 4096) return norm_go<T, W, 256, 16>(a, s);
-  if (a.dim <= 8192) return norm_go<T, W, 256, 32>(a, s);
-  if (a.dim <= 16384) return norm_go<T, W, 256, 64>(a, s);
+  if (a.dim < 16 / sizeof(T)) return launch(norm_long_kernel<T, W>, grid_of(a.rows), 1024, 0, s, a);
+  // Lanes as the row fills them with 8 to 24 elements each.  More elements and
+  // fewer lanes leave too few waves, more lanes wait longer at the barriers
+  // (16384 rows of 4096 bf16: 256 lanes 47 us, 64 lanes 71, 512 lanes 62).
+  if (a.dim <= 128) return norm_go<T, W, 16, 8, 2>(a, s);
+  if (a.dim <= 256) return norm_go<T, W, 32, 8, 2>(a, s);
+  if (a.dim <= 512) return norm_go<T, W, 64, 8, 2>(a, s);
+  if (a.dim <= 1024) return norm_go<T, W, 64, 16, 2>(a, s);
+  if (a.dim <= 2048) return norm_go<T, W, 128, 16, 2>(a, s);
+  if (a.dim <= 4096) return norm_go<T, W, 256, 16, 2>(a, s);
+  if (a.dim <= 8192) return norm_go<T, W, 512, 16>(a, s);
+  if (a.dim <= 12288) return norm_go<T, W, 512, 24>(a, s);
+  if (a.dim <= 16384) return norm_go<T, W, 1024, 16>(a, s);
   if (a.dim <= 32768) return norm_go<T, W, 1024, 32>(a, s);
   return launch(norm_long_kernel<T, W>, grid_of(a.rows), 1024, 0, s, a);
 }
@@ -488,13 +589,22 @@ hipError_t norm(const NormArgs& a, hipStream_t s) {
 uint32_t grad_pitch(uint64_t dim) { return static_cast<uint32_t>((dim + 15) / 16 * 16); }
 uint32_t grad_parts(uint64_t rows) { return static_cast<uint32_t>(rows < kGradGroups ? rows : kGradGroups); }
 
-template <class T, class W, int G, int EPL, bool CK>
+template <class T, class W, int G, int EPL, int K, int R, bool CK>
 hipError_t grad_go(const NormGradArgs& a, uint32_t pitch, uint32_t* parts, hipStream_t s) {
-  constexpr uint32_t kRows = G >= kThreads ? 1 : kThreads / G;
-  const uint32_t need = static_cast<uint32_t>((a.rows + kRows - 1) / kRows < kGradGroups ? (a.rows + kRows - 1) / kRows
-                                                                                         : kGradGroups);
-  *parts = need;
-  return launch(norm_grad_kernel<T, W, G, EPL, CK>, dim3(need), G > kThreads ? G : kThreads, 0, s, a, pitch);
+  constexpr uint64_t kRows = K / G * R;
+  *parts = grad_parts((a.rows + kRows - 1) / kRows);
+  return launch(norm_grad_kernel<T, W, G, EPL, K, R, CK>, dim3(*parts), K, 0, s, a, pitch);
+}
+
+// Rows too long for the registers, or too short for a vector.
+template <class T, class W, bool CK>
+hipError_t grad_long(const NormGradArgs& a, uint32_t pitch, uint32_t* parts, hipStream_t s) {
+  *parts = grad_parts(a.rows);
+  const uint32_t per = kThreads * (16 / sizeof(T));
+  const uint32_t columns = static_cast<uint32_t>((a.dim + per - 1) / per);
+  const hipError_t e = launch(norm_columns_kernel<T, CK>, dim3(columns * *parts), kThreads, 0, s, a, pitch, *parts, columns);
+  if (e != hipSuccess) return e;
+  return launch(norm_grad_long_kernel<T, W, CK>, grid_of(a.rows), 1024, 0, s, a);
 }
 
 template <class T, class W, bool CK>
@@ -503,29 +613,31 @@ hipError_t norm_grad(const NormGradArgs& a, hipStream_t s) {
   uint32_t parts = 0;
   hipError_t e = hipSuccess;
   if (a.rows != 0) {
-    if (a.dim <= 512) {
-      e = grad_go<T, W, 64, 8, CK>(a, pitch, &parts, s);
+    // Few elements to a lane, so that its sums of dw and db leave registers to
+    // the rows on their way (16384 rows of 4096 bf16 from a checkpoint: 8
+    // elements 83 us, 16 elements 112).
+    if (a.dim < 16 / sizeof(T) || a.dim > 16384) {
+      e = grad_long<T, W, CK>(a, pitch, &parts, s);
+    } else if (a.dim <= 128) {
+      e = grad_go<T, W, 16, 8, 256, 2, CK>(a, pitch, &parts, s);
+    } else if (a.dim <= 256) {
+      e = grad_go<T, W, 32, 8, 256, 2, CK>(a, pitch, &parts, s);
+    } else if (a.dim <= 512) {
+      e = grad_go<T, W, 64, 8, 256, 2, CK>(a, pitch, &parts, s);
     } else if (a.dim <= 1024) {
-      e = grad_go<T, W, 64, 16, CK>(a, pitch, &parts, s);
+      e = grad_go<T, W, 128, 8, 256, 2, CK>(a, pitch, &parts, s);
     } else if (a.dim <= 2048) {
-      e = grad_go<T, W, 256, 8, CK>(a, pitch, &parts, s);
+      e = grad_go<T, W, 256, 8, 512, 1, CK>(a, pitch, &parts, s);
     } else if (a.dim <= 4096) {
-      e = grad_go<T, W, 256, 16, CK>(a, pitch, &parts, s);
+      e = grad_go<T, W, 512, 8, 512, 1, CK>(a, pitch, &parts, s);
     } else if (a.dim <= 8192) {
-      e = grad_go<T, W, 512, 16, CK>(a, pitch, &parts, s);
-    } else if (a.dim <= 16384) {
-      e = grad_go<T, W, 1024, 16, CK>(a, pitch, &parts, s);
+      e = grad_go<T, W, 512, 16, 512, 1, CK>(a, pitch, &parts, s);
     } else {
-      parts = grad_parts(a.rows);
-      const uint32_t per = kThreads * (16 / sizeof(T));
-      const uint32_t columns = static_cast<uint32_t>((a.dim + per - 1) / per);
-      e = launch(norm_columns_kernel<T, CK>, dim3(columns * parts), kThreads, 0, s, a, pitch, parts, columns);
-      if (e != hipSuccess) return e;
-      e = launch(norm_grad_long_kernel<T, W, CK>, grid_of(a.rows), 1024, 0, s, a);
+      e = grad_go<T, W, 1024, 16, 1024, 1, CK>(a, pitch, &parts, s);
     }
   }
   if (e != hipSuccess || (a.dweight == nullptr && a.dbias == nullptr)) return e;
-  return launch(norm_sum_kernel<W>, dim3(static_cast<uint32_t>((a.dim + 63) / 64), 2), 1024, 0, s, a.partial, pitch,
+  return launch(norm_sum_kernel<W>, dim3(static_cast<uint32_t>((a.dim + 31) / 32), 2), 1024, 0, s, a.partial, pitch,
                 parts, static_cast<uint32_t>(a.dim), static_cast<W*>(a.dweight), static_cast<W*>(a.dbias));
 }
 

@@ -54,8 +54,8 @@ __device__ __forceinline__ void store_once(T* p, typename Vec<T, N>::type v) {
                               reinterpret_cast<typename Vec<T, N>::loose*>(p));
 }
 
-// Vector at element e of a row of `dim`; elements past the row's end are 0.
-// `ONCE`: a streamed load.
+// Vector at element e of a row of `dim`; elements past the row's end are 0,
+// and are not touched.  `ONCE`: a streamed load.
 template <class T, int N, bool ONCE = true>
 __device__ __forceinline__ typename Vec<T, N>::type load_row(const T* row, uint32_t e, uint32_t dim) {
   typename Vec<T, N>::type v = {};
@@ -77,6 +77,56 @@ __device__ __forceinline__ void store_row(T* row, uint32_t e, uint32_t dim, type
     for (int i = 0; i < N; ++i)
       if (e + i < dim) row[e + i] = v[i];
   }
+}
+
+// The same for rows of at least N elements, in two steps: a vector that does
+// not fit is loaded from the row's end (load_in), and moved into place when it
+// is used (in_place).  Loads by element, or a move at once, wait for the load:
+// every row of a width that fills no vector then has no other row on its way
+// (gradient of 32767 rows of 4095 bf16: 356 and 214 us).
+template <class T, int N, bool ONCE = true>
+__device__ __forceinline__ typename Vec<T, N>::type load_in(const T* row, uint32_t e, uint32_t dim) {
+  const T* p = row + min(e, dim - N);
+  return ONCE ? load_once<T, N>(p) : load_kept<T, N>(p);
+}
+template <class T, int N>
+__device__ __forceinline__ typename Vec<T, N>::type in_place(typename Vec<T, N>::type v, uint32_t e, uint32_t dim) {
+  constexpr int kBytes = static_cast<int>(sizeof(T)) * N;
+  typedef typename Vec<T, N>::type V;
+  typedef uint64_t Two __attribute__((ext_vector_type(2)));
+  const uint32_t by = min(e - min(e, dim - N), static_cast<uint32_t>(N));
+  if (__ballot(by != 0) == 0) return v;
+  const uint32_t bits = by * static_cast<uint32_t>(sizeof(T)) * 8;
+  auto down = [](Two u, uint32_t n) {  // n <= 128
+    const uint64_t lo = n == 0 ? u[0] : n < 64 ? (u[0] >> n) | (u[1] << (64 - n)) : n < 128 ? u[1] >> (n - 64) : 0;
+    return Two{lo, n < 64 ? u[1] >> n : 0};
+  };
+  if constexpr (kBytes == 16) {
+    return __builtin_bit_cast(V, down(__builtin_bit_cast(Two, v), bits));
+  } else if constexpr (kBytes == 8) {
+    return __builtin_bit_cast(V, bits < 64 ? __builtin_bit_cast(uint64_t, v) >> bits : 0);
+  } else {
+    static_assert(kBytes == 4, "");
+    return __builtin_bit_cast(V, bits < 32 ? __builtin_bit_cast(uint32_t, v) >> bits : 0u);
+  }
+}
+// Both at once, for 16 or 32 bytes, through the caches.
+template <class T, int N>
+__device__ __forceinline__ typename Vec<T, N>::type load_pair(const T* row, uint32_t e, uint32_t dim) {
+  if constexpr (sizeof(T) * N <= 16) {
+    return in_place<T, N>(load_in<T, N, false>(row, e, dim), e, dim);
+  } else {
+    return __builtin_shufflevector(load_pair<T, N / 2>(row, e, dim), load_pair<T, N / 2>(row, e + N / 2, dim), 0, 1, 2, 3, 4, 5,
+                                   6, 7);
+  }
+}
+
+// v, as far as the compiler knows another value each time: what is computed
+// from it in a loop stays in the loop, instead of in registers before it.
+template <class V>
+__device__ __forceinline__ V fresh(V v) {
+  asm volatile("" : "+v"(v));
+  return v;
 }
 
 template <class T, int N>
@@ -126,15 +176,44 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// Sums over the G lanes that share a row.  G = 64: a wave, no LDS.  Otherwise
-// the row has the whole workgroup and `slot` is a [G / 64] array that no sum
-// still in use shares (callers alternate between arrays, one barrier each).
+// For values that are the same in the whole wave, but not to the compiler.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(v)));
+}
+__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
+  return (static_cast<uint64_t>(uniform(static_cast<uint32_t>(v >> 32))) << 32) | uniform(static_cast<uint32_t>(v));
+}
+// Which of the rows of a workgroup, G lanes each, is this lane's.
+template <int G, int K>
+__device__ __forceinline__ uint32_t sub_row() {
+  if constexpr (G >= K) return 0;
+  if constexpr (G >= 64) return uniform(threadIdx.x / G);
+  return threadIdx.x / G;
+}
+
+// Sums over the G lanes that share a row, the same in each of them.  Up to
+// G = 64 in a wave, no LDS.  Otherwise every thread of the workgroup takes
+// part, and `slot` is an array that no sum still in use shares (callers
+// alternate between arrays, one barrier each).
 template <int G, int N>
 __device__ __forceinline__ void group_sum(float (&v)[N], float (*slot)[16]) {
+  static_assert(G == 16 || G == 32 || G % 64 == 0, "");
+  if constexpr (G < 64) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+    for (int i = 0; i < N; ++i) {
+      v[i] += dpp<kSwap1>(v[i]);
+      v[i] += dpp<kSwap2>(v[i]);
+      v[i] += dpp<kHalfMirror>(v[i]);
+      v[i] += dpp<kMirror>(v[i]);
+      if constexpr (G == 32)  // lane ^ 16
+        v[i] += __builtin_bit_cast(float, __builtin_amdgcn_ds_swizzle(__builtin_bit_cast(int, v[i]), 0x401f));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  }
   if constexpr (G > 64) {
-    const int wave = threadIdx.x / 64;
+    const int wave = threadIdx.x / 64, first = wave / (G / 64) * (G / 64);
     if (threadIdx.x % 64 == 0) {
 #pragma unroll
       for (int i = 0; i < N; ++i) slot[i][wave] = v[i];
@@ -144,7 +223,7 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float (*slot)[16]) {
     for (int i = 0; i < N; ++i) {
       float t = 0.0f;
 #pragma unroll
-      for (int w = 0; w < G / 64; ++w) t += slot[i][w];
+      for (int w = 0; w < G / 64; ++w) t += slot[i][first + w];
       v[i] = t;
     }
   }

@@ -177,6 +177,8 @@ NORM = [  # rows, dim, x, weight, pad, affine
     (2, 32768, F32, F32, 0, "wb"), (2, 33001, F16, F32, 1, "wb"), (2, 70001, F32, F32, 0, "w"),
     (2048, 100, BF16, BF16, 0, "wb"), (2051, 600, F32, F32, 0, "wb"), (2050, 1111, F16, F16, 1, "wb"),
     (2049, 2056, BF16, F32, 0, "wb"), (2048, 4096, F32, F32, 0, "wb"),
+    (4097, 40, BF16, F32, 0, "wb"), (4099, 255, F32, F32, 1, "wb"), (4101, 511, F16, F16, 0, "w"), (4097, 1030, BF16, BF16, 0, "b"),
+    (4097, 2050, F16, F32, 1, "wb"), (3, 9001, BF16, F32, 0, "wb"), (2, 12287, F32, F32, 1, "wb"), (2, 8, BF16, BF16, 0, "wb"),
 ]
 
 
@@ -233,6 +235,8 @@ NGRAD = [  # rows, dim, x, weight, pad, affine
     (3, 2049, F16, F16, 1, "w"), (1200, 1025, BF16, BF16, 0, "w"), (515, 4096, BF16, BF16, 0, "w"), (3, 8191, BF16, F32, 0, "w"),
     (520, 8192, F32, F32, 0, "w"), (2, 16383, F32, F32, 2, "w"), (514, 12000, BF16, BF16, 0, "w"), (3, 16385, BF16, BF16, 0, "w"),
     (513, 20001, F32, F32, 1, "w"), (2100, 96, BF16, F32, 0, "w"),
+    (16385, 16, BF16, F32, 0, "w"), (8193, 129, F32, F32, 1, "w"), (4097, 300, F16, F16, 0, ""), (1025, 2047, F32, F32, 0, "w"),
+    (513, 8191, BF16, BF16, 1, "w"), (514, 16380, F32, F32, 0, "w"), (2, 8, BF16, BF16, 0, "w"),
 ]
 
 
