@@ -110,15 +110,30 @@ __device__ __forceinline__ typename Vec<T, N>::type in_place(typename Vec<T, N>:
     return __builtin_bit_cast(V, bits < 32 ? __builtin_bit_cast(uint32_t, v) >> bits : 0u);
   }
 }
-// Both at once, for 16 or 32 bytes, through the caches.
-template <class T, int N>
-__device__ __forceinline__ typename Vec<T, N>::type load_pair(const T* row, uint32_t e, uint32_t dim) {
+// Both steps for vectors of 32 bytes too.
+template <class T, int N, bool ONCE>
+__device__ __forceinline__ typename Vec<T, N>::type load_wide(const T* row, uint32_t e, uint32_t dim) {
   if constexpr (sizeof(T) * N <= 16) {
-    return in_place<T, N>(load_in<T, N, false>(row, e, dim), e, dim);
+    return load_in<T, N, ONCE>(row, e, dim);
   } else {
-    return __builtin_shufflevector(load_pair<T, N / 2>(row, e, dim), load_pair<T, N / 2>(row, e + N / 2, dim), 0, 1, 2, 3, 4, 5,
+    return __builtin_shufflevector(load_in<T, N / 2, ONCE>(row, e, dim), load_in<T, N / 2, ONCE>(row, e + N / 2, dim), 0, 1, 2, 3,
+                                   4, 5, 6, 7);
+  }
+}
+template <class T, int N>
+__device__ __forceinline__ typename Vec<T, N>::type wide_in_place(typename Vec<T, N>::type v, uint32_t e, uint32_t dim) {
+  if constexpr (sizeof(T) * N <= 16) {
+    return in_place<T, N>(v, e, dim);
+  } else {
+    return __builtin_shufflevector(in_place<T, N / 2>(__builtin_shufflevector(v, v, 0, 1, 2, 3), e, dim),
+                                   in_place<T, N / 2>(__builtin_shufflevector(v, v, 4, 5, 6, 7), e + N / 2, dim), 0, 1, 2, 3, 4, 5,
                                    6, 7);
   }
+}
+// Both at once, through the caches.
+template <class T, int N>
+__device__ __forceinline__ typename Vec<T, N>::type load_pair(const T* row, uint32_t e, uint32_t dim) {
+  return wide_in_place<T, N>(load_wide<T, N, false>(row, e, dim), e, dim);
 }
 
 // v, as far as the compiler knows another value each time: what is computed

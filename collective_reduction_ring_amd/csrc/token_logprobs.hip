@@ -9,7 +9,9 @@
 // The forward pass reads a row once: each lane keeps a running maximum m, the
 // sum s of 2^u and the sum t of 2^u u, u = (z - m) log2 e, all in fp32.  Then
 // lse = m + ln s and H = ln s - t ln 2 / s, a sum of two terms that are not
-// negative, so nothing cancels.  A masked logit (-inf) adds nothing; a row of
+// negative, so nothing cancels.  The instructions bound it nearly as much as
+// the reads do, so u is one: z log2 e - r, with r = m log2 e rounded; what the
+// rounding took is put back once, at the end.  A masked logit (-inf) adds nothing; a row of
 // nothing else has lse = -inf, log probabilities of -inf, entropy 0 and a
 // gradient of 0.  A row with a NaN or +inf has NaN for lse, log probabilities,
 // entropy and gradient.  A token outside the row has log probability 0 and no
@@ -20,7 +22,6 @@ namespace rsx {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -93,12 +94,13 @@ __device__ __forceinline__ void insert(Best& b, uint64_t c, uint32_t lane, uint3
   const uint64_t last = lane_value64(b.mine, static_cast<int>(top) - 1);
   b.least = last > b.floor ? last : b.floor;
 }
-// The top-th largest of the lanes' values, one bit at a time.
+// A lower bound of the top-th largest of the lanes' values, its upper 16 bits
+// one at a time (of 16-bit logits the others follow from the sign).
 __device__ __forceinline__ uint32_t lanes_nth(uint32_t v, uint32_t top) {
   uint64_t alive = ~0ull;
   uint32_t found = 0, need = top;
 #pragma unroll
-  for (int bit = 31; bit >= 0; --bit) {
+  for (int bit = 31; bit >= 16; --bit) {
     const uint64_t set = __ballot((v >> bit) & 1u) & alive;
     const uint32_t c = static_cast<uint32_t>(__popcll(set));
     if (c >= need) {
@@ -113,136 +115,240 @@ __device__ __forceinline__ uint32_t lanes_nth(uint32_t v, uint32_t top) {
 }
 
 // ---------------------------------------------------------------- forward
-constexpr int kUnroll = 4;  // vectors a lane has in flight
+constexpr int kUnroll = 4;  // vectors a lane has in flight, and as many on their way
 
 struct Partial {
   float m, s, t, pad;
 };
 
-__device__ __forceinline__ float finish_row(const LogprobArgs& a, uint64_t row, const Stats& st) {
+// A row (or a slice of one) as single elements up to the first 16-byte
+// boundary, whole vectors, and single elements again: accesses that are off a
+// boundary cost a quarter of the rate.
+template <class T>
+struct Cut {
+  static constexpr int E = 16 / sizeof(T);
+  uint32_t head, vectors, tail;
+  const T* middle;
+  __device__ __forceinline__ Cut(const T* row, const void* align, uint32_t n) {
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(align) / sizeof(T)) % E;
+    head = min((E - off) % E, n);
+    vectors = (n - head) / E;
+    tail = n - head - vectors * E;
+    middle = row + head;
+  }
+  // Threads 0 .. head - 1 and E .. E + tail - 1 have a single element each;
+  // its index, or `n` and more for none.
+  __device__ __forceinline__ uint32_t single(uint32_t thread) const {
+    if (thread < head) return thread;
+    const uint32_t i = thread - E;
+    return thread >= E && i < tail ? head + vectors * E + i : 0xffffffffu;
+  }
+};
+
+__device__ __forceinline__ float logit_at(const LogprobArgs& a, uint64_t at) {
+  return a.type == RSX_FLOAT32    ? static_cast<const float*>(a.logits)[at]
+         : a.type == RSX_BFLOAT16 ? static_cast<float>(static_cast<const bf16_t*>(a.logits)[at])
+                                  : static_cast<float>(static_cast<const f16_t*>(a.logits)[at]);
+}
+
+// What a row's results need of its token; asked for before the row is read.
+struct Token {
+  bool there;
+  float z;
+};
+__device__ __forceinline__ Token row_token(const LogprobArgs& a, uint64_t row) {
+  const uint64_t tok = token_at(a.tokens, row, a.wide);
+  const bool there = tok < a.vocab;
+  return {there, there ? logit_at(a, row * a.stride + tok) : 0.0f};
+}
+__device__ __forceinline__ float finish_row(const LogprobArgs& a, uint64_t row, const Stats& st, const Token& tok) {
   const bool none = st.s == 0.0f && st.m == -INFINITY;  // every logit masked
   const float ln_s = logf(st.s);
   const float lse = none ? -INFINITY : st.m + ln_s;
-  const uint64_t tok = token_at(a.tokens, row, a.wide);
-  float z = 0.0f, lp = 0.0f;
-  if (tok < a.vocab) {
-    const uint64_t at = row * a.stride + tok;
-    z = a.type == RSX_FLOAT32    ? static_cast<const float*>(a.logits)[at]
-        : a.type == RSX_BFLOAT16 ? static_cast<float>(static_cast<const bf16_t*>(a.logits)[at])
-                                 : static_cast<float>(static_cast<const f16_t*>(a.logits)[at]);
-    // (z - m) - ln s keeps more digits than z - lse where the maximum is large
-    lp = none ? -INFINITY : (z - st.m) - ln_s;
-  }
-  a.logprob[row] = lp;
+  // (z - m) - ln s keeps more digits than z - lse where the maximum is large
+  a.logprob[row] = !tok.there ? 0.0f : none ? -INFINITY : (tok.z - st.m) - ln_s;
   a.lse[row] = lse;
   if (a.entropy != nullptr) a.entropy[row] = none ? 0.0f : ln_s - st.t * kLn2 / st.s;
   return lse;
 }
 
+// A lane's statistics on the way.  `r` stands for m log2 e, for m of at least
+// -kFar: what lies further down adds nothing to a row that has more.  A row
+// whose maximum itself is beyond +-kFar (masked by the type's lowest value
+// throughout, for one) is summed again by `careful` steps.
+constexpr float kFar = 0x1p126f;
+struct Running {
+  float m, r, s, t;
+};
+__device__ __forceinline__ float scaled(float m) { return fmaxf(m, -kFar) * kLog2e; }
+__device__ __forceinline__ void raise(Running& a, float m) {
+  const float r = scaled(m), d = fmaxf(a.r - r, kLeast), f = __builtin_amdgcn_exp2f(d);
+  a.t = fmaf(d, a.s, a.t) * f;
+  a.s *= f;
+  a.r = r;
+  a.m = m;
+}
+__device__ __forceinline__ void add(Running& a, float z) {
+  const float u = fmaf(z, kLog2e, -a.r);
+  const float p = __builtin_amdgcn_exp2f(u);
+  a.s += p;
+  a.t = fmaf(p, fmaxf(u, kLeast), a.t);
+}
+// The same sums against m itself.
+__device__ __forceinline__ Stats settled(const Running& a) {
+  if (a.m < -kFar) return {a.m, a.s, a.t};  // s is 0 or a NaN
+  const float off = fmaf(a.m, kLog2e, -a.r), f = __builtin_amdgcn_exp2f(-off);
+  return {a.m, a.s * f, fmaf(-off, a.s, a.t) * f};
+}
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) > kFar && fabsf(m) < INFINITY; }
+__device__ __forceinline__ void add_careful(Stats& a, float z) {
+  if (z > a.m) a = rebase(a, z);
+  const float u = (z - reference(a.m)) * kLog2e;
+  const float p = __builtin_amdgcn_exp2f(u);
+  a.s += p;
+  a.t = fmaf(p, fmaxf(u, kLeast), a.t);
+}
+
+// The smallest logit that may pass `least`.  Numbers alone are compared so; as
+// long as a NaN may pass, it has to go by candidates.
+__device__ __forceinline__ float passing(uint64_t least) {
+  return order_value(static_cast<uint32_t>(least >> 32));
+}
+__device__ __forceinline__ bool nan_passes(uint64_t least) { return (least >> 32) <= 1u; }
+
+// The elements of a lane in a step, as candidates.
+__device__ __forceinline__ void offer(Best& best, float z, uint32_t index, bool there, uint32_t lane, uint32_t top) {
+  const uint64_t c = there ? candidate(value_order(z), index) : 0ull;
+  uint64_t who = __ballot(c > best.least);
+  while (who) {
+    const int l = __builtin_ctzll(who);
+    insert(best, lane_value64(c, l), lane, top);
+    who = __ballot(c > best.least) & ~((2ull << l) - 1);
+  }
+}
+
 // Workgroup (row, slice): the statistics and best candidates of `slice`
-// elements; with one slice to a row, the row's results.
-template <class T, bool TOP>
-__global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs a, uint32_t slices, uint32_t slice,
-                                                           Partial* partial, uint64_t* best_out) {
+// elements; with one slice to a row, the row's results.  K waves.
+template <class T, bool TOP, int K>
+__global__ __launch_bounds__(K * 64) void logprob_kernel(LogprobArgs a, uint32_t slices, uint32_t slice,
+                                                         Partial* partial, uint64_t* best_out) {
   constexpr int E = 16 / sizeof(T);
   typedef Vec<T, E> X;
-  __shared__ Stats wave_stats[kWaves];
-  __shared__ uint64_t wave_best[TOP ? kWaves * RSX_TOP_MAX : 1];
+  __shared__ Stats wave_stats[K];
+  __shared__ uint64_t wave_best[TOP ? K * RSX_TOP_MAX : 1];
   __shared__ float row_lse;
   const uint64_t block = block_id();
   const uint64_t row = block / slices;
   if (row >= a.rows) return;
   const uint32_t part = static_cast<uint32_t>(block - row * slices);
-  const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const uint32_t lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
   const uint32_t begin = part * slice;
-  const uint32_t end = min(begin + slice, static_cast<uint32_t>(a.vocab));
-  const T* z = static_cast<const T*>(a.logits) + row * a.stride;
+  const uint32_t n = min(slice, static_cast<uint32_t>(a.vocab) - begin);
+  const T* z = static_cast<const T*>(a.logits) + row * a.stride + begin;
+  const Cut<T> cut(z, z, n);
   const uint32_t top = a.top;
+  Token token = {false, 0.0f};
+  if (slices == 1 && threadIdx.x == 0) token = row_token(a, row);
+  const uint32_t one = cut.single(threadIdx.x);
+  float alone = one < n ? static_cast<float>(z[one]) : -INFINITY;
 
-  Stats st = {-INFINITY, 0.0f, 0.0f};
+  Running st = {-INFINITY, scaled(-INFINITY), 0.0f, 0.0f};
   Best best = {0ull, 0ull, 0ull};
   bool seeded = false;
-  constexpr uint32_t kSpan = 64 * E;             // elements of one vector across a wave
-  constexpr uint32_t kGroup = kSpan * kUnroll;   // of a wave's step
-  for (uint32_t base = begin + wave * kGroup; base < end; base += kWaves * kGroup) {
-    typename X::wide f[kUnroll];
-    const bool full = base + kGroup <= end;  // the same for the wave
-    if (full) {
-      typename X::type raw[kUnroll];
+  // A step is kUnroll vectors of each lane; those past the end read as masked.
+  constexpr uint32_t kGroup = 64 * kUnroll;
+  typename X::type next[kUnroll];
+  auto load = [&](uint32_t base) {
+    const T* p = cut.middle + static_cast<uint64_t>(base + lane) * E;
+    if (base + kGroup <= cut.vectors) {  // the same for the wave
 #pragma unroll
-      for (int j = 0; j < kUnroll; ++j) raw[j] = load_once<T, E>(z + base + j * kSpan + lane * E);
-#pragma unroll
-      for (int j = 0; j < kUnroll; ++j) f[j] = widen<T, E>(raw[j]);
+      for (int j = 0; j < kUnroll; ++j) next[j] = load_once<T, E>(p + j * 64 * E);
     } else {
 #pragma unroll
       for (int j = 0; j < kUnroll; ++j) {
-        const uint32_t e = base + j * kSpan + lane * E;
-        f[j] = widen<T, E>(load_row<T, E>(z, e, end));
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-          if (e + i >= end) f[j][i] = -INFINITY;
+        next[j] = static_cast<T>(-INFINITY);
+        if (base + j * 64 + lane < cut.vectors) next[j] = load_once<T, E>(p + j * 64 * E);
       }
     }
-    float most = f[0][0];
+  };
+  uint32_t base = wave * kGroup;
+  if (base < cut.vectors) load(base);
+  for (; base < cut.vectors; base += K * kGroup) {
+    typename X::type raw[kUnroll];
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j)
+    for (int j = 0; j < kUnroll; ++j) raw[j] = next[j];
+    if (base + K * kGroup < cut.vectors) load(base + K * kGroup);
+    float most = static_cast<float>(raw[0][0]);
 #pragma unroll
-      for (int i = 0; i < E; ++i) most = fmaxf(most, f[j][i]);
-    if (most > st.m) st = rebase(st, most);
-    const float ref = reference(st.m);
+    for (int j = 0; j < kUnroll; ++j) {
+      const typename X::wide f = widen<T, E>(raw[j]);
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j)
+      for (int i = 0; i < E; ++i) most = fmaxf(most, f[i]);
+    }
+    if (most > st.m) raise(st, most);
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const float u = (f[j][i] - ref) * kLog2e;
-        const float p = __builtin_amdgcn_exp2f(u);
-        st.s += p;
-        st.t = fmaf(p, fmaxf(u, kLeast), st.t);
-      }
+    for (int j = 0; j < kUnroll; ++j) {
+      const typename X::wide f = widen<T, E>(raw[j]);
+#pragma unroll
+      for (int i = 0; i < E; ++i) add(st, f[i]);
+    }
     if constexpr (TOP) {
       const uint32_t mine = value_order(most);
       if (!seeded) {
-        // The top-th largest of the lanes' maxima, 64 elements of their own,
-        // is a lower bound of the top-th largest: few candidates pass it.
-        // A maximum of -inf may stand for NaNs (which fmaxf passes over) or for
-        // the fill past the slice's end, and counts as the lowest order; lanes
-        // that are past the end altogether have no element.
+        // The top-th largest of the lanes' maxima, elements of their own, is a
+        // lower bound of the top-th largest: few candidates pass it.  A maximum
+        // of -inf may stand for NaNs (which fmaxf passes over) or for the fill
+        // past the slice's end, and counts as the lowest order; lanes that are
+        // past the end altogether have no element.
         const uint32_t sure = most > -INFINITY ? mine : 1u;
-        const uint32_t bound = lanes_nth(base + lane * E < end ? sure : 0u, top);
-        best.floor = bound == 0u ? 0ull : candidate(bound, 0xffffffffu) - 1;
+        const uint32_t bound = lanes_nth(base + lane < cut.vectors ? sure : 0u, top);
+        best.floor = bound <= 1u ? 0ull : candidate(bound, 0xffffffffu) - 1;
         best.least = best.floor;
         seeded = true;
       }
-      if (__ballot(candidate(mine, base) > best.least)) {
+      const uint32_t first = begin + cut.head + (base + lane) * E;
+      if (nan_passes(best.least) || __ballot(most >= passing(best.least))) {
 #pragma unroll
-        for (int j = 0; j < kUnroll; ++j)
+        for (int j = 0; j < kUnroll; ++j) {
+          const typename X::wide f = widen<T, E>(raw[j]);
+          const bool there = base + j * 64 + lane < cut.vectors;
 #pragma unroll
-          for (int i = 0; i < E; ++i) {
-            const uint32_t e = base + j * kSpan + lane * E + i;
-            const uint64_t c = e < end ? candidate(value_order(f[j][i]), e) : 0ull;
-            uint64_t who = __ballot(c > best.least);
-            while (who) {
-              const int l = __builtin_ctzll(who);
-              insert(best, lane_value64(c, l), lane, top);
-              who = __ballot(c > best.least) & ~((2ull << l) - 1);
-            }
-          }
+          for (int i = 0; i < E; ++i)
+            if (nan_passes(best.least) || __ballot(f[i] >= passing(best.least)))
+              offer(best, f[i], first + j * 64 * E + i, there, lane, top);
+        }
       }
     }
   }
+  if (wave == 0) {
+    if (alone > st.m) raise(st, alone);
+    add(st, alone);
+    if constexpr (TOP) offer(best, alone, begin + one, one < n, lane, top);
+  }
 
-  st = wave_merge(st);
-  if (lane == 0) wave_stats[wave] = st;
+  Stats own = wave_merge(settled(st));
+  if (lane == 0) wave_stats[wave] = own;
   if constexpr (TOP) {
     if (lane < top) wave_best[wave * top + lane] = best.mine;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    Stats all = wave_stats[0];
+  Stats all = wave_stats[0];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) all = merge(all, wave_stats[w]);
+  for (int w = 1; w < K; ++w) all = merge(all, wave_stats[w]);
+  if (is_far(all.m)) {  // the same for the workgroup
+    Stats c = {-INFINITY, 0.0f, 0.0f};
+    for (uint32_t i = threadIdx.x; i < n; i += K * 64) add_careful(c, static_cast<float>(z[i]));
+    c = wave_merge(c);
+    __syncthreads();
+    if (lane == 0) wave_stats[wave] = c;
+    __syncthreads();
+    all = wave_stats[0];
+#pragma unroll
+    for (int w = 1; w < K; ++w) all = merge(all, wave_stats[w]);
+  }
+  if (threadIdx.x == 0) {
     if (slices == 1)
-      row_lse = finish_row(a, row, all);
+      row_lse = finish_row(a, row, all, token);
     else
       partial[block] = {all.m, all.s, all.t, 0.0f};
   }
@@ -251,10 +357,11 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs a, uint32
     const float lse = row_lse;
     // A candidate's rank is the number of larger ones; all are different but
     // for 0, which is none.
-    for (uint32_t i = threadIdx.x; i < kWaves * top; i += kThreads) {
+    for (uint32_t i = threadIdx.x; i < K * top; i += K * 64) {
       const uint64_t c = wave_best[i];
       uint32_t rank = 0;
-      for (uint32_t j = 0; j < kWaves * top; ++j) rank += wave_best[j] > c ? 1u : 0u;
+#pragma unroll 8
+      for (uint32_t j = 0; j < K * top; ++j) rank += wave_best[j] > c ? 1u : 0u;
       if (slices == 1) {
         if (c != 0 && rank < top) {
           const float v = order_value(static_cast<uint32_t>(c >> 32));
@@ -268,8 +375,9 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs a, uint32
     if (slices > 1) {
       // Fewer candidates than `top` in this slice: the rest is none.
       uint32_t found = 0;
-      for (uint32_t j = 0; j < kWaves * top; ++j) found += wave_best[j] != 0 ? 1u : 0u;
-      for (uint32_t i = threadIdx.x; i < top; i += kThreads)
+#pragma unroll 8
+      for (uint32_t j = 0; j < K * top; ++j) found += wave_best[j] != 0 ? 1u : 0u;
+      for (uint32_t i = threadIdx.x; i < top; i += K * 64)
         if (i >= found) best_out[block * top + i] = 0ull;
     }
   }
@@ -278,12 +386,15 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs a, uint32
 // A row's slices joined in order.
 __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs a, uint32_t slices, const Partial* partial,
                                                                 const uint64_t* best) {
+  constexpr int kWaves = kThreads / 64;
   extern __shared__ uint64_t cand[];
   __shared__ Stats wave_stats[kWaves];
   __shared__ float row_lse;
   const uint64_t row = block_id();
   if (row >= a.rows) return;
   const uint32_t top = a.top, n = slices * top;
+  Token token = {false, 0.0f};
+  if (threadIdx.x == 0) token = row_token(a, row);
   for (uint32_t i = threadIdx.x; i < n; i += kThreads) cand[i] = best[row * n + i];
   Stats st = {-INFINITY, 0.0f, 0.0f};
   for (uint32_t i = threadIdx.x; i < slices; i += kThreads) {
@@ -297,7 +408,7 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs a, u
     Stats all = wave_stats[0];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) all = merge(all, wave_stats[w]);
-    row_lse = finish_row(a, row, all);
+    row_lse = finish_row(a, row, all, token);
   }
   if (top == 0) return;
   __syncthreads();
@@ -306,6 +417,7 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs a, u
     const uint64_t c = cand[i];
     if (c == 0) continue;
     uint32_t rank = 0;
+#pragma unroll 8
     for (uint32_t j = 0; j < n; ++j) rank += cand[j] > c ? 1u : 0u;
     if (rank < top) {
       a.top_token[row * top + rank] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(c));
@@ -317,7 +429,7 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs a, u
 
 // Slices of a row.  Enough workgroups for the chip, none below one step of its
 // four waves, and no more than the join takes in one go.
-constexpr uint32_t kStepElems = 8192;   // kWaves * 64 lanes * kUnroll vectors of 8
+constexpr uint32_t kStepElems = 8192;   // 4 waves * 64 lanes * kUnroll vectors of 8
 constexpr uint32_t kWantGroups = 1024;
 constexpr uint32_t kMaxSlices = 64;
 constexpr uint32_t kMaxJoin = 1024;  // candidates, each compared with every other
@@ -336,6 +448,11 @@ Slices slices_of(uint64_t rows, uint64_t vocab, uint32_t top) {
   return {static_cast<uint32_t>((vocab + length - 1) / length), static_cast<uint32_t>(length)};
 }
 
+// One wave to a row where a wave's step holds most of it and there are rows
+// enough: four have barriers, and three of them little to do.
+constexpr uint64_t kWaveRow = 4096;
+constexpr uint64_t kWaveRows = 1024;
+
 template <class T>
 hipError_t logprobs(const LogprobArgs& a, hipStream_t s) {
   const Slices sl = slices_of(a.rows, a.vocab, a.top);
@@ -343,7 +460,10 @@ hipError_t logprobs(const LogprobArgs& a, hipStream_t s) {
   Partial* partial = static_cast<Partial*>(a.ws);
   uint64_t* best = reinterpret_cast<uint64_t*>(static_cast<char*>(a.ws) + (grid * sizeof(Partial) + 255) / 256 * 256);
   const dim3 g = grid_of(grid);
-  const hipError_t e = launch(a.top != 0 ? logprob_kernel<T, true> : logprob_kernel<T, false>, g, kThreads, 0, s, a,
+  if (a.vocab <= kWaveRow && a.rows >= kWaveRows)  // one slice
+    return launch(a.top != 0 ? logprob_kernel<T, true, 1> : logprob_kernel<T, false, 1>, g, 64, 0, s, a, sl.count, sl.length,
+                  partial, best);
+  const hipError_t e = launch(a.top != 0 ? logprob_kernel<T, true, 4> : logprob_kernel<T, false, 4>, g, kThreads, 0, s, a,
                               sl.count, sl.length, partial, best);
   if (e != hipSuccess || sl.count == 1) return e;
   return launch(logprob_join_kernel, grid_of(a.rows), kThreads, sl.count * a.top * sizeof(uint64_t), s, a, sl.count,
@@ -351,19 +471,29 @@ hipError_t logprobs(const LogprobArgs& a, hipStream_t s) {
 }
 
 // --------------------------------------------------------------- gradient
-// Workgroup (row, tile) of kThreads * kUnroll vectors.
+// Workgroup (row, tile) of kThreads * kUnroll vectors; those of the gradient
+// lie on 16-byte boundaries.  The first tile has the row's single elements too.
 template <class T>
 __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs a, uint32_t tiles) {
   constexpr int E = 16 / sizeof(T);
   typedef Vec<T, E> X;
-  constexpr uint32_t kSpan = kThreads * E;
   const uint64_t block = block_id();
   const uint64_t row = block / tiles;
   if (row >= a.rows) return;
-  const uint32_t base = static_cast<uint32_t>(block - row * tiles) * (kSpan * kUnroll) + threadIdx.x * E;
+  const uint32_t tile = static_cast<uint32_t>(block - row * tiles);
+  const uint32_t base = tile * (kThreads * kUnroll) + threadIdx.x;
   const uint32_t vocab = static_cast<uint32_t>(a.vocab);
   const T* z = static_cast<const T*>(a.logits) + row * a.stride;
   T* dz = static_cast<T*>(a.dlogits) + row * a.dstride;
+  const Cut<T> cut(z, dz, vocab);
+  T* out = dz + cut.head;
+  typename X::type raw[kUnroll];
+#pragma unroll
+  for (int j = 0; j < kUnroll; ++j)
+    if (base + j * kThreads < cut.vectors)
+      raw[j] = load_once<T, E>(cut.middle + static_cast<uint64_t>(base + j * kThreads) * E);
+  const uint32_t one = tile == 0 ? cut.single(threadIdx.x) : 0xffffffffu;
+  const float alone = one < vocab ? static_cast<float>(z[one]) : 0.0f;
   const float lse = a.lse[row];
   const uint64_t tok = token_at(a.tokens, row, a.wide);
   const uint32_t mine = tok < a.vocab ? static_cast<uint32_t>(tok) : 0xffffffffu;  // no element's index
@@ -371,22 +501,23 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs 
   const float h = a.dentropy != nullptr ? a.dentropy[row] : 0.0f;
   const float c = a.dentropy != nullptr ? fmaf(h, a.entropy[row], g) : g;  // dz_j = -p_j (c + h log p_j)
   const bool none = lse == -INFINITY;
-  typename X::type raw[kUnroll];
-#pragma unroll
-  for (int j = 0; j < kUnroll; ++j) raw[j] = load_row<T, E>(z, base + j * kSpan, vocab);
+  auto gradient = [&](float v, uint32_t e) {
+    const float lp = v - lse;
+    const float p = __builtin_amdgcn_exp2f(lp * kLog2e);
+    float d = -p * fmaf(h, fmaxf(lp, kLeast), c);
+    if (mine == e) d += g;
+    return none ? 0.0f : d;
+  };
 #pragma unroll
   for (int j = 0; j < kUnroll; ++j) {
-    const uint32_t e = base + j * kSpan;
+    const uint32_t v = base + j * kThreads;
+    if (v >= cut.vectors) break;
     typename X::wide f = widen<T, E>(raw[j]);
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const float lp = f[i] - lse;
-      const float p = __builtin_amdgcn_exp2f(lp * kLog2e);
-      f[i] = none ? 0.0f : -p * fmaf(h, fmaxf(lp, kLeast), c);
-      if (mine == e + i) f[i] += none ? 0.0f : g;
-    }
-    store_row<T, E>(dz, e, vocab, narrow<T, E>(f));
+    for (int i = 0; i < E; ++i) f[i] = gradient(f[i], cut.head + v * E + i);
+    store_once<T, E>(out + static_cast<uint64_t>(v) * E, narrow<T, E>(f));
   }
+  if (one < vocab) dz[one] = static_cast<T>(gradient(alone, one));
 }
 
 template <class T>

@@ -170,6 +170,9 @@ def token_logprobs(z, tokens, top):
         zb = z.gather(1, best)
         out["top_logprob"] = torch.where(none[:, None], -math.inf, torch.where(bad[:, None], math.nan, zb - lse[:, None]))
         tol["top_logprob"] = safe(r_s + 4 * U * (ln_s.abs() + lse.abs()))[:, None] + 2 * U * safe(zb.abs())
+    # results are fp32: what is past its range is an infinity there
+    most = torch.finfo(torch.float32).max
+    out = {k: torch.where(r.abs() > most, torch.sign(r) * math.inf, r) if r.is_floating_point() else r for k, r in out.items()}
     return out, tol
 
 

@@ -309,7 +309,8 @@ def test_layer_norm_grad_without_rows_and_with_expanded_rows():
 # ------------------------------------------------------------- checkpoints
 @pytest.mark.parametrize("rows,dim,xt,pad", [(1, 1, F32, 0), (3, 31, BF16, 1), (5, 32, F16, 0), (4, 33, F32, 1), (700, 8, BF16, 0),
                                              (33, 100, F32, 0), (9, 511, BF16, 3), (6, 1025, F16, 0), (2, 70003, BF16, 0),
-                                             (300, 4096, BF16, 0)])
+                                             (300, 4096, BF16, 0), (2049, 1030, F32, 1), (700, 6001, BF16, 0), (301, 8000, F16, 3),
+                                             (70001, 33, BF16, 0), (300001, 7, F32, 0), (129, 16400, F32, 0), (2, 8, BF16, 0)])
 def test_checkpoint(rows, dim, xt, pad):
     g = gen(rows + dim)
     x = rand(g, rows, dim, dtype=xt) * torch.exp(torch.randn(rows, 1, generator=g) * 3).to(xt)
@@ -360,6 +361,8 @@ LOGP = [  # rows, vocab, top, type, tokens, pad
     (2, 8191, 3, F16, torch.int64, 0), (2, 8193, 64, BF16, torch.int64, 0), (1, 50021, 20, F32, torch.int64, 0),
     (8, 131072, 8, BF16, torch.int64, 0), (1, 262144, 64, BF16, torch.int32, 0), (1030, 777, 4, BF16, torch.int64, 0),
     (300, 20003, 7, BF16, torch.int64, 1), (1, 600000, 1, F16, torch.int64, 0),
+    (1025, 7, 3, F32, torch.int64, 1), (1024, 4096, 8, F16, torch.int64, 0), (1024, 4093, 0, BF16, torch.int32, 1),
+    (5, 8191, 10, BF16, torch.int64, 5), (2, 16389, 2, F32, torch.int64, 3),
 ]
 
 
@@ -398,6 +401,32 @@ def test_token_logprobs(rows, vocab, top, zt, kt, pad):
         assert pad == 0 or untouched(big, pad, vocab)
     rsx.token_logprobs_grad(zd, td, p.lse, gl.to(DEV), dlogits=zd)
     assert same_bits(zd, dz)
+
+
+@pytest.mark.parametrize("zt", [F32, BF16])
+@pytest.mark.parametrize("vocab,rows", [(9000, 6), (70000, 6), (300, 1200)])
+def test_token_logprobs_far_rows(vocab, rows, zt):
+    """Logits near the ends of the type's range, some of them only in parts of a row; large ones shift nothing."""
+    top = torch.finfo(zt).max
+    z = torch.zeros(rows, vocab, dtype=torch.float64)
+    z[0] = -top
+    z[0, ::2] = -math.inf                             # the lowest beside masked ones
+    z[1, vocab // 3:] = -top                          # whole slices of the lowest
+    z[2] = torch.where(torch.arange(vocab) % 5 == 0, top, -top)
+    z[3] = torch.arange(vocab) % 7 + 2.0 ** 14        # large and close
+    z[4, :vocab // 2] = -math.inf                     # whole slices masked
+    z[5] = torch.randn(vocab, generator=gen(vocab)) * 1e4
+    z = z.to(zt)
+    tok = torch.arange(rows) % 3
+    say("token_logprobs far", vocab, rows, zt)
+    p = rsx.token_logprobs(z.to(DEV), tok.to(DEV), 3)
+    ref, tol = so.token_logprobs(z, tok, 3)
+    for k, r in ref.items():
+        got = getattr(p, k)
+        if k == "top_token":
+            assert torch.equal(got.cpu(), r), k
+        else:
+            so.close(got, r, tol[k] + 1.01 * so.rounding(r, F32), k)
 
 
 @pytest.mark.parametrize("zt", TYPES)
