@@ -114,6 +114,10 @@ constexpr int kBins = 1 << kDigit;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr uint32_t kSmallSort = 8192;  // tokens that one workgroup sorts in its LDS
+constexpr uint32_t kMaxTiles = 64;     // of a larger sort
+// Tokens that are sorted by counting alone, without passes (32 tokens of 1024
+// bf16: 18.1 us by passes, 14.4 so).
+constexpr uint32_t kRankSort = 128;
 
 // Lanes of the wave whose digit equals this lane's, among `valid`.
 __device__ __forceinline__ uint64_t same_digit(uint32_t d, uint64_t valid) {
@@ -183,14 +187,19 @@ __device__ void mark_rows(const EmbedGradArgs& a, uint64_t v0, uint32_t rows, ui
   const uint32_t n = static_cast<uint32_t>(a.n);
   for (uint32_t i = threadIdx.x; i < (rows + 31) / 32; i += kSortThreads) named[i] = 0;
   __syncthreads();
-  constexpr uint32_t kStep = 8 * kSortThreads;
-  for (uint32_t i0 = threadIdx.x; i0 < n; i0 += kStep) {
-    uint64_t r[8];
+  constexpr int kAhead = 8;
+  for (uint32_t i0 = threadIdx.x; i0 < n; i0 += kAhead * kSortThreads) {
+    uint64_t r[kAhead];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = token_row(a.tokens, min(i0 + j * kSortThreads, n - 1), a.first, a.wide) - v0;
+    for (int j = 0; j < kAhead; ++j) r[j] = token_row(a.tokens, min(i0 + j * kSortThreads, n - 1), a.first, a.wide) - v0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (r[j] < rows) atomicOr(&named[r[j] / 32], 1u << (r[j] % 32));
+    for (int j = 0; j < kAhead; ++j) {
+      if (i0 + j * kSortThreads >= n || r[j] >= rows) continue;
+      // A frequent token's mark is there already; setting it again would queue.
+      const uint32_t word = static_cast<uint32_t>(r[j]) / 32, bit = 1u << (r[j] % 32);
+      if ((__hip_atomic_load(&named[word], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) & bit) == 0)
+        atomicOr(&named[word], bit);
+    }
   }
   __syncthreads();
 }
@@ -231,10 +240,34 @@ __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(EmbedGradArgs 
   const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const uint32_t part = ((n + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;  // entries of a wave
   const uint32_t begin = min(wave * part, n), end = min(begin + part, n);
-  for (uint32_t i = threadIdx.x; i < n; i += kSortThreads) {
-    const uint64_t row = token_row(a.tokens, i, a.first, a.wide);
-    key[0][i] = row < a.vocab ? static_cast<uint32_t>(row) : static_cast<uint32_t>(a.vocab);
-    place[0][i] = static_cast<uint16_t>(i);
+  uint64_t rows[kSmallSort / kSortThreads];  // all asked for at once
+#pragma unroll
+  for (uint32_t j = 0; j < kSmallSort / kSortThreads; ++j)
+    rows[j] = token_row(a.tokens, min(threadIdx.x + j * kSortThreads, n - 1), a.first, a.wide);
+#pragma unroll
+  for (uint32_t j = 0; j < kSmallSort / kSortThreads; ++j) {
+    const uint32_t i = threadIdx.x + j * kSortThreads;
+    if (i < n) {
+      key[0][i] = rows[j] < a.vocab ? static_cast<uint32_t>(rows[j]) : static_cast<uint32_t>(a.vocab);
+      place[0][i] = static_cast<uint16_t>(i);
+    }
+  }
+  if (n <= kRankSort) {
+    // An entry's place is the number of entries before it, counted by its thread.
+    __syncthreads();
+    const uint32_t mine = threadIdx.x;
+    if (mine < n) {
+      const uint32_t k = key[0][mine];
+      uint32_t to = 0;
+#pragma unroll 16
+      for (uint32_t j = 0; j < n; ++j) {
+        const uint32_t other = key[0][j];
+        to += other < k || (other == k && j < mine) ? 1u : 0u;
+      }
+      keys[to] = k;
+      places[to] = mine;
+    }
+    return;
   }
   int from = 0;
   for (int shift = 0; shift < bits; shift += kDigit, from ^= 1) {
@@ -313,34 +346,11 @@ __global__ __launch_bounds__(kSortThreads) void sort_move_kernel(EmbedGradArgs a
                                                                  uint32_t tiles, const uint32_t* hist,
                                                                  uint32_t* keys_out, uint32_t* places_out, ZeroPlan z) {
   __shared__ uint32_t counts[kSortWaves][kBins];
-  __shared__ uint32_t base[kBins];
+  __shared__ uint32_t base[2][kBins], sums[kBins];
   __shared__ uint32_t totals[kBins / 64];
   if (block_id() >= tiles) return zero_group<B>(a, z, block_id() - tiles, nullptr);
   const uint32_t n = static_cast<uint32_t>(a.n), t = threadIdx.x;
   const uint32_t lane = t % 64, wave = t / 64;
-  for (uint32_t i = t; i < kSortWaves * kBins; i += kSortThreads) (&counts[0][0])[i] = 0;
-  uint32_t before = 0, total = 0;
-  if (t < kBins) {
-#pragma unroll 8
-    for (uint32_t b = 0; b < tiles; ++b) {
-      const uint32_t c = hist[b * kBins + t];
-      before += b < blockIdx.x ? c : 0u;
-      total += c;
-    }
-  }
-  uint32_t v = total;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint32_t o = __shfl_up(v, d);
-    if (lane >= static_cast<uint32_t>(d)) v += o;
-  }
-  if (t < kBins && lane == 63) totals[wave] = v;
-  __syncthreads();
-  if (t < kBins) {
-    uint32_t start = v - total + before;
-    for (uint32_t w = 0; w < wave; ++w) start += totals[w];
-    base[t] = start;
-  }
   const uint32_t tile_begin = blockIdx.x * tile, tile_end = min(n - tile_begin, tile) + tile_begin;
   const uint32_t part = tile / kSortWaves;  // a multiple of 64
   const uint32_t begin = min(tile_begin + wave * part, tile_end), end = min(begin + part, tile_end);
@@ -349,14 +359,56 @@ __global__ __launch_bounds__(kSortThreads) void sort_move_kernel(EmbedGradArgs a
     const uint64_t row = token_row(a.tokens, i, a.first, a.wide);
     return row < a.vocab ? static_cast<uint32_t>(row) : static_cast<uint32_t>(a.vocab);
   };
-  for (uint32_t i = begin + lane; i < end; i += 64) atomicAdd(&counts[wave][(key_at(i) >> shift) % kBins], 1u);
+  auto place_at = [&](uint32_t i) { return places_in != nullptr ? places_in[i] : i; };
+  // The first 64 entries of each wave, all of them up to 65536 tokens, are
+  // asked for before anything else.
+  const uint32_t first_key = begin + lane < end ? key_at(begin + lane) : 0u;
+  const uint32_t first_place = begin + lane < end ? place_at(begin + lane) : 0u;
+  for (uint32_t i = t; i < kSortWaves * kBins; i += kSortThreads) (&counts[0][0])[i] = 0;
+  // The tiles' counts of a digit, half of them to each half of the workgroup,
+  // all on their way at once.
+  static_assert(kSortThreads == 2 * kBins && kMaxTiles % 2 == 0, "");
+  const uint32_t bin = t % kBins, half = t / kBins;
+  uint32_t c[kMaxTiles / 2];
+#pragma unroll
+  for (uint32_t j = 0; j < kMaxTiles / 2; ++j) {
+    const uint32_t b = half * (kMaxTiles / 2) + j;
+    c[j] = b < tiles ? hist[b * kBins + bin] : 0u;
+  }
+  uint32_t before = 0, total = 0;
+#pragma unroll
+  for (uint32_t j = 0; j < kMaxTiles / 2; ++j) {
+    before += half * (kMaxTiles / 2) + j < blockIdx.x ? c[j] : 0u;
+    total += c[j];
+  }
+  base[half][bin] = before;
+  if (half != 0) sums[bin] = total;
   __syncthreads();
-  scan_counts(counts, totals, base);
+  if (half == 0) total += sums[bin];
+  uint32_t v = total;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t o = __shfl_up(v, d);
+    if (lane >= static_cast<uint32_t>(d)) v += o;
+  }
+  if (half == 0 && lane == 63) totals[wave] = v;
+  __syncthreads();
+  if (half == 0) {
+    uint32_t start = v - total + base[0][t] + base[1][t];
+    for (uint32_t w = 0; w < wave; ++w) start += totals[w];
+    base[0][t] = start;
+  }
+  for (uint32_t i = begin + lane; i < end; i += 64) {
+    const uint32_t k = i < begin + 64 ? first_key : key_at(i);
+    atomicAdd(&counts[wave][(k >> shift) % kBins], 1u);
+  }
+  __syncthreads();
+  scan_counts(counts, totals, base[0]);
   for (uint32_t at = begin; at < end; at += 64) {
     const uint32_t i = at + lane;
     const bool there = i < end;
-    const uint32_t k = there ? key_at(i) : 0u;
-    const uint32_t p = !there ? 0u : places_in != nullptr ? places_in[i] : i;
+    const uint32_t k = at == begin ? first_key : there ? key_at(i) : 0u;
+    const uint32_t p = at == begin ? first_place : there ? place_at(i) : 0u;
     const uint32_t d = (k >> shift) % kBins;
     const uint64_t mates = same_digit(d, __ballot(there));
     const uint32_t rank = lanes_below(mates);
@@ -513,7 +565,8 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(EmbedGradArgs a, const ui
       for (int j = 0; j < kAhead; ++j) {
         const uint32_t i = min(i0 + j, count - 1);
         const uint64_t place = static_cast<uint32_t>(__builtin_amdgcn_readlane(p, i));
-        v[j] = load_row<T, E>(dout + place * a.dout_stride, e, dim);
+        const T* row = dout + place * a.dout_stride;
+        v[j] = dim >= E ? load_in<T, E>(row, e, dim) : load_row<T, E>(row, e, dim);
       }
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
@@ -529,7 +582,7 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(EmbedGradArgs a, const ui
           sum = 0.0f;
         }
         if (run == vocab) return;  // tokens outside the table are last: nothing to sum
-        sum += widen<T, E>(v[j]);
+        sum += widen<T, E>(dim >= E ? in_place<T, E>(v[j], e, dim) : v[j]);
       }
     }
   }
@@ -542,15 +595,15 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(EmbedGradArgs a, const ui
 }
 
 // A run that starts in chunk c and goes on: its tail, then the heads of the
-// following chunks while they begin with its row.  The four waves of a
-// workgroup take a quarter of the chunks each and are added in order.
-template <class U, int E>
-__global__ __launch_bounds__(kThreads) void join_kernel(EmbedGradArgs a, const uint32_t* keys, const float* head,
-                                                        const float* tail, uint32_t chunk, uint32_t columns,
-                                                        uint64_t pitch) {
-  __shared__ float part[kThreads / 64][64 * E];
+// following chunks while they begin with its row.  The K waves of a workgroup
+// take an equal part of the chunks each and are added in order.
+template <class U, int E, int K>
+__global__ __launch_bounds__(K * 64) void join_kernel(EmbedGradArgs a, const uint32_t* keys, const float* head,
+                                                      const float* tail, uint32_t chunk, uint32_t columns,
+                                                      uint64_t pitch) {
+  __shared__ float part[K][64 * E];
   const uint32_t n = static_cast<uint32_t>(a.n), dim = static_cast<uint32_t>(a.dim);
-  const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const uint32_t lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
   const uint64_t block = block_id();
   const uint32_t c = static_cast<uint32_t>(block / columns);
   const uint32_t chunks = (n + chunk - 1) / chunk;
@@ -559,29 +612,39 @@ __global__ __launch_bounds__(kThreads) void join_kernel(EmbedGradArgs a, const u
   const uint32_t run = keys[next - 1];
   // Not a run that goes on, or not one that starts in this chunk.
   if (run == static_cast<uint32_t>(a.vocab) || keys[next] != run || (c != 0 && keys[c * chunk - 1] == run)) return;
-  uint32_t heads = 0;  // chunks after c that begin with the run's row
-  for (;;) {
-    const uint64_t at = static_cast<uint64_t>(c) + 1 + heads + lane;
-    const uint64_t m = __ballot(at < chunks && keys[at < chunks ? at * chunk : 0] == run);
-    const uint32_t more = m == ~0ull ? 64u : static_cast<uint32_t>(__builtin_ctzll(~m));
-    heads += more;
-    if (more < 64) break;
+  // Chunks after c that begin with the run's row: from c + 1 on, a 64-way search.
+  uint32_t lo = c + 1, hi = chunks;  // chunk lo begins with it, chunk hi (if there) does not
+  while (hi - lo > 1) {
+    const uint32_t step = (hi - lo + 63) / 64;
+    const uint64_t at = lo + static_cast<uint64_t>(lane) * step;
+    const uint64_t with = __ballot(at < hi && keys[(at < hi ? at : lo) * chunk] == run);
+    const uint32_t k = static_cast<uint32_t>(__popcll(with));  // at least lane 0
+    hi = static_cast<uint32_t>(min(static_cast<uint64_t>(hi), lo + static_cast<uint64_t>(k) * step));
+    lo += (k - 1) * step;
   }
+  const uint32_t heads = lo - c;
   const uint32_t column = static_cast<uint32_t>(block - static_cast<uint64_t>(c) * columns);
   const uint32_t e = column * (64 * E) + lane * E;
-  const uint32_t quarter = (heads + 3) / 4;
-  const uint32_t begin = min(wave * quarter, heads), end = min(begin + quarter, heads);
+  const uint32_t share = (heads + K - 1) / K;
+  const uint32_t begin = min(wave * share, heads), end = min(begin + share, heads);
   typename Vec<float, E>::type sum = {};
   if (wave == 0) sum = get_part<E>(tail + c * pitch, column);
   const float* h = head + (static_cast<uint64_t>(c) + 1) * pitch;
-#pragma unroll 8
-  for (uint32_t i = begin; i < end; ++i) sum += get_part<E>(h + i * pitch, column);
+  constexpr int kAhead = 8;
+  for (uint32_t i0 = begin; i0 < end; i0 += kAhead) {
+    typename Vec<float, E>::type v[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) v[j] = get_part<E>(h + min(i0 + j, end - 1) * pitch, column);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (i0 + j < end) sum += v[j];
+  }
 #pragma unroll
   for (int i = 0; i < E; ++i) part[wave][lane * E + i] = sum[i];
   __syncthreads();
   if (wave != 0) return;
 #pragma unroll
-  for (int w = 1; w < kThreads / 64; ++w)
+  for (int w = 1; w < K; ++w)
 #pragma unroll
     for (int i = 0; i < E; ++i) sum[i] += part[w][lane * E + i];
   put_sum<U, E>(a, run, e, dim, sum);
@@ -599,17 +662,16 @@ constexpr uint64_t kScanTokens = 1u << 17;
 
 GradPlan grad_plan(uint64_t vocab, uint64_t dim, uint64_t n) {
   GradPlan p;
-  // About 64 tiles, of whole 64-entry steps for each of the 16 waves.
+  // Tiles of whole 64-entry steps for each of the 16 waves.
   const uint64_t unit = kSortThreads;
-  p.tile = static_cast<uint32_t>(((n + 63) / 64 + unit - 1) / unit * unit);
+  p.tile = static_cast<uint32_t>(((n + kMaxTiles - 1) / kMaxTiles + unit - 1) / unit * unit);
   if (p.tile == 0) p.tile = unit;
   p.tiles = static_cast<uint32_t>((n + p.tile - 1) / p.tile);
   // Long chunks have few partial rows, short ones fill the chip: about 4096
-  // waves of 512 columns.  A batch of at most 32 is one chunk and needs no join.
+  // waves of 512 columns.
   const uint64_t columns = (dim + 511) / 512;
   p.chunk = 8;
   while (p.chunk < 128 && n * columns > static_cast<uint64_t>(p.chunk) * 4096) p.chunk *= 2;
-  if (n <= 32) p.chunk = 32;
   p.chunks = static_cast<uint32_t>((n + p.chunk - 1) / p.chunk);
   p.pitch = columns * 512;
   uint64_t at = 0;
@@ -716,8 +778,10 @@ hipError_t grad(const EmbedGradArgs& a, hipStream_t s) {
   const hipError_t e = launch(sum_kernel<T, U>, grid_of(sums + zeros), kThreads, kSumReserve, s, a, keys, places, head, tail, p.chunk,
                               p.chunks, columns, sums, p.pitch, z);
   if (e != hipSuccess || p.chunks < 2) return e;
-  return launch(join_kernel<U, E>, grid_of(static_cast<uint64_t>(p.chunks - 1) * columns), kThreads, 0, s, a, keys, head,
-                tail, p.chunk, columns, p.pitch);
+  // Most workgroups find no run to join: few waves each where they are many.
+  const uint64_t joins = static_cast<uint64_t>(p.chunks - 1) * columns;
+  return joins > 4000 ? launch(join_kernel<U, E, 4>, grid_of(joins), 256, 0, s, a, keys, head, tail, p.chunk, columns, p.pitch)
+                      : launch(join_kernel<U, E, 8>, grid_of(joins), 512, 0, s, a, keys, head, tail, p.chunk, columns, p.pitch);
 }
 
 }  // namespace

@@ -100,6 +100,9 @@ GRAD = [  # n, vocab, dim, dout, grad, tokens, first, kind, accumulate, pad
     (140001, 3001, 24, BF16, F32, torch.int64, 5, "zipf", False, 1), (131073, 520, 9, F32, BF16, torch.int32, 0, "few", False, 0),
     (131072, 5000, 10, F16, F32, torch.int64, -3, "zipf", False, 0), (10, 70000, 2, F32, BF16, torch.int64, 0, "any", False, 0),
     (9001, 600000, 1, BF16, BF16, torch.int64, 0, "zipf", False, 0), (70000, 2000, 1100, BF16, BF16, torch.int64, 0, "zipf", False, 0),
+    (128, 77, 30, F16, F16, torch.int64, 0, "few", False, 0), (129, 77, 30, F16, F16, torch.int64, 0, "few", False, 1),
+    (70001, 3, 30, F32, BF16, torch.int64, 0, "any", False, 0), (30001, 900, 4, BF16, F32, torch.int32, 0, "one", True, 0),
+    (65537, 2 ** 20, 11, BF16, BF16, torch.int64, 0, "zipf", False, 0), (8193, 40000, 3, F16, F16, torch.int64, -7, "any", False, 0),
 ]
 
 
