@@ -505,8 +505,8 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(const float* partial, ui
 // ------------------------------------------------------------ checkpoints
 // A thread has V vectors of 8 elements on their way.  Rows of up to 2048: `lanes`
 // threads to a row (a power of two, at least 4: a block's lanes stay together),
-// the vectors in V rows.  Longer ones: a workgroup to a row's piece, the vectors
-// 2048 elements apart; lanes is 0.
+// the vectors in V rows.  Longer ones are cut into pieces of 2048, a workgroup
+// takes V pieces one after the other, from row to row; lanes is 256.
 struct Place {
   uint64_t row;
   uint32_t e;
@@ -514,15 +514,20 @@ struct Place {
 template <int V>
 __device__ __forceinline__ void pack_places(Place (&p)[V], uint32_t lanes, uint32_t pieces) {
   const uint64_t block = block_id();
-  if (lanes != 0) {
+  if (pieces == 1) {
     const uint32_t rows = kThreads / lanes;
 #pragma unroll
     for (int k = 0; k < V; ++k) p[k] = {(block * V + k) * rows + threadIdx.x / lanes, threadIdx.x % lanes * 8};
   } else {
-    const uint64_t row = block / pieces;
-    const uint32_t piece = static_cast<uint32_t>(block - row * pieces);
+    uint64_t row = block * V / pieces;
+    uint32_t piece = static_cast<uint32_t>(block * V - row * pieces);
 #pragma unroll
-    for (int k = 0; k < V; ++k) p[k] = {row, (piece * V + k) * (kThreads * 8) + threadIdx.x * 8};
+    for (int k = 0; k < V; ++k) {
+      p[k] = {row, piece * (kThreads * 8) + threadIdx.x * 8};
+      const bool last = ++piece == pieces;
+      row += last ? 1 : 0;
+      piece = last ? 0 : piece;
+    }
   }
 }
 
@@ -581,29 +586,20 @@ __global__ __launch_bounds__(kThreads) void unpack_kernel(PackArgs a, uint32_t l
 
 template <class T, int V>
 hipError_t checkpoint_go(const PackArgs& a, bool pack, hipStream_t s) {
-  uint32_t lanes = 0, pieces = 0;
-  uint64_t grid;
-  if (a.dim <= kThreads * 8) {
-    lanes = 4;
-    while (lanes * 8 < a.dim) lanes *= 2;
-    const uint64_t rows = kThreads / lanes * V;
-    grid = (a.rows + rows - 1) / rows;
-  } else {
-    pieces = static_cast<uint32_t>((a.dim + kThreads * 8 * V - 1) / (kThreads * 8 * V));
-    grid = a.rows * pieces;
-  }
-  return launch(pack ? pack_kernel<T, V> : unpack_kernel<T, V>, grid_of(grid), kThreads, 0, s, a, lanes, pieces);
+  uint32_t lanes = 4;
+  while (lanes < kThreads && lanes * 8 < a.dim) lanes *= 2;
+  const uint32_t pieces = static_cast<uint32_t>((a.dim + kThreads * 8 - 1) / (kThreads * 8));
+  const uint64_t rows = kThreads / lanes;  // of one vector of the workgroup; 1 where rows have pieces
+  const uint64_t items = (a.rows + rows - 1) / rows * pieces;
+  return launch(pack ? pack_kernel<T, V> : unpack_kernel<T, V>, grid_of((items + V - 1) / V), kThreads, 0, s, a, lanes,
+                pieces);
 }
 
 template <class T>
 hipError_t checkpoint(const PackArgs& a, bool pack, hipStream_t s) {
-  // As many vectors as the row has (32768 rows of 4096 bf16, both ways: 144 us,
-  // with one 157); one where there is little to do.
-  if (a.rows * a.dim < (1u << 21)) return checkpoint_go<T, 1>(a, pack, s);
-  if (a.dim <= kThreads * 8) return checkpoint_go<T, 4>(a, pack, s);
-  const uint64_t vectors = (a.dim + kThreads * 8 - 1) / (kThreads * 8);
-  return vectors % 4 == 0 ? checkpoint_go<T, 4>(a, pack, s)
-                          : vectors % 3 == 0 ? checkpoint_go<T, 3>(a, pack, s) : checkpoint_go<T, 2>(a, pack, s);
+  // 32768 rows of 4096 bf16, both ways: 138 us, with one vector 157; one where
+  // there is little to do.
+  return a.rows * a.dim < (1u << 21) ? checkpoint_go<T, 1>(a, pack, s) : checkpoint_go<T, 4>(a, pack, s);
 }
 
 // --------------------------------------------------------------- launches

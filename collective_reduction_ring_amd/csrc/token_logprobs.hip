@@ -163,12 +163,14 @@ __device__ __forceinline__ Token row_token(const LogprobArgs& a, uint64_t row) {
 }
 __device__ __forceinline__ float finish_row(const LogprobArgs& a, uint64_t row, const Stats& st, const Token& tok) {
   const bool none = st.s == 0.0f && st.m == -INFINITY;  // every logit masked
-  const float ln_s = logf(st.s);
+  // The maximum's own term is 1 and u is not positive, but for roundings.
+  const float s = st.s < 1.0f ? 1.0f : st.s, t = st.t > 0.0f ? 0.0f : st.t;
+  const float ln_s = logf(s);
   const float lse = none ? -INFINITY : st.m + ln_s;
   // (z - m) - ln s keeps more digits than z - lse where the maximum is large
   a.logprob[row] = !tok.there ? 0.0f : none ? -INFINITY : (tok.z - st.m) - ln_s;
   a.lse[row] = lse;
-  if (a.entropy != nullptr) a.entropy[row] = none ? 0.0f : ln_s - st.t * kLn2 / st.s;
+  if (a.entropy != nullptr) a.entropy[row] = none ? 0.0f : ln_s - t * kLn2 / s;
   return lse;
 }
 

@@ -579,6 +579,20 @@ def test_graph_replays_match_eager_calls():
         assert all(same_bits(a, b) for a, b in zip(got, outs)), turn
 
 
+def test_example_learns_and_its_ranks_agree():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "train_step.py")
+    spec = importlib.util.spec_from_file_location("train_step", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    losses, world = example.train(ranks=3, steps=30, vocab=200, dim=64, tokens=1000)
+    # a model that knows nothing has ln 200 = 5.3; one that has learned the rule has little left
+    assert 4.5 < losses[0] < 7.0 and losses[-1] < 2.0 and losses[-1] < losses[0]
+    for r in world[1:]:
+        assert all(same_bits(p, q) for p, q in zip(r.params, world[0].params))
+
+
 def test_python_refusals():
     x = torch.zeros(4, 8, device=DEV)
     t = torch.zeros(4, dtype=torch.int64, device=DEV)
