@@ -177,18 +177,19 @@ __device__ void scan_counts(uint32_t (*counts)[kBins], uint32_t* totals, const u
 constexpr uint32_t kNamedWords = kSortWaves * kBins;  // marks that a workgroup holds in LDS
 constexpr uint32_t kScanGroup = 1u << 18;  // bytes of a group that scans
 constexpr uint32_t kZeroGroup = 1u << 15;  // bytes of one that does not
+constexpr uint32_t kPlanes = 4;            // sets of marks of the whole table, each from a part of the tokens
 struct ZeroPlan {
-  const uint32_t* named;  // marks of the whole table; null: not there
+  const uint32_t* named;  // marks of the whole table, kPlanes times `words`; null: not there
+  uint64_t words;
   uint32_t rows, lanes;   // rows of a group; lanes that share a row
   uint64_t first, end;    // groups of this launch
 };
-// Marks of rows v0 .. v0 + rows in LDS, from a scan of all tokens.
-__device__ void mark_rows(const EmbedGradArgs& a, uint64_t v0, uint32_t rows, uint32_t* named) {
-  const uint32_t n = static_cast<uint32_t>(a.n);
+// Marks of rows v0 .. v0 + rows in LDS, from a scan of tokens begin .. n.
+__device__ void mark_rows(const EmbedGradArgs& a, uint64_t v0, uint32_t rows, uint32_t* named, uint32_t begin, uint32_t n) {
   for (uint32_t i = threadIdx.x; i < (rows + 31) / 32; i += kSortThreads) named[i] = 0;
   __syncthreads();
   constexpr int kAhead = 8;
-  for (uint32_t i0 = threadIdx.x; i0 < n; i0 += kAhead * kSortThreads) {
+  for (uint32_t i0 = begin + threadIdx.x; i0 < n; i0 += kAhead * kSortThreads) {
     uint64_t r[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) r[j] = token_row(a.tokens, min(i0 + j * kSortThreads, n - 1), a.first, a.wide) - v0;
@@ -205,13 +206,15 @@ __device__ void mark_rows(const EmbedGradArgs& a, uint64_t v0, uint32_t rows, ui
 }
 template <class B>
 __device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, const ZeroPlan& z, uint64_t v0, uint32_t rows,
-                                          const uint32_t* named, uint64_t bit0) {
+                                          const uint32_t* named, uint32_t planes, uint64_t bit0) {
   constexpr int E = 16 / sizeof(B);
   const uint32_t dim = static_cast<uint32_t>(a.dim);
   const typename Vec<B, E>::type zero = {};
   for (uint32_t r = threadIdx.x / z.lanes; r < rows; r += blockDim.x / z.lanes) {
     const uint64_t bit = bit0 + r;
-    if ((named[bit / 32] >> (bit % 32)) & 1u) continue;
+    uint32_t word = named[bit / 32];
+    for (uint32_t p = 1; p < planes; ++p) word |= named[p * z.words + bit / 32];
+    if ((word >> (bit % 32)) & 1u) continue;
     B* g = static_cast<B*>(a.grad) + (v0 + r) * a.grad_stride;
     for (uint32_t e = threadIdx.x % z.lanes * E; e < dim; e += z.lanes * E) store_row<B, E>(g, e, dim, zero);
   }
@@ -222,9 +225,9 @@ __device__ __forceinline__ void zero_group(const EmbedGradArgs& a, const ZeroPla
   const uint64_t group = z.first + block, v0 = group * z.rows;
   if (group >= z.end) return;
   const uint32_t rows = static_cast<uint32_t>(min(static_cast<uint64_t>(z.rows), a.vocab - v0));
-  if (z.named != nullptr) return zero_rows<B>(a, z, v0, rows, z.named, v0);
-  mark_rows(a, v0, rows, lds);
-  zero_rows<B>(a, z, v0, rows, lds, 0);
+  if (z.named != nullptr) return zero_rows<B>(a, z, v0, rows, z.named, kPlanes, v0);
+  mark_rows(a, v0, rows, lds, 0, static_cast<uint32_t>(a.n));
+  zero_rows<B>(a, z, v0, rows, lds, 1, 0);
 }
 
 // The whole sort of at most kSmallSort tokens in one workgroup.
@@ -313,11 +316,13 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(EmbedGradArgs 
   __shared__ uint32_t counts[kNamedWords];
   if (block_id() >= tiles) {
     if (marks == nullptr) return zero_group<B>(a, z, block_id() - tiles, nullptr);
-    const uint64_t v0 = (block_id() - tiles) * marked;
+    const uint32_t plane = static_cast<uint32_t>((block_id() - tiles) % kPlanes);
+    const uint64_t v0 = (block_id() - tiles) / kPlanes * marked;
     if (v0 >= a.vocab) return;
     const uint32_t rows = static_cast<uint32_t>(min(static_cast<uint64_t>(marked), a.vocab - v0));
-    mark_rows(a, v0, rows, counts);
-    for (uint32_t i = threadIdx.x; i < (rows + 31) / 32; i += kSortThreads) marks[v0 / 32 + i] = counts[i];
+    const uint32_t all = static_cast<uint32_t>(a.n), part = (all + kPlanes - 1) / kPlanes;
+    mark_rows(a, v0, rows, counts, plane * part, min((plane + 1) * part, all));
+    for (uint32_t i = threadIdx.x; i < (rows + 31) / 32; i += kSortThreads) marks[plane * z.words + v0 / 32 + i] = counts[i];
     return;
   }
   const uint32_t n = static_cast<uint32_t>(a.n);
@@ -685,7 +690,7 @@ GradPlan grad_plan(uint64_t vocab, uint64_t dim, uint64_t n) {
   p.keys2 = take(n * 4);
   p.places2 = take(n * 4);
   p.hist = take(static_cast<uint64_t>(p.tiles) * kBins * 4);
-  p.marks = take(n > kSmallSort && n <= kScanTokens ? (vocab + 31) / 32 * 4 : 0);
+  p.marks = take(n > kSmallSort && n <= kScanTokens ? (vocab + 31) / 32 * kPlanes * 4 : 0);
   p.head = take(p.chunks * p.pitch * 4);
   p.tail = take(p.chunks * p.pitch * 4);
   p.total = at;
@@ -713,9 +718,9 @@ hipError_t sort(const EmbedGradArgs& a, const GradPlan& p, ZeroPlan* z, hipStrea
   // Marks by one workgroup on each of the CUs that the sort leaves, and 256 KiB
   // of zeros for each, which are about done with the sort's step.
   constexpr uint64_t kBeside = 192;
-  uint64_t marked = ((a.vocab + kBeside - 1) / kBeside + 31) / 32 * 32;
+  uint64_t marked = ((a.vocab * kPlanes + kBeside - 1) / kBeside + 31) / 32 * 32;
   marked = std::min<uint64_t>(marked, kNamedWords * 32);
-  const uint64_t marking = groups != 0 ? (a.vocab + marked - 1) / marked : 0;
+  const uint64_t marking = groups != 0 ? (a.vocab + marked - 1) / marked * kPlanes : 0;
   const uint64_t beside_groups = kBeside * (kScanGroup / kZeroGroup);
   const int passes = (bits + kDigit - 1) / kDigit;
   const uint32_t *kin = nullptr, *pin = nullptr;
@@ -751,7 +756,7 @@ hipError_t grad(const EmbedGradArgs& a, hipStream_t s) {
   const uint32_t* places = reinterpret_cast<const uint32_t*>(ws + p.places);
   float* head = reinterpret_cast<float*>(ws + p.head);
   float* tail = reinterpret_cast<float*>(ws + p.tail);
-  ZeroPlan z = {nullptr, 0, lanes_of(a.dim, 16 / sizeof(U)), 0, 0};
+  ZeroPlan z = {nullptr, (a.vocab + 31) / 32, 0, lanes_of(a.dim, 16 / sizeof(U)), 0, 0};
   uint64_t zeros = 0;  // workgroups beside the sums
   if (!a.accumulate && a.n != 0 && a.n <= kScanTokens) {
     // Where a group scans the tokens by itself, four times what the scan reads
