@@ -115,7 +115,7 @@ __device__ __forceinline__ uint32_t lanes_nth(uint32_t v, uint32_t top) {
 }
 
 // ---------------------------------------------------------------- forward
-constexpr int kUnroll = 4;  // vectors a lane has in flight, and as many on their way
+constexpr int kUnroll = 4;  // vectors of a step, with as many on their way
 
 struct Partial {
   float m, s, t, pad;
@@ -161,17 +161,18 @@ __device__ __forceinline__ Token row_token(const LogprobArgs& a, uint64_t row) {
   const bool there = tok < a.vocab;
   return {there, there ? logit_at(a, row * a.stride + tok) : 0.0f};
 }
-__device__ __forceinline__ float finish_row(const LogprobArgs& a, uint64_t row, const Stats& st, const Token& tok) {
+__device__ __forceinline__ float row_lse_of(const Stats& st) {
+  return st.s == 0.0f && st.m == -INFINITY ? -INFINITY : st.m + logf(st.s < 1.0f ? 1.0f : st.s);
+}
+__device__ __forceinline__ void finish_row(const LogprobArgs& a, uint64_t row, const Stats& st, const Token& tok) {
   const bool none = st.s == 0.0f && st.m == -INFINITY;  // every logit masked
   // The maximum's own term is 1 and u is not positive, but for roundings.
   const float s = st.s < 1.0f ? 1.0f : st.s, t = st.t > 0.0f ? 0.0f : st.t;
   const float ln_s = logf(s);
-  const float lse = none ? -INFINITY : st.m + ln_s;
   // (z - m) - ln s keeps more digits than z - lse where the maximum is large
   a.logprob[row] = !tok.there ? 0.0f : none ? -INFINITY : (tok.z - st.m) - ln_s;
-  a.lse[row] = lse;
+  a.lse[row] = row_lse_of(st);
   if (a.entropy != nullptr) a.entropy[row] = none ? 0.0f : ln_s - t * kLn2 / s;
-  return lse;
 }
 
 // A lane's statistics on the way.  `r` stands for m log2 e, for m of at least
@@ -230,15 +231,15 @@ __device__ __forceinline__ void offer(Best& best, float z, uint32_t index, bool 
 }
 
 // Workgroup (row, slice): the statistics and best candidates of `slice`
-// elements; with one slice to a row, the row's results.  K waves.
-template <class T, bool TOP, int K>
+// elements; with one slice to a row, the row's results.  K waves, steps of U
+// vectors.
+template <class T, bool TOP, int K, int U>
 __global__ __launch_bounds__(K * 64) void logprob_kernel(LogprobArgs a, uint32_t slices, uint32_t slice,
                                                          Partial* partial, uint64_t* best_out) {
   constexpr int E = 16 / sizeof(T);
   typedef Vec<T, E> X;
   __shared__ Stats wave_stats[K];
   __shared__ uint64_t wave_best[TOP ? K * RSX_TOP_MAX : 1];
-  __shared__ float row_lse;
   const uint64_t block = block_id();
   const uint64_t row = block / slices;
   if (row >= a.rows) return;
@@ -257,17 +258,17 @@ __global__ __launch_bounds__(K * 64) void logprob_kernel(LogprobArgs a, uint32_t
   Running st = {-INFINITY, scaled(-INFINITY), 0.0f, 0.0f};
   Best best = {0ull, 0ull, 0ull};
   bool seeded = false;
-  // A step is kUnroll vectors of each lane; those past the end read as masked.
-  constexpr uint32_t kGroup = 64 * kUnroll;
-  typename X::type next[kUnroll];
+  // A step is U vectors of each lane; those past the end read as masked.
+  constexpr uint32_t kGroup = 64 * U;
+  typename X::type next[U];
   auto load = [&](uint32_t base) {
     const T* p = cut.middle + static_cast<uint64_t>(base + lane) * E;
     if (base + kGroup <= cut.vectors) {  // the same for the wave
 #pragma unroll
-      for (int j = 0; j < kUnroll; ++j) next[j] = load_once<T, E>(p + j * 64 * E);
+      for (int j = 0; j < U; ++j) next[j] = load_once<T, E>(p + j * 64 * E);
     } else {
 #pragma unroll
-      for (int j = 0; j < kUnroll; ++j) {
+      for (int j = 0; j < U; ++j) {
         next[j] = static_cast<T>(-INFINITY);
         if (base + j * 64 + lane < cut.vectors) next[j] = load_once<T, E>(p + j * 64 * E);
       }
@@ -276,20 +277,22 @@ __global__ __launch_bounds__(K * 64) void logprob_kernel(LogprobArgs a, uint32_t
   uint32_t base = wave * kGroup;
   if (base < cut.vectors) load(base);
   for (; base < cut.vectors; base += K * kGroup) {
-    typename X::type raw[kUnroll];
+    typename X::type raw[U];
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) raw[j] = next[j];
+    for (int j = 0; j < U; ++j) raw[j] = next[j];
     if (base + K * kGroup < cut.vectors) load(base + K * kGroup);
-    float most = static_cast<float>(raw[0][0]);
+    float highest[U], most = -INFINITY;  // of each vector and of all
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
+    for (int j = 0; j < U; ++j) {
       const typename X::wide f = widen<T, E>(raw[j]);
+      highest[j] = f[0];
 #pragma unroll
-      for (int i = 0; i < E; ++i) most = fmaxf(most, f[i]);
+      for (int i = 1; i < E; ++i) highest[j] = fmaxf(highest[j], f[i]);
+      most = fmaxf(most, highest[j]);
     }
     if (most > st.m) raise(st, most);
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
+    for (int j = 0; j < U; ++j) {
       const typename X::wide f = widen<T, E>(raw[j]);
 #pragma unroll
       for (int i = 0; i < E; ++i) add(st, f[i]);
@@ -311,7 +314,8 @@ __global__ __launch_bounds__(K * 64) void logprob_kernel(LogprobArgs a, uint32_t
       const uint32_t first = begin + cut.head + (base + lane) * E;
       if (nan_passes(best.least) || __ballot(most >= passing(best.least))) {
 #pragma unroll
-        for (int j = 0; j < kUnroll; ++j) {
+        for (int j = 0; j < U; ++j) {
+          if (!nan_passes(best.least) && !__ballot(highest[j] >= passing(best.least))) continue;
           const typename X::wide f = widen<T, E>(raw[j]);
           const bool there = base + j * 64 + lane < cut.vectors;
 #pragma unroll
@@ -350,13 +354,12 @@ __global__ __launch_bounds__(K * 64) void logprob_kernel(LogprobArgs a, uint32_t
   }
   if (threadIdx.x == 0) {
     if (slices == 1)
-      row_lse = finish_row(a, row, all, token);
+      finish_row(a, row, all, token);
     else
       partial[block] = {all.m, all.s, all.t, 0.0f};
   }
   if constexpr (TOP) {
-    __syncthreads();
-    const float lse = row_lse;
+    const float lse = row_lse_of(all);
     // A candidate's rank is the number of larger ones; all are different but
     // for 0, which is none.
     for (uint32_t i = threadIdx.x; i < K * top; i += K * 64) {
@@ -386,68 +389,78 @@ __global__ __launch_bounds__(K * 64) void logprob_kernel(LogprobArgs a, uint32_t
 }
 
 // A row's slices joined in order.
-__global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs a, uint32_t slices, const Partial* partial,
-                                                                const uint64_t* best) {
-  constexpr int kWaves = kThreads / 64;
-  extern __shared__ uint64_t cand[];
-  __shared__ Stats wave_stats[kWaves];
+constexpr int kJoinThreads = 512;
+constexpr uint32_t kMaxSlices = 64;
+constexpr uint32_t kMaxJoin = 1024;  // candidates, each compared with every other
+__global__ __launch_bounds__(kJoinThreads) void logprob_join_kernel(LogprobArgs a, uint32_t slices,
+                                                                    const Partial* partial, const uint64_t* best) {
+  __shared__ uint64_t cand[kMaxJoin];
+  __shared__ uint32_t ranks[kMaxJoin];
   __shared__ float row_lse;
   const uint64_t row = block_id();
   if (row >= a.rows) return;
   const uint32_t top = a.top, n = slices * top;
   Token token = {false, 0.0f};
   if (threadIdx.x == 0) token = row_token(a, row);
-  for (uint32_t i = threadIdx.x; i < n; i += kThreads) cand[i] = best[row * n + i];
   Stats st = {-INFINITY, 0.0f, 0.0f};
-  for (uint32_t i = threadIdx.x; i < slices; i += kThreads) {
-    const Partial p = partial[row * slices + i];
-    st = merge(st, {p.m, p.s, p.t});
+  for (uint32_t i = threadIdx.x; i < n; i += kJoinThreads) {
+    cand[i] = best[row * n + i];
+    ranks[i] = 0;
   }
-  st = wave_merge(st);
-  if (threadIdx.x % 64 == 0) wave_stats[threadIdx.x / 64] = st;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    Stats all = wave_stats[0];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) all = merge(all, wave_stats[w]);
-    row_lse = finish_row(a, row, all, token);
+  if (threadIdx.x < 64) {  // slices <= 64: one wave has them all
+    if (threadIdx.x < slices) {
+      const Partial p = partial[row * slices + threadIdx.x];
+      st = {p.m, p.s, p.t};
+    }
+    st = wave_merge(st);
+    if (threadIdx.x == 0) row_lse = row_lse_of(st);
   }
-  if (top == 0) return;
   __syncthreads();
-  const float lse = row_lse;
-  for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-    const uint64_t c = cand[i];
-    if (c == 0) continue;
+  // A candidate's rank is the number of larger ones, counted in parts.
+  constexpr uint32_t kPart = 64;
+  const uint32_t parts = (n + kPart - 1) / kPart;
+  for (uint32_t i = threadIdx.x; i < n * parts; i += kJoinThreads) {
+    const uint32_t who = i % n, first = i / n * kPart, last = min(first + kPart, n);
+    const uint64_t c = cand[who];
     uint32_t rank = 0;
 #pragma unroll 8
-    for (uint32_t j = 0; j < n; ++j) rank += cand[j] > c ? 1u : 0u;
-    if (rank < top) {
-      a.top_token[row * top + rank] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(c));
-      a.top_logprob[row * top + rank] =
-          lse == -INFINITY ? -INFINITY : order_value(static_cast<uint32_t>(c >> 32)) - lse;
-    }
+    for (uint32_t j = first; j < last; ++j) rank += cand[j] > c ? 1u : 0u;
+    if (rank != 0) atomicAdd(&ranks[who], rank);
   }
+  __syncthreads();
+  const float lse = row_lse;
+  for (uint32_t i = threadIdx.x; i < n; i += kJoinThreads) {
+    const uint64_t c = cand[i];
+    const uint32_t rank = ranks[i];
+    if (c == 0 || rank >= top) continue;
+    a.top_token[row * top + rank] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(c));
+    a.top_logprob[row * top + rank] =
+        lse == -INFINITY ? -INFINITY : order_value(static_cast<uint32_t>(c >> 32)) - lse;
+  }
+  if (threadIdx.x == 0) finish_row(a, row, st, token);  // the token's logit is the last to come
 }
 
 // Slices of a row.  Enough workgroups for the chip, none below one step of its
-// four waves, and no more than the join takes in one go.
-constexpr uint32_t kStepElems = 8192;   // 4 waves * 64 lanes * kUnroll vectors of 8
+// four waves, and no more than the join takes in one go.  Where steps of
+// kUnroll vectors leave CUs idle, half as long ones.
 constexpr uint32_t kWantGroups = 1024;
-constexpr uint32_t kMaxSlices = 64;
-constexpr uint32_t kMaxJoin = 1024;  // candidates, each compared with every other
 struct Slices {
   uint32_t count, length;
+  bool brief;
 };
 Slices slices_of(uint64_t rows, uint64_t vocab, uint32_t top) {
+  uint64_t step = 4 * 64 * kUnroll * 8;  // elements of 16 bits; twice that of fp32
+  const bool brief = rows * ((vocab + step - 1) / step) < kCus;
+  if (brief) step /= 2;
   uint64_t n = rows == 0 ? 1 : (kWantGroups + rows - 1) / rows;
-  const uint64_t most = (vocab + kStepElems - 1) / kStepElems;
+  const uint64_t most = (vocab + step - 1) / step;
   n = n < most ? n : most;
   const uint64_t room = top > kMaxJoin / kMaxSlices ? kMaxJoin / top : kMaxSlices;
   n = n < room ? n : room;
   n = n > 0 ? n : 1;
   uint64_t length = (vocab + n - 1) / n;
-  length = (length + kStepElems - 1) / kStepElems * kStepElems;
-  return {static_cast<uint32_t>((vocab + length - 1) / length), static_cast<uint32_t>(length)};
+  length = (length + step - 1) / step * step;
+  return {static_cast<uint32_t>((vocab + length - 1) / length), static_cast<uint32_t>(length), brief};
 }
 
 // One wave to a row where a wave's step holds most of it and there are rows
@@ -463,13 +476,13 @@ hipError_t logprobs(const LogprobArgs& a, hipStream_t s) {
   uint64_t* best = reinterpret_cast<uint64_t*>(static_cast<char*>(a.ws) + (grid * sizeof(Partial) + 255) / 256 * 256);
   const dim3 g = grid_of(grid);
   if (a.vocab <= kWaveRow && a.rows >= kWaveRows)  // one slice
-    return launch(a.top != 0 ? logprob_kernel<T, true, 1> : logprob_kernel<T, false, 1>, g, 64, 0, s, a, sl.count, sl.length,
-                  partial, best);
-  const hipError_t e = launch(a.top != 0 ? logprob_kernel<T, true, 4> : logprob_kernel<T, false, 4>, g, kThreads, 0, s, a,
-                              sl.count, sl.length, partial, best);
+    return launch(a.top != 0 ? logprob_kernel<T, true, 1, kUnroll> : logprob_kernel<T, false, 1, kUnroll>, g, 64, 0, s, a,
+                  sl.count, sl.length, partial, best);
+  const auto kernel = sl.brief ? (a.top != 0 ? logprob_kernel<T, true, 4, kUnroll / 2> : logprob_kernel<T, false, 4, kUnroll / 2>)
+                               : (a.top != 0 ? logprob_kernel<T, true, 4, kUnroll> : logprob_kernel<T, false, 4, kUnroll>);
+  const hipError_t e = launch(kernel, g, kThreads, 0, s, a, sl.count, sl.length, partial, best);
   if (e != hipSuccess || sl.count == 1) return e;
-  return launch(logprob_join_kernel, grid_of(a.rows), kThreads, sl.count * a.top * sizeof(uint64_t), s, a, sl.count,
-                partial, best);
+  return launch(logprob_join_kernel, grid_of(a.rows), kJoinThreads, 0, s, a, sl.count, partial, best);
 }
 
 // --------------------------------------------------------------- gradient
