@@ -175,13 +175,14 @@ __device__ void scan_counts(uint32_t (*counts)[kBins], uint32_t* totals, const u
 // stores, so each hides the other.  A workgroup takes a group of `rows` rows;
 // those that a token names are marked as bits of `named`.
 constexpr uint32_t kNamedWords = kSortWaves * kBins;  // marks that a workgroup holds in LDS
-constexpr uint32_t kScanGroup = 1u << 18;  // bytes of a group that scans
+constexpr uint32_t kScanGroup = 3u << 17;  // bytes of a group that scans, about
 constexpr uint32_t kZeroGroup = 1u << 15;  // bytes of one that does not
 constexpr uint32_t kPlanes = 4;            // sets of marks of the whole table, each from a part of the tokens
 struct ZeroPlan {
   const uint32_t* named;  // marks of the whole table, kPlanes times `words`; null: not there
   uint64_t words;
   uint32_t rows, lanes;   // rows of a group; lanes that share a row
+  uint32_t magic;         // 2^32 / dim + 1 of a table without gaps, else 0
   uint64_t first, end;    // groups of this launch
 };
 // Marks of rows v0 .. v0 + rows in LDS, from a scan of tokens begin .. n.
@@ -219,6 +220,36 @@ __device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, const ZeroPlan
     for (uint32_t e = threadIdx.x % z.lanes * E; e < dim; e += z.lanes * E) store_row<B, E>(g, e, dim, zero);
   }
 }
+// The same of a table without gaps, as one run of 16-byte vectors: rows of any
+// width fill every lane and every cache line.
+template <class B>
+__device__ __forceinline__ void zero_run(const EmbedGradArgs& a, const ZeroPlan& z, uint64_t v0, uint32_t rows,
+                                         const uint32_t* named) {
+  constexpr uint32_t E = 16 / sizeof(B);
+  const uint32_t dim = static_cast<uint32_t>(a.dim), n = rows * dim;
+  B* g = static_cast<B*>(a.grad) + v0 * a.dim;
+  auto row_of = [&](uint32_t e) {
+    uint32_t r = __umulhi(e, z.magic);  // the row, or one more
+    if (r * dim > e) --r;
+    return r;
+  };
+  auto is_named = [&](uint32_t r) { return (named[r / 32] >> (r % 32)) & 1u; };
+  const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(g) / sizeof(B)) % E;
+  const typename Vec<B, static_cast<int>(E)>::type zero = {};
+  for (uint32_t q = threadIdx.x; q * E < n + off; q += blockDim.x) {
+    const uint32_t e = q * E - off;  // wraps before the run
+    const uint32_t first = q * E < off ? 0u : e, last = min(e + E, n);  // elements of this vector
+    uint32_t r = row_of(first);
+    uint32_t some = is_named(r);
+    for (uint32_t end = (r + 1) * dim; end < last && some == 0; end += dim) some = is_named(++r);
+    if (some == 0 && last - first == E) {
+      store_once<B, static_cast<int>(E)>(g + e, zero);
+    } else {
+      for (uint32_t i = first; i < last; ++i)
+        if (!is_named(row_of(i))) g[i] = static_cast<B>(0);
+    }
+  }
+}
 // Group z.first + block, from the marks of the table or, without, of its own.
 template <class B>
 __device__ __forceinline__ void zero_group(const EmbedGradArgs& a, const ZeroPlan& z, uint64_t block, uint32_t* lds) {
@@ -227,7 +258,34 @@ __device__ __forceinline__ void zero_group(const EmbedGradArgs& a, const ZeroPla
   const uint32_t rows = static_cast<uint32_t>(min(static_cast<uint64_t>(z.rows), a.vocab - v0));
   if (z.named != nullptr) return zero_rows<B>(a, z, v0, rows, z.named, kPlanes, v0);
   mark_rows(a, v0, rows, lds, 0, static_cast<uint32_t>(a.n));
+  if (z.magic != 0) return zero_run<B>(a, z, v0, rows, lds);
   zero_rows<B>(a, z, v0, rows, lds, 1, 0);
+}
+
+// The whole sort of at most kRankSort tokens in one workgroup: an entry's place
+// is the number of entries before it, counted by its thread.
+template <class B>
+__global__ __launch_bounds__(kSortThreads) void sort_rank_kernel(EmbedGradArgs a, uint32_t* keys, uint32_t* places,
+                                                                 ZeroPlan z) {
+  __shared__ uint32_t key[kRankSort];
+  __shared__ uint32_t named[kNamedWords];
+  if (block_id() != 0) return zero_group<B>(a, z, block_id() - 1, named);
+  const uint32_t n = static_cast<uint32_t>(a.n), mine = threadIdx.x;
+  if (mine < n) {
+    const uint64_t row = token_row(a.tokens, mine, a.first, a.wide);
+    key[mine] = row < a.vocab ? static_cast<uint32_t>(row) : static_cast<uint32_t>(a.vocab);
+  }
+  __syncthreads();
+  if (mine >= n) return;
+  const uint32_t k = key[mine];
+  uint32_t to = 0;
+#pragma unroll 16
+  for (uint32_t j = 0; j < n; ++j) {
+    const uint32_t other = key[j];
+    to += other < k || (other == k && j < mine) ? 1u : 0u;
+  }
+  keys[to] = k;
+  places[to] = mine;
 }
 
 // The whole sort of at most kSmallSort tokens in one workgroup.
@@ -254,23 +312,6 @@ __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(EmbedGradArgs 
       key[0][i] = rows[j] < a.vocab ? static_cast<uint32_t>(rows[j]) : static_cast<uint32_t>(a.vocab);
       place[0][i] = static_cast<uint16_t>(i);
     }
-  }
-  if (n <= kRankSort) {
-    // An entry's place is the number of entries before it, counted by its thread.
-    __syncthreads();
-    const uint32_t mine = threadIdx.x;
-    if (mine < n) {
-      const uint32_t k = key[0][mine];
-      uint32_t to = 0;
-#pragma unroll 16
-      for (uint32_t j = 0; j < n; ++j) {
-        const uint32_t other = key[0][j];
-        to += other < k || (other == k && j < mine) ? 1u : 0u;
-      }
-      keys[to] = k;
-      places[to] = mine;
-    }
-    return;
   }
   int from = 0;
   for (int shift = 0; shift < bits; shift += kDigit, from ^= 1) {
@@ -713,6 +754,7 @@ hipError_t sort(const EmbedGradArgs& a, const GradPlan& p, ZeroPlan* z, hipStrea
   const uint64_t groups = z->rows != 0 ? (a.vocab + z->rows - 1) / z->rows : 0;
   if (a.n <= kSmallSort) {
     z->end = groups;
+    if (a.n <= kRankSort) return launch(sort_rank_kernel<B>, grid_of(1 + groups), kSortThreads, 0, s, a, keys, places, *z);
     return launch(sort_small_kernel<B>, grid_of(1 + groups), kSortThreads, 0, s, a, bits, keys, places, *z);
   }
   // Marks by one workgroup on each of the CUs that the sort leaves, and 256 KiB
@@ -721,7 +763,7 @@ hipError_t sort(const EmbedGradArgs& a, const GradPlan& p, ZeroPlan* z, hipStrea
   uint64_t marked = ((a.vocab * kPlanes + kBeside - 1) / kBeside + 31) / 32 * 32;
   marked = std::min<uint64_t>(marked, kNamedWords * 32);
   const uint64_t marking = groups != 0 ? (a.vocab + marked - 1) / marked * kPlanes : 0;
-  const uint64_t beside_groups = kBeside * (kScanGroup / kZeroGroup);
+  const uint64_t beside_groups = kBeside * 8;
   const int passes = (bits + kDigit - 1) / kDigit;
   const uint32_t *kin = nullptr, *pin = nullptr;
   uint32_t *kout = passes % 2 ? keys : keys2, *pout = passes % 2 ? places : places2;
@@ -756,14 +798,24 @@ hipError_t grad(const EmbedGradArgs& a, hipStream_t s) {
   const uint32_t* places = reinterpret_cast<const uint32_t*>(ws + p.places);
   float* head = reinterpret_cast<float*>(ws + p.head);
   float* tail = reinterpret_cast<float*>(ws + p.tail);
-  ZeroPlan z = {nullptr, (a.vocab + 31) / 32, 0, lanes_of(a.dim, 16 / sizeof(U)), 0, 0};
+  ZeroPlan z = {nullptr, (a.vocab + 31) / 32, 0, lanes_of(a.dim, 16 / sizeof(U)), 0, 0, 0};
   uint64_t zeros = 0;  // workgroups beside the sums
   if (!a.accumulate && a.n != 0 && a.n <= kScanTokens) {
-    // Where a group scans the tokens by itself, four times what the scan reads
-    // at most.  Else short: groups of 32 KiB sweep the table in order, groups of
-    // 256 KiB are 2048 places that are written at once (336 and 353 us for the
-    // gradient of 65536 rows of 4096 bf16 in a table of 131072).
-    const uint64_t rows = (a.n <= kSmallSort ? kScanGroup : kZeroGroup) / (a.dim * sizeof(U));
+    // Where a group scans the tokens by itself, rounds of a workgroup to each CU
+    // (two of the least sort's) but the sort's own, all of one size, of about
+    // kScanGroup.  Else short: groups of 32 KiB sweep the table in order, groups
+    // of 256 KiB are 2048 places that are written at once (336 and 353 us for
+    // the gradient of 65536 rows of 4096 bf16 in a table of 131072).
+    const uint64_t row_bytes = a.dim * sizeof(U);
+    uint64_t rows = kZeroGroup / row_bytes;
+    if (a.n <= kSmallSort) {
+      const uint64_t slots = (a.n <= kRankSort ? 2 * kCus : kCus) - 1;
+      const uint64_t rounds = (a.vocab * row_bytes + slots * kScanGroup - 1) / (slots * kScanGroup);
+      rows = (a.vocab + slots * rounds - 1) / (slots * rounds);
+      // runs of less than 2^31 elements; rows of many lanes are as good by row
+      if (a.grad_stride == a.dim && row_bytes < 4096) z.magic = static_cast<uint32_t>((1ull << 32) / a.dim + 1);
+      if (a.dim == 1) z.magic = 0;
+    }
     z.rows = static_cast<uint32_t>(std::max<uint64_t>(1, std::min<uint64_t>(rows, kNamedWords * 32)));
   } else if (!a.accumulate) {
     zeros = (a.vocab + kZeroRows - 1) / kZeroRows;

@@ -103,6 +103,9 @@ GRAD = [  # n, vocab, dim, dout, grad, tokens, first, kind, accumulate, pad
     (128, 77, 30, F16, F16, torch.int64, 0, "few", False, 0), (129, 77, 30, F16, F16, torch.int64, 0, "few", False, 1),
     (70001, 3, 30, F32, BF16, torch.int64, 0, "any", False, 0), (30001, 900, 4, BF16, F32, torch.int32, 0, "one", True, 0),
     (65537, 2 ** 20, 11, BF16, BF16, torch.int64, 0, "zipf", False, 0), (8193, 40000, 3, F16, F16, torch.int64, -7, "any", False, 0),
+    (5568, 32831, 66, BF16, BF16, torch.int64, 0, "zipf", False, 0), (124, 25216, 507, BF16, BF16, torch.int64, 0, "any", False, 0),
+    (3, 72576, 263, F16, F32, torch.int64, 0, "any", False, 0), (20, 5001, 7, F16, F16, torch.int32, 0, "any", False, 0),
+    (700, 900, 3, F32, F32, torch.int64, 0, "any", False, 0), (129, 100001, 1, BF16, BF16, torch.int64, 0, "any", False, 0),
 ]
 
 
@@ -139,6 +142,20 @@ def test_embedding_grad(n, vocab, dim, dt, gt, kt, first, kind, acc, pad):
     grad.copy_(old)
     plan()
     assert same_bits(once, grad)  # one order of the sums
+
+
+@pytest.mark.parametrize("shift", [1, 3, 7])
+@pytest.mark.parametrize("n,vocab,dim,gt", [(50, 3001, 33, BF16), (50, 3001, 33, F32), (900, 700, 5, F16), (9000, 20001, 9, BF16)])
+def test_embedding_grad_of_a_table_off_its_boundary(n, vocab, dim, gt, shift):
+    g = gen(n + shift)
+    flat = torch.full((vocab * dim + 16,), math.nan, dtype=gt, device=DEV)
+    grad = flat[shift:shift + vocab * dim].view(vocab, dim)
+    d, tok = rand(g, n, dim), torch.randint(0, vocab, (n,), generator=g)
+    say("embedding_grad off a boundary", n, vocab, dim, gt, shift)
+    rsx.embedding_grad(d.to(DEV), tok.to(DEV), grad)
+    ref, tol = so.embedding_grad(d, tok, vocab, 1.0, 0)
+    so.close(grad, ref, tol + 1.01 * so.rounding(ref, gt), "grad")
+    assert torch.isnan(flat[:shift]).all() and torch.isnan(flat[shift + vocab * dim:]).all()
 
 
 def test_embedding_grad_rows_beyond_32_bits():
