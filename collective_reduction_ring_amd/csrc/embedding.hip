@@ -55,10 +55,12 @@ __global__ __launch_bounds__(kThreads) void lookup_kernel(EmbedArgs a, uint32_t 
     const T* src = static_cast<const T*>(a.table) + row * a.table_stride;
     // Kept: frequent tokens' rows are read again from the caches.
 #pragma unroll
-    for (int j = 0; j < V; ++j) v[j] = load_row<T, E, false>(src, base + j * 64 * E, dim);
+    for (int j = 0; j < V; ++j) v[j] = load_wide<T, E, false>(src, base + j * 64 * E, dim);
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      store_row<U, E>(out, base + j * 64 * E, dim, narrow<U, E>(widen<T, E>(v[j]) * a.scale));
+    for (int j = 0; j < V; ++j) {
+      const uint32_t e = base + j * 64 * E;
+      store_row<U, E>(out, e, dim, narrow<U, E>(widen<T, E>(wide_in_place<T, E>(v[j], e, dim)) * a.scale));
+    }
   } else {
     const typename Vec<U, E>::type zero = {};
 #pragma unroll
@@ -77,8 +79,10 @@ __global__ __launch_bounds__(kThreads) void lookup_narrow_kernel(EmbedArgs a, ui
   if (i >= a.n || e >= dim) return;
   const uint64_t row = token_row(a.tokens, i, a.first, a.wide);
   typename Vec<T, E>::wide f = 0.0f;
-  if (row < a.vocab)
-    f = widen<T, E>(load_row<T, E, false>(static_cast<const T*>(a.table) + row * a.table_stride, e, dim)) * a.scale;
+  if (row < a.vocab) {
+    const T* src = static_cast<const T*>(a.table) + row * a.table_stride;
+    f = widen<T, E>(dim >= E ? load_pair<T, E>(src, e, dim) : load_row<T, E, false>(src, e, dim)) * a.scale;
+  }
   store_row<U, E>(static_cast<U*>(a.out) + i * a.out_stride, e, dim, narrow<U, E>(f));
 }
 
@@ -95,7 +99,11 @@ hipError_t lookup(const EmbedArgs& a, hipStream_t s) {
   const uint32_t lanes = lanes_of(a.dim, 16 / sizeof(U));
   if (lanes < 64)
     return launch(lookup_narrow_kernel<T, U>, grid_of((a.n * lanes + kThreads - 1) / kThreads), kThreads, 0, s, a, lanes);
-  return a.n * a.dim < (1u << 22) ? lookup_go<T, U, 1>(a, s) : lookup_go<T, U, 4>(a, s);
+  // No more vectors than the row has (65536 rows of 300 bf16: 15 us, with four
+  // 24); one where there is little to do.
+  constexpr uint64_t kSpan = 64 * (16 / sizeof(U));
+  if (a.n * a.dim < (1u << 22) || a.dim <= kSpan) return lookup_go<T, U, 1>(a, s);
+  return a.dim <= 2 * kSpan ? lookup_go<T, U, 2>(a, s) : lookup_go<T, U, 4>(a, s);
 }
 
 // ------------------------------------------------------------------- sort
