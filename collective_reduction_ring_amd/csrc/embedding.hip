@@ -137,9 +137,6 @@ __device__ __forceinline__ uint64_t same_digit(uint32_t d, uint64_t valid) {
   }
   return m;
 }
-__device__ __forceinline__ uint32_t lanes_below(uint64_t m) {
-  return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(m >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(m), 0));
-}
 
 // Exclusive scan over (digit, wave) of counts[wave][digit] in place, on top of
 // `base` for each digit (null: none); every thread of the workgroup calls it.

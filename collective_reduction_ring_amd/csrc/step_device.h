@@ -198,6 +198,10 @@ __device__ __forceinline__ uint32_t uniform(uint32_t v) {
 __device__ __forceinline__ uint64_t uniform64(uint64_t v) {
   return (static_cast<uint64_t>(uniform(static_cast<uint32_t>(v >> 32))) << 32) | uniform(static_cast<uint32_t>(v));
 }
+// Set bits of m below this lane's.
+__device__ __forceinline__ uint32_t lanes_below(uint64_t m) {
+  return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(m >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(m), 0));
+}
 // Which of the rows of a workgroup, G lanes each, is this lane's.
 template <int G, int K>
 __device__ __forceinline__ uint32_t sub_row() {

@@ -486,6 +486,27 @@ def test_token_logprobs_special_rows(vocab, zt):
     so.close(dz[fine], rz, tz + 1.01 * so.rounding(rz, zt), "dlogits")
 
 
+@pytest.mark.parametrize("zt", [F32, F16])
+@pytest.mark.parametrize("rows,vocab,top", [(3, 30001, 64), (4, 2000, 17), (1100, 1500, 33), (2, 200000, 16)])
+def test_alternatives_among_equals_and_rising_rows(rows, vocab, top, zt):
+    g = gen(vocab)
+    z = torch.randint(0, 4, (rows, vocab), generator=g).float()   # thousands of equals
+    z[0] = torch.arange(vocab) / 64                                # each step beats the last (in fp16 with equals)
+    z[1] = -z[0]
+    z[2 % rows, ::3] = -math.inf
+    z = z.to(zt)
+    tok = torch.zeros(rows, dtype=torch.int64)
+    say("alternatives", rows, vocab, top, zt)
+    p = rsx.token_logprobs(z.to(DEV), tok.to(DEV), top)
+    ref, tol = so.token_logprobs(z, tok, top)
+    assert torch.equal(p.top_token.cpu(), ref["top_token"])
+    so.close(p.top_logprob, ref["top_logprob"], tol["top_logprob"] + 1.01 * so.rounding(ref["top_logprob"], F32))
+    z[:, 5:9] = math.nan                                           # NaNs come last, and few numbers before them
+    z[:, top // 2 + 9:] = math.nan
+    p = rsx.token_logprobs(z.to(DEV), tok.to(DEV), top)
+    assert torch.equal(p.top_token.cpu(), so.token_logprobs(z, tok, top)[0]["top_token"])
+
+
 def test_token_logprobs_grad_against_differences():
     g = gen(4)
     z = torch.randn(3, 11, generator=g)
