@@ -182,6 +182,11 @@ __device__ void scan_counts(uint32_t (*counts)[kBins], uint32_t* totals, const u
 constexpr uint32_t kNamedWords = kSortWaves * kBins;  // marks that a workgroup holds in LDS
 constexpr uint32_t kScanGroup = 3u << 17;  // bytes of a group that scans, about
 constexpr uint32_t kZeroGroup = 1u << 15;  // bytes of one that does not
+// Bytes that a small sort has time for, about, and the joins; the rest is
+// zeroed beside the sums (8192 rows of 1024 into 50000 fp32 rows: all of it
+// beside the sort 52 us, so 50).
+constexpr uint64_t kSortZeros = 128000000;
+constexpr uint64_t kJoinZeros = 24000000;
 constexpr uint32_t kPlanes = 4;            // sets of marks of the whole table, each from a part of the tokens
 struct ZeroPlan {
   const uint32_t* named;  // marks of the whole table, kPlanes times `words`; null: not there
@@ -482,7 +487,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_move_kernel(EmbedGradArgs a
 // goes to head[chunk], the first part of one that goes on to tail[chunk];
 // join_kernel adds a run's tail and the heads after it, in order.  So a
 // frequent token is spread over many waves and the order of its sum is fixed.
-constexpr uint32_t kZeroRows = 64;
+constexpr uint32_t kZeroRows = 64;  // most rows of a group that reads its marks off the sorted entries
 
 // LDS that a workgroup of the sums reserves and does not use: four to a CU
 // leave the memory's pages in better order than eight (330 and 336 us, for the
@@ -509,37 +514,46 @@ __device__ __forceinline__ uint32_t first_at_least(const uint32_t* keys, uint32_
   return lo;
 }
 
-// The same for more tokens than a scan for the marks is worth: which of the
-// rows v0 .. v0 + 63 are named is read off the sorted entries from the first
-// at or past v0, a workgroup's width at a time; where one row fills that
-// width, on to the next.
+// Zeros once the entries are sorted, without marks of the table: which of the
+// rows v0 .. v0 + rows are named is read off the entries from the first at or
+// past v0, a workgroup's width at a time; where one row fills that width, on
+// to the next.
+struct SortedZeros {
+  uint64_t first, end;  // rows of this launch
+  uint32_t rows;        // of a workgroup, at most kZeroRows
+};
+inline uint64_t zero_blocks(const SortedZeros& z) { return (z.end - z.first + z.rows - 1) / z.rows; }
 template <class U>
-__device__ void zero_sorted_rows(const EmbedGradArgs& a, const uint32_t* keys, uint64_t first_row) {
-  constexpr int E = 16 / sizeof(U);
-  __shared__ uint32_t named[kZeroRows];
-  if (first_row >= a.vocab) return;
-  const uint32_t n = static_cast<uint32_t>(a.n), dim = static_cast<uint32_t>(a.dim);
-  const uint32_t v0 = static_cast<uint32_t>(first_row);
+__device__ void zero_sorted_rows(const EmbedGradArgs& a, const uint32_t* keys, const ZeroPlan& plan, const SortedZeros& z,
+                                 uint64_t block) {
+  __shared__ uint32_t named[kZeroRows / 32];
+  const uint64_t first_row = z.first + block * z.rows;
+  if (first_row >= z.end) return;
+  const uint32_t rows = static_cast<uint32_t>(min(static_cast<uint64_t>(z.rows), z.end - first_row));
+  const uint32_t n = static_cast<uint32_t>(a.n), v0 = static_cast<uint32_t>(first_row);
   uint32_t at = first_at_least(keys, 0, n, v0);
-  if (threadIdx.x < kZeroRows) named[threadIdx.x] = 0;
+  if (threadIdx.x < kZeroRows / 32) named[threadIdx.x] = 0;
   __syncthreads();
   while (at < n) {  // the same for the whole workgroup
     const uint32_t i = at + threadIdx.x;
     const uint32_t k = i < n ? keys[i] : kNoKey;
-    if (k - v0 < kZeroRows) named[k - v0] = 1;
-    const uint32_t last = at + kThreads - 1;
+    if (k - v0 < rows) atomicOr(&named[(k - v0) / 32], 1u << ((k - v0) % 32));
+    const uint32_t last = at + blockDim.x - 1;
     if (last >= n) break;
     const uint32_t kl = keys[last];
-    if (kl - v0 >= kZeroRows) break;
+    if (kl - v0 >= rows) break;
     at = kl == keys[at] ? first_at_least(keys, last, n, kl + 1) : last + 1;
   }
   __syncthreads();
-  const typename Vec<U, E>::type zero = {};
-  for (uint32_t r = threadIdx.x / 64; r < kZeroRows && v0 + r < a.vocab; r += kThreads / 64) {
-    if (named[r]) continue;
-    U* g = static_cast<U*>(a.grad) + (v0 + r) * a.grad_stride;
-    for (uint32_t e = threadIdx.x % 64 * E; e < dim; e += 64 * E) store_row<U, E>(g, e, dim, zero);
-  }
+  if (plan.magic != 0) return zero_run<U>(a, plan, first_row, rows, named);
+  zero_rows<U>(a, plan, first_row, rows, named, 1, 0);
+}
+// The zeros of a launch beside its own work, from marks or without.
+template <class U>
+__device__ __forceinline__ void zeros_beside(const EmbedGradArgs& a, const uint32_t* keys, const ZeroPlan& z,
+                                             const SortedZeros& sorted, uint64_t block) {
+  if (z.named != nullptr) return zero_group<U>(a, z, block, nullptr);
+  zero_sorted_rows<U>(a, keys, z, sorted, block);
 }
 
 template <class U, int E>
@@ -581,13 +595,10 @@ template <class T, class U>
 __global__ __launch_bounds__(kThreads) void sum_kernel(EmbedGradArgs a, const uint32_t* keys, const uint32_t* places,
                                                        float* head, float* tail, uint32_t chunk, uint32_t chunks,
                                                        uint32_t columns, uint64_t sum_groups, uint64_t pitch,
-                                                       ZeroPlan z) {
+                                                       ZeroPlan z, SortedZeros sorted) {
   constexpr int E = kVector<T, U>;
   const uint64_t block = block_id();
-  if (block >= sum_groups) {
-    if (z.named != nullptr) return zero_group<U>(a, z, block - sum_groups, nullptr);
-    return zero_sorted_rows<U>(a, keys, (block - sum_groups) * kZeroRows);
-  }
+  if (block >= sum_groups) return zeros_beside<U>(a, keys, z, sorted, block - sum_groups);
   const uint32_t n = static_cast<uint32_t>(a.n), dim = static_cast<uint32_t>(a.dim);
   const uint32_t lane = threadIdx.x % 64;
   const uint64_t item = uniform64(block * (kThreads / 64) + threadIdx.x / 64);
@@ -651,14 +662,14 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(EmbedGradArgs a, const ui
 template <class U, int E, int K>
 __global__ __launch_bounds__(K * 64) void join_kernel(EmbedGradArgs a, const uint32_t* keys, const float* head,
                                                       const float* tail, uint32_t chunk, uint32_t columns,
-                                                      uint64_t pitch) {
+                                                      uint64_t pitch, uint64_t joins, ZeroPlan z, SortedZeros sorted) {
   __shared__ float part[K][64 * E];
   const uint32_t n = static_cast<uint32_t>(a.n), dim = static_cast<uint32_t>(a.dim);
   const uint32_t lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
   const uint64_t block = block_id();
+  if (block >= joins) return zeros_beside<U>(a, keys, z, sorted, block - joins);
   const uint32_t c = static_cast<uint32_t>(block / columns);
   const uint32_t chunks = (n + chunk - 1) / chunk;
-  if (block / columns >= chunks - 1) return;  // the last chunk starts no run that goes on
   const uint32_t next = (c + 1) * chunk;
   const uint32_t run = keys[next - 1];
   // Not a run that goes on, or not one that starts in this chunk.
@@ -758,7 +769,8 @@ hipError_t sort(const EmbedGradArgs& a, const GradPlan& p, ZeroPlan* z, hipStrea
   while (bits < 32 && (a.vocab >> bits) != 0) ++bits;  // rows run up to `vocab` itself
   const uint64_t groups = z->rows != 0 ? (a.vocab + z->rows - 1) / z->rows : 0;
   if (a.n <= kSmallSort) {
-    z->end = groups;
+    // as many as are done with the sort; the rest beside the sums and the joins
+    z->end = std::min(groups, (kSortZeros + a.dim * sizeof(B) * z->rows) / (a.dim * sizeof(B) * std::max(z->rows, 1u)));
     if (a.n <= kRankSort) return launch(sort_rank_kernel<B>, grid_of(1 + groups), kSortThreads, 0, s, a, keys, places, *z);
     return launch(sort_small_kernel<B>, grid_of(1 + groups), kSortThreads, 0, s, a, bits, keys, places, *z);
   }
@@ -804,46 +816,63 @@ hipError_t grad(const EmbedGradArgs& a, hipStream_t s) {
   float* head = reinterpret_cast<float*>(ws + p.head);
   float* tail = reinterpret_cast<float*>(ws + p.tail);
   ZeroPlan z = {nullptr, (a.vocab + 31) / 32, 0, lanes_of(a.dim, 16 / sizeof(U)), 0, 0, 0};
-  uint64_t zeros = 0;  // workgroups beside the sums
+  const uint64_t row_bytes = a.dim * sizeof(U);
+  const bool small = a.n <= kSmallSort;
+  // Runs of less than 2^31 elements, with few named rows in between; rows of
+  // many lanes are as good by row.
+  if (small && a.grad_stride == a.dim && a.dim != 1 && row_bytes < 4096) z.magic = static_cast<uint32_t>((1ull << 32) / a.dim + 1);
   if (!a.accumulate && a.n != 0 && a.n <= kScanTokens) {
     // Where a group scans the tokens by itself, rounds of a workgroup to each CU
     // (two of the least sort's) but the sort's own, all of one size, of about
     // kScanGroup.  Else short: groups of 32 KiB sweep the table in order, groups
     // of 256 KiB are 2048 places that are written at once (336 and 353 us for
     // the gradient of 65536 rows of 4096 bf16 in a table of 131072).
-    const uint64_t row_bytes = a.dim * sizeof(U);
     uint64_t rows = kZeroGroup / row_bytes;
-    if (a.n <= kSmallSort) {
+    if (small) {
       const uint64_t slots = (a.n <= kRankSort ? 2 * kCus : kCus) - 1;
-      const uint64_t rounds = (a.vocab * row_bytes + slots * kScanGroup - 1) / (slots * kScanGroup);
-      rows = (a.vocab + slots * rounds - 1) / (slots * rounds);
-      // runs of less than 2^31 elements; rows of many lanes are as good by row
-      if (a.grad_stride == a.dim && row_bytes < 4096) z.magic = static_cast<uint32_t>((1ull << 32) / a.dim + 1);
-      if (a.dim == 1) z.magic = 0;
+      const uint64_t bytes = std::min<uint64_t>(a.vocab * row_bytes, kSortZeros);
+      const uint64_t rounds = (bytes + slots * kScanGroup - 1) / (slots * kScanGroup);
+      rows = (bytes / row_bytes + slots * rounds - 1) / (slots * rounds);
     }
     z.rows = static_cast<uint32_t>(std::max<uint64_t>(1, std::min<uint64_t>(rows, kNamedWords * 32)));
-  } else if (!a.accumulate) {
-    zeros = (a.vocab + kZeroRows - 1) / kZeroRows;
   }
   if (a.n != 0) {
     const hipError_t e = sizeof(U) == 4 ? sort<uint32_t>(a, p, &z, s) : sort<uint16_t>(a, p, &z, s);
     if (e != hipSuccess) return e;
-    if (z.rows != 0) {
-      z.first = z.end;
-      z.end = (a.vocab + z.rows - 1) / z.rows;
-      zeros = z.end - z.first;
-    }
   }
   const uint32_t columns = static_cast<uint32_t>((a.dim + 64 * E - 1) / (64 * E));
   const uint64_t sums = (static_cast<uint64_t>(p.chunks) * columns + kThreads / 64 - 1) / (kThreads / 64);
+  const uint64_t joins = p.chunks < 2 ? 0 : static_cast<uint64_t>(p.chunks - 1) * columns;
+  // What the sort has left of the zeros: beside the joins what is done with
+  // them, the other beside the sums.
+  uint64_t zeros = 0, last_zeros = 0;  // workgroups
+  ZeroPlan last_z = z;
+  SortedZeros sorted = {0, 0, static_cast<uint32_t>(std::max<uint64_t>(1, std::min<uint64_t>(kZeroRows, 2 * kZeroGroup / row_bytes)))};
+  SortedZeros last_sorted = sorted;
+  if (z.named != nullptr) {
+    const uint64_t groups = (a.vocab + z.rows - 1) / z.rows;
+    z.first = z.end;
+    z.end = groups - (joins != 0 ? std::min<uint64_t>(groups - z.first, kJoinZeros / kZeroGroup) : 0);
+    last_z.first = z.end;
+    last_z.end = groups;
+    zeros = z.end - z.first;
+    last_zeros = last_z.end - last_z.first;
+  } else if (!a.accumulate) {
+    sorted.first = std::min<uint64_t>(a.vocab, z.end * z.rows);
+    sorted.end = a.vocab - (joins != 0 ? std::min<uint64_t>(a.vocab - sorted.first, kJoinZeros / row_bytes) : 0);
+    last_sorted.first = sorted.end;
+    last_sorted.end = a.vocab;
+    zeros = zero_blocks(sorted);
+    last_zeros = zero_blocks(last_sorted);
+  }
   if (sums + zeros == 0) return hipSuccess;
   const hipError_t e = launch(sum_kernel<T, U>, grid_of(sums + zeros), kThreads, kSumReserve, s, a, keys, places, head, tail, p.chunk,
-                              p.chunks, columns, sums, p.pitch, z);
-  if (e != hipSuccess || p.chunks < 2) return e;
+                              p.chunks, columns, sums, p.pitch, z, sorted);
+  if (e != hipSuccess || joins == 0) return e;
   // Most workgroups find no run to join: few waves each where they are many.
-  const uint64_t joins = static_cast<uint64_t>(p.chunks - 1) * columns;
-  return joins > 4000 ? launch(join_kernel<U, E, 4>, grid_of(joins), 256, 0, s, a, keys, head, tail, p.chunk, columns, p.pitch)
-                      : launch(join_kernel<U, E, 8>, grid_of(joins), 512, 0, s, a, keys, head, tail, p.chunk, columns, p.pitch);
+  const auto join = joins > 4000 ? join_kernel<U, E, 4> : join_kernel<U, E, 8>;
+  return launch(join, grid_of(joins + last_zeros), joins > 4000 ? 256u : 512u, 0, s, a, keys, head, tail, p.chunk, columns,
+                p.pitch, joins, last_z, last_sorted);
 }
 
 }  // namespace
