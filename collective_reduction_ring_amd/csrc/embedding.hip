@@ -123,9 +123,6 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr uint32_t kSmallSort = 8192;  // tokens that one workgroup sorts in its LDS
 constexpr uint32_t kMaxTiles = 64;     // of a larger sort
-// Tokens that are sorted by counting alone, without passes (32 tokens of 1024
-// bf16: 18.1 us by passes, 14.4 so).
-constexpr uint32_t kRankSort = 128;
 
 // Lanes of the wave whose digit equals this lane's, among `valid`.
 __device__ __forceinline__ uint64_t same_digit(uint32_t d, uint64_t valid) {
@@ -270,32 +267,6 @@ __device__ __forceinline__ void zero_group(const EmbedGradArgs& a, const ZeroPla
   mark_rows(a, v0, rows, lds, 0, static_cast<uint32_t>(a.n));
   if (z.magic != 0) return zero_run<B>(a, z, v0, rows, lds);
   zero_rows<B>(a, z, v0, rows, lds, 1, 0);
-}
-
-// The whole sort of at most kRankSort tokens in one workgroup: an entry's place
-// is the number of entries before it, counted by its thread.
-template <class B>
-__global__ __launch_bounds__(kSortThreads) void sort_rank_kernel(EmbedGradArgs a, uint32_t* keys, uint32_t* places,
-                                                                 ZeroPlan z) {
-  __shared__ uint32_t key[kRankSort];
-  __shared__ uint32_t named[kNamedWords];
-  if (block_id() != 0) return zero_group<B>(a, z, block_id() - 1, named);
-  const uint32_t n = static_cast<uint32_t>(a.n), mine = threadIdx.x;
-  if (mine < n) {
-    const uint64_t row = token_row(a.tokens, mine, a.first, a.wide);
-    key[mine] = row < a.vocab ? static_cast<uint32_t>(row) : static_cast<uint32_t>(a.vocab);
-  }
-  __syncthreads();
-  if (mine >= n) return;
-  const uint32_t k = key[mine];
-  uint32_t to = 0;
-#pragma unroll 16
-  for (uint32_t j = 0; j < n; ++j) {
-    const uint32_t other = key[j];
-    to += other < k || (other == k && j < mine) ? 1u : 0u;
-  }
-  keys[to] = k;
-  places[to] = mine;
 }
 
 // The whole sort of at most kSmallSort tokens in one workgroup.
@@ -712,6 +683,118 @@ __global__ __launch_bounds__(K * 64) void join_kernel(EmbedGradArgs a, const uin
   put_sum<U, E>(a, run, e, dim, sum);
 }
 
+// Few tokens need no sort, and one launch does it all: a workgroup takes token
+// i and 64 * E columns, and is done if an earlier token names the same row;
+// else it sums the rows of i and of the later tokens with that row, in fp32.
+// Each wave has 64 of the tokens, and the waves are added in order.  Further
+// workgroups zero rows, marked from the same tokens.  Bound by the one launch
+// and its waits: a token, its row, the store.  Against the sort, the sums and
+// the joins, bf16: 250 tokens of 64 columns 5.5 us, so 16.2; 500 of 512 6.8 and
+// 16.5; 500 of 1024 into 32000 rows 16.9 and 23.6; 500 times one token of 1024
+// 11.1 and 15.0.  Every workgroup looks at every token, so that many tokens or
+// columns are better sorted: 1000 of 1024 took 41.4 and 24.7, 500 of 4096 20.4
+// and 18.1 (32000 waves), 500 of 2048 12.7 and 16.7 (16000).
+constexpr uint32_t kDirect = 512;
+constexpr uint64_t kDirectWaves = 1u << 14;  // most waves
+constexpr uint32_t kDirectRows = 2048;  // most rows of a group of zeros
+constexpr int kDirectAhead = 16;        // rows in flight
+
+// Adds the rows of the first N tokens in `set`, counted from `base`, and takes
+// them out of it.
+template <class T, int E, int N>
+__device__ __forceinline__ void add_rows(const T* dout, uint64_t stride, uint32_t base, uint64_t* set, uint32_t e,
+                                         uint32_t dim, typename Vec<float, E>::type* sum) {
+  typename Vec<T, E>::type v[N];
+  uint64_t left = *set;
+  uint32_t i = 0;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    if (left != 0) i = static_cast<uint32_t>(__builtin_ctzll(left));
+    left &= left - 1;  // of 0: 0
+    v[j] = load_in<T, E>(dout + (base + i) * stride, e, dim);
+  }
+  // Each load is issued before the first is waited for: without this the
+  // compiler moves one to its use, behind the test, and they wait in turn.
+  typedef uint32_t Words __attribute__((ext_vector_type(sizeof(T) * E / 4)));
+#pragma unroll
+  for (int j = 0; j < N; ++j) v[j] = __builtin_bit_cast(typename Vec<T, E>::type, fresh(__builtin_bit_cast(Words, v[j])));
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    if (*set == 0) break;
+    *set &= *set - 1;
+    *sum += widen<T, E>(in_place<T, E>(v[j], e, dim));
+  }
+}
+
+template <class T, class U>
+__global__ __launch_bounds__(kDirect) void direct_kernel(EmbedGradArgs a, uint32_t columns, uint64_t sums, ZeroPlan z) {
+  constexpr int E = kVector<T, U>;
+  typedef typename Vec<float, E>::type Sum;
+  __shared__ uint32_t key[kDirect];
+  __shared__ uint32_t named[kDirectRows / 32];
+  extern __shared__ __attribute__((aligned(16))) char lds[];  // a sum of each thread
+  Sum* part = reinterpret_cast<Sum*>(lds);
+  const uint32_t n = static_cast<uint32_t>(a.n), dim = static_cast<uint32_t>(a.dim);
+  const uint32_t vocab = static_cast<uint32_t>(a.vocab);
+  const uint64_t block = block_id();
+  for (uint32_t i = threadIdx.x; i < n; i += blockDim.x) {
+    const uint64_t row = token_row(a.tokens, i, a.first, a.wide);
+    key[i] = row < vocab ? static_cast<uint32_t>(row) : vocab;
+  }
+  if (block >= sums) {
+    const uint64_t first_row = (block - sums) * z.rows;
+    const uint32_t rows = first_row < vocab ? static_cast<uint32_t>(min(static_cast<uint64_t>(z.rows), vocab - first_row)) : 0u;
+    const uint32_t v0 = static_cast<uint32_t>(first_row);
+    for (uint32_t i = threadIdx.x; i < kDirectRows / 32; i += blockDim.x) named[i] = 0;
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < n; i += blockDim.x)
+      if (key[i] - v0 < rows) atomicOr(&named[(key[i] - v0) / 32], 1u << ((key[i] - v0) % 32));
+    __syncthreads();
+    if (rows == 0) return;
+    if (z.magic != 0) return zero_run<U>(a, z, first_row, rows, named);
+    return zero_rows<U>(a, z, first_row, rows, named, 1, 0);
+  }
+  __syncthreads();
+  const uint32_t lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
+  const uint32_t mine = static_cast<uint32_t>(block / columns);
+  const uint32_t e = static_cast<uint32_t>(block - static_cast<uint64_t>(mine) * columns) * (64 * E) + lane * E;
+  const uint32_t run = uniform(key[mine]);
+  if (run == vocab) return;
+  auto same = [&](uint32_t base) { return __ballot(base + lane < n && key[min(base + lane, n - 1)] == run); };
+  uint32_t waves = 0;  // that have such tokens
+  for (uint32_t base = 0; base < n; base += 64) {
+    const uint64_t set = same(base);
+    if (set == 0) continue;
+    // The first of them all: the same test in every wave.
+    if (waves == 0 && base + static_cast<uint32_t>(__builtin_ctzll(set)) < mine) return;
+    waves |= 1u << (base / 64);
+  }
+  Sum sum = {};
+  const T* dout = static_cast<const T*>(a.dout);
+  const uint32_t base = wave * 64;
+  uint64_t set = same(base);
+  if (dim < E) {
+    for (; set != 0; set &= set - 1)
+      sum += widen<T, E>(load_row<T, E>(dout + (base + static_cast<uint32_t>(__builtin_ctzll(set))) * a.dout_stride, e, dim));
+  }
+  while (set != 0) {
+    if ((set & (set - 1)) == 0) {
+      add_rows<T, E, 1>(dout, a.dout_stride, base, &set, e, dim, &sum);
+    } else {
+      add_rows<T, E, kDirectAhead>(dout, a.dout_stride, base, &set, e, dim, &sum);
+    }
+  }
+  if ((waves & (waves - 1)) != 0) {
+    part[threadIdx.x] = sum;
+    __syncthreads();
+    if (wave != 0) return;
+    for (uint32_t w = 1; w < blockDim.x / 64; ++w) sum += part[w * 64 + lane];  // zeros where it has none
+  } else if ((waves >> wave) != 1) {
+    return;
+  }
+  put_sum<U, E>(a, run, e, dim, sum);
+}
+
 // Sizes of the sort and of the sums, the same for the workspace and the launch.
 struct GradPlan {
   uint32_t tile, tiles;    // sort
@@ -771,7 +854,6 @@ hipError_t sort(const EmbedGradArgs& a, const GradPlan& p, ZeroPlan* z, hipStrea
   if (a.n <= kSmallSort) {
     // as many as are done with the sort; the rest beside the sums and the joins
     z->end = std::min(groups, (kSortZeros + a.dim * sizeof(B) * z->rows) / (a.dim * sizeof(B) * std::max(z->rows, 1u)));
-    if (a.n <= kRankSort) return launch(sort_rank_kernel<B>, grid_of(1 + groups), kSortThreads, 0, s, a, keys, places, *z);
     return launch(sort_small_kernel<B>, grid_of(1 + groups), kSortThreads, 0, s, a, bits, keys, places, *z);
   }
   // Marks by one workgroup on each of the CUs that the sort leaves, and 256 KiB
@@ -809,38 +891,49 @@ hipError_t sort(const EmbedGradArgs& a, const GradPlan& p, ZeroPlan* z, hipStrea
 template <class T, class U>
 hipError_t grad(const EmbedGradArgs& a, hipStream_t s) {
   constexpr int E = kVector<T, U>;
+  const uint32_t columns = static_cast<uint32_t>((a.dim + 64 * E - 1) / (64 * E));
+  const uint64_t row_bytes = a.dim * sizeof(U);
+  const bool small = a.n <= kSmallSort;
+  // The direct sums' waves: one to 64 tokens, at least four.
+  const uint64_t waves = std::max<uint64_t>(4, (a.n + 63) / 64);
+  const bool direct = a.n <= kDirect && a.n * columns * waves <= kDirectWaves;
+  ZeroPlan z = {nullptr, (a.vocab + 31) / 32, 0, lanes_of(a.dim, 16 / sizeof(U)), 0, 0, 0};
+  // Runs of less than 2^31 elements, with few named rows in between; rows of
+  // many lanes are as good by row, unless a group has few of them.
+  if (small && a.grad_stride == a.dim && a.dim != 1 && (row_bytes < 4096 || direct))
+    z.magic = static_cast<uint32_t>((1ull << 32) / a.dim + 1);
+  if (direct) {
+    // Groups of zeros of up to 32 KiB, of small tables less.
+    const uint64_t bytes = std::min<uint64_t>(kZeroGroup, std::max<uint64_t>(4096, a.vocab * row_bytes / 2048));
+    z.rows = static_cast<uint32_t>(std::max<uint64_t>(1, std::min<uint64_t>(bytes / row_bytes, kDirectRows)));
+    const uint64_t sums = a.n * columns, groups = a.accumulate ? 0 : (a.vocab + z.rows - 1) / z.rows;
+    if (sums + groups == 0) return hipSuccess;
+    const uint32_t threads = static_cast<uint32_t>(waves) * 64;
+    return launch(direct_kernel<T, U>, grid_of(sums + groups), threads, threads * E * 4, s, a, columns, sums, z);
+  }
   const GradPlan p = grad_plan(a.vocab, a.dim, a.n);
   char* ws = static_cast<char*>(a.ws);
   const uint32_t* keys = reinterpret_cast<const uint32_t*>(ws + p.keys);
   const uint32_t* places = reinterpret_cast<const uint32_t*>(ws + p.places);
   float* head = reinterpret_cast<float*>(ws + p.head);
   float* tail = reinterpret_cast<float*>(ws + p.tail);
-  ZeroPlan z = {nullptr, (a.vocab + 31) / 32, 0, lanes_of(a.dim, 16 / sizeof(U)), 0, 0, 0};
-  const uint64_t row_bytes = a.dim * sizeof(U);
-  const bool small = a.n <= kSmallSort;
-  // Runs of less than 2^31 elements, with few named rows in between; rows of
-  // many lanes are as good by row.
-  if (small && a.grad_stride == a.dim && a.dim != 1 && row_bytes < 4096) z.magic = static_cast<uint32_t>((1ull << 32) / a.dim + 1);
-  if (!a.accumulate && a.n != 0 && a.n <= kScanTokens) {
+  if (!a.accumulate && a.n <= kScanTokens) {
     // Where a group scans the tokens by itself, rounds of a workgroup to each CU
-    // (two of the least sort's) but the sort's own, all of one size, of about
-    // kScanGroup.  Else short: groups of 32 KiB sweep the table in order, groups
-    // of 256 KiB are 2048 places that are written at once (336 and 353 us for
-    // the gradient of 65536 rows of 4096 bf16 in a table of 131072).
+    // but the sort's own, all of one size, of about kScanGroup.  Else short:
+    // groups of 32 KiB sweep the table in order, groups of 256 KiB are 2048
+    // places that are written at once (336 and 353 us for the gradient of 65536
+    // rows of 4096 bf16 in a table of 131072).
     uint64_t rows = kZeroGroup / row_bytes;
     if (small) {
-      const uint64_t slots = (a.n <= kRankSort ? 2 * kCus : kCus) - 1;
+      const uint64_t slots = kCus - 1;
       const uint64_t bytes = std::min<uint64_t>(a.vocab * row_bytes, kSortZeros);
       const uint64_t rounds = (bytes + slots * kScanGroup - 1) / (slots * kScanGroup);
       rows = (bytes / row_bytes + slots * rounds - 1) / (slots * rounds);
     }
     z.rows = static_cast<uint32_t>(std::max<uint64_t>(1, std::min<uint64_t>(rows, kNamedWords * 32)));
   }
-  if (a.n != 0) {
-    const hipError_t e = sizeof(U) == 4 ? sort<uint32_t>(a, p, &z, s) : sort<uint16_t>(a, p, &z, s);
-    if (e != hipSuccess) return e;
-  }
-  const uint32_t columns = static_cast<uint32_t>((a.dim + 64 * E - 1) / (64 * E));
+  const hipError_t sorting = sizeof(U) == 4 ? sort<uint32_t>(a, p, &z, s) : sort<uint16_t>(a, p, &z, s);
+  if (sorting != hipSuccess) return sorting;
   const uint64_t sums = (static_cast<uint64_t>(p.chunks) * columns + kThreads / 64 - 1) / (kThreads / 64);
   const uint64_t joins = p.chunks < 2 ? 0 : static_cast<uint64_t>(p.chunks - 1) * columns;
   // What the sort has left of the zeros: beside the joins what is done with
@@ -865,7 +958,6 @@ hipError_t grad(const EmbedGradArgs& a, hipStream_t s) {
     zeros = zero_blocks(sorted);
     last_zeros = zero_blocks(last_sorted);
   }
-  if (sums + zeros == 0) return hipSuccess;
   const hipError_t e = launch(sum_kernel<T, U>, grid_of(sums + zeros), kThreads, kSumReserve, s, a, keys, places, head, tail, p.chunk,
                               p.chunks, columns, sums, p.pitch, z, sorted);
   if (e != hipSuccess || joins == 0) return e;
@@ -900,6 +992,7 @@ hipError_t launch_embedding(const EmbedArgs& a, hipStream_t s) {
   }
 }
 
+// Of few tokens too, which use none: the rule that callers see has no step in it.
 uint64_t embedding_grad_ws(uint64_t vocab, uint64_t dim, uint64_t n) { return grad_plan(vocab, dim, n).total; }
 
 hipError_t launch_embedding_grad(const EmbedGradArgs& a, hipStream_t s) {

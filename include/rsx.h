@@ -419,8 +419,8 @@ rsx_status_t rsx_embedding(const void* table, size_t table_stride, size_t vocab,
 /*
  * Gradient of rsx_embedding in its table:
  * grad[v] = (accumulate ? grad[v] : 0) + scale * sum of dout[i] over the i
- * with tokens[i] - first = v.  The tokens are sorted, so that a row's sum is
- * taken in the order of its positions, in chunks.  Without `accumulate` every
+ * with tokens[i] - first = v.  A row's sum is taken in the order of its
+ * positions, in parts: many tokens are sorted for it.  Without `accumulate` every
  * row is written, with it only the rows that occur.
  */
 size_t rsx_embedding_grad_workspace_size(size_t ntokens, size_t vocab, size_t dim);

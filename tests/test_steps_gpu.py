@@ -106,6 +106,15 @@ GRAD = [  # n, vocab, dim, dout, grad, tokens, first, kind, accumulate, pad
     (5568, 32831, 66, BF16, BF16, torch.int64, 0, "zipf", False, 0), (124, 25216, 507, BF16, BF16, torch.int64, 0, "any", False, 0),
     (3, 72576, 263, F16, F32, torch.int64, 0, "any", False, 0), (20, 5001, 7, F16, F16, torch.int32, 0, "any", False, 0),
     (700, 900, 3, F32, F32, torch.int64, 0, "any", False, 0), (129, 100001, 1, BF16, BF16, torch.int64, 0, "any", False, 0),
+    (512, 700, 300, BF16, BF16, torch.int64, 0, "zipf", False, 0), (513, 700, 300, BF16, BF16, torch.int64, 0, "zipf", False, 0),
+    (512, 1, 1030, F16, F32, torch.int64, 0, "one", False, 0), (257, 9, 8200, BF16, BF16, torch.int32, 0, "few", False, 1),
+    (511, 3000, 5, F32, F16, torch.int64, 9, "few", True, 3), (512, 40, 4100, F32, F32, torch.int64, 0, "one", True, 0),
+    (64, 300, 2, BF16, F32, torch.int64, 0, "one", False, 1), (65, 20, 515, BF16, F32, torch.int64, 0, "sorted", False, 0),
+    (400, 65, 77, BF16, BF16, torch.int64, 0, "outside", False, 0), (0, 3000, 33, F32, BF16, torch.int64, 0, "any", False, 1),
+    (321, 40000, 16, BF16, F32, torch.int32, -4, "zipf", False, 0), (7, 600000, 16, F32, F32, torch.int64, 0, "any", False, 0),
+    (2, 3, 40000, F32, F32, torch.int64, 0, "any", False, 0), (512, 90, 2048, BF16, BF16, torch.int64, 0, "zipf", False, 0),
+    (512, 90, 2049, BF16, BF16, torch.int64, 0, "zipf", False, 0), (160, 70, 9001, BF16, F32, torch.int64, 0, "any", False, 0),
+    (520, 65, 40, BF16, BF16, torch.int64, 0, "outside", False, 0),
 ]
 
 
