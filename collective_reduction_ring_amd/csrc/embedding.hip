@@ -21,6 +21,19 @@ __device__ __forceinline__ uint64_t token_row(const void* tokens, uint64_t i, in
 __device__ __forceinline__ uint64_t token_row(const void* tokens, uint64_t i, int64_t first, int wide) {
   return wide ? token_row<int64_t>(tokens, i, first) : token_row<int32_t>(tokens, i, first);
 }
+// Rows of tokens i, i + step, ..., all asked for at once: with the test of
+// `wide` around each, those of 4 bytes would be waited for in turn.  Past `last`: of that.
+template <int N>
+__device__ __forceinline__ void token_rows(const void* tokens, uint32_t i, uint32_t step, uint32_t last, int64_t first,
+                                           int wide, uint64_t (&rows)[N]) {
+  if (wide) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) rows[j] = token_row<int64_t>(tokens, min(i + j * step, last), first);
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) rows[j] = token_row<int32_t>(tokens, min(i + j * step, last), first);
+  }
+}
 
 // Elements of a vector of the gradient: 16 bytes of the wider type, so that
 // each of a wave's accesses covers one unbroken span on either side.
@@ -124,15 +137,19 @@ constexpr int kSortWaves = kSortThreads / 64;
 constexpr uint32_t kSmallSort = 8192;  // tokens that one workgroup sorts in its LDS
 constexpr uint32_t kMaxTiles = 64;     // of a larger sort
 
-// Lanes of the wave whose digit equals this lane's, among `valid`.
+// Lanes of the wave whose digit equals this lane's, among `valid`.  Sign masks
+// and compares by hand take 4 instructions a bit (plain shifts and selects
+// become 11), and these are most of what a sort in one workgroup runs.
 __device__ __forceinline__ uint64_t same_digit(uint32_t d, uint64_t valid) {
-  uint64_t m = valid;
+  uint32_t lo = static_cast<uint32_t>(valid), hi = static_cast<uint32_t>(valid >> 32);
 #pragma unroll
   for (int b = 0; b < kDigit; ++b) {
-    const uint64_t set = __ballot((d >> b) & 1u);
-    m &= ((d >> b) & 1u) ? set : ~set;
+    const uint32_t bit = static_cast<uint32_t>(__builtin_amdgcn_sbfe(static_cast<int>(d), b, 1));  // 0 or all ones
+    const uint64_t set = __builtin_amdgcn_uicmp(bit, 0u, 33);                                     // lanes where it is not 0
+    lo &= ~(static_cast<uint32_t>(set) ^ bit);
+    hi &= ~(static_cast<uint32_t>(set >> 32) ^ bit);
   }
-  return m;
+  return (static_cast<uint64_t>(hi) << 32) | lo;
 }
 
 // Exclusive scan over (digit, wave) of counts[wave][digit] in place, on top of
@@ -199,8 +216,9 @@ __device__ void mark_rows(const EmbedGradArgs& a, uint64_t v0, uint32_t rows, ui
   constexpr int kAhead = 8;
   for (uint32_t i0 = begin + threadIdx.x; i0 < n; i0 += kAhead * kSortThreads) {
     uint64_t r[kAhead];
+    token_rows(a.tokens, i0, kSortThreads, n - 1, a.first, a.wide, r);
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) r[j] = token_row(a.tokens, min(i0 + j * kSortThreads, n - 1), a.first, a.wide) - v0;
+    for (int j = 0; j < kAhead; ++j) r[j] -= v0;
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (i0 + j * kSortThreads >= n || r[j] >= rows) continue;
@@ -282,10 +300,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(EmbedGradArgs 
   const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const uint32_t part = ((n + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;  // entries of a wave
   const uint32_t begin = min(wave * part, n), end = min(begin + part, n);
-  uint64_t rows[kSmallSort / kSortThreads];  // all asked for at once
-#pragma unroll
-  for (uint32_t j = 0; j < kSmallSort / kSortThreads; ++j)
-    rows[j] = token_row(a.tokens, min(threadIdx.x + j * kSortThreads, n - 1), a.first, a.wide);
+  uint64_t rows[kSmallSort / kSortThreads];
+  token_rows(a.tokens, threadIdx.x, kSortThreads, n - 1, a.first, a.wide, rows);
 #pragma unroll
   for (uint32_t j = 0; j < kSmallSort / kSortThreads; ++j) {
     const uint32_t i = threadIdx.x + j * kSortThreads;
