@@ -129,7 +129,7 @@ hipError_t lookup(const EmbedArgs& a, hipStream_t s) {
 // its rows by digit; a scan over (digit, wave) turns the counts into each
 // wave's first place for each digit; then every wave takes its part 64
 // entries at a time, and an entry's place is the digit's next place plus the
-// number of earlier lanes with that digit, found by one ballot per bit.
+// number of earlier lanes with that digit, found by one compare per bit.
 constexpr int kDigit = 9;
 constexpr int kBins = 1 << kDigit;
 constexpr int kSortThreads = 1024;
@@ -287,58 +287,69 @@ __device__ __forceinline__ void zero_group(const EmbedGradArgs& a, const ZeroPla
   zero_rows<B>(a, z, v0, rows, lds, 1, 0);
 }
 
-// The whole sort of at most kSmallSort tokens in one workgroup.
+// The whole sort of at most kSmallSort tokens in one workgroup.  A lane has its
+// 8 entries in registers; they are counted and ranked in one go, an entry's
+// rank in its wave being its digit's count so far (8000 tokens of a vocabulary
+// of 30000, two passes: 17.0 us, counted by atomics first 19.3; one pass for a
+// vocabulary of 500: 13.3 and 11.7).  Bound by the instructions of one CU.
 template <class B>
 __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(EmbedGradArgs a, int bits, uint32_t* keys,
                                                                   uint32_t* places, ZeroPlan z) {
-  __shared__ uint32_t key[2][kSmallSort];
-  __shared__ uint16_t place[2][kSmallSort];
+  constexpr uint32_t kMine = kSmallSort / kSortThreads;
+  __shared__ uint32_t key[kSmallSort];
+  __shared__ uint16_t place[kSmallSort];
   __shared__ uint32_t counts[kSortWaves][kBins];
   __shared__ uint32_t totals[kBins / 64];
   if (block_id() != 0) return zero_group<B>(a, z, block_id() - 1, &counts[0][0]);
   const uint32_t n = static_cast<uint32_t>(a.n);
-  const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const uint32_t part = ((n + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;  // entries of a wave
+  const uint32_t lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
+  const uint32_t part = ((n + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;  // entries of a wave, at most 64 * kMine
   const uint32_t begin = min(wave * part, n), end = min(begin + part, n);
-  uint64_t rows[kSmallSort / kSortThreads];
-  token_rows(a.tokens, threadIdx.x, kSortThreads, n - 1, a.first, a.wide, rows);
+  uint64_t rows[kMine];
+  token_rows(a.tokens, begin + lane, 64, n - 1, a.first, a.wide, rows);
+  uint32_t k[kMine], p[kMine], rank[kMine];
 #pragma unroll
-  for (uint32_t j = 0; j < kSmallSort / kSortThreads; ++j) {
-    const uint32_t i = threadIdx.x + j * kSortThreads;
-    if (i < n) {
-      key[0][i] = rows[j] < a.vocab ? static_cast<uint32_t>(rows[j]) : static_cast<uint32_t>(a.vocab);
-      place[0][i] = static_cast<uint16_t>(i);
-    }
+  for (uint32_t j = 0; j < kMine; ++j) {
+    k[j] = rows[j] < a.vocab ? static_cast<uint32_t>(rows[j]) : static_cast<uint32_t>(a.vocab);
+    p[j] = begin + j * 64 + lane;
   }
-  int from = 0;
-  for (int shift = 0; shift < bits; shift += kDigit, from ^= 1) {
-    for (uint32_t i = threadIdx.x; i < kSortWaves * kBins; i += kSortThreads) (&counts[0][0])[i] = 0;
-    __syncthreads();
-    for (uint32_t i = begin + lane; i < end; i += 64) atomicAdd(&counts[wave][(key[from][i] >> shift) % kBins], 1u);
+  for (int shift = 0; shift < bits; shift += kDigit) {
+    for (uint32_t i = lane; i < kBins; i += 64) counts[wave][i] = 0;  // the wave's own
+    if (shift != 0) {
+#pragma unroll
+      for (uint32_t j = 0; j < kMine; ++j) {
+        const uint32_t i = min(begin + j * 64 + lane, n - 1);
+        k[j] = key[i];
+        p[j] = place[i];
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (uint32_t j = 0; j < kMine; ++j) {
+      if (begin + j * 64 >= end) continue;  // the same for the wave
+      const bool there = begin + j * 64 + lane < end;
+      const uint32_t d = (k[j] >> shift) % kBins;
+      const uint64_t mates = same_digit(d, __ballot(there));
+      const uint32_t before = lanes_below(mates);
+      const uint32_t c = there ? counts[wave][d] : 0u;
+      rank[j] = c + before;
+      __builtin_amdgcn_wave_barrier();
+      if (there && before == 0) counts[wave][d] = c + static_cast<uint32_t>(__popcll(mates));
+      __builtin_amdgcn_wave_barrier();
+    }
     __syncthreads();
     scan_counts(counts, totals, nullptr);
     const bool last = shift + kDigit >= bits;
-    for (uint32_t at = begin; at < end; at += 64) {
-      const uint32_t i = at + lane;
-      const bool there = i < end;
-      const uint32_t k = there ? key[from][i] : 0u;
-      const uint32_t p = there ? place[from][i] : 0u;
-      const uint32_t d = (k >> shift) % kBins;
-      const uint64_t mates = same_digit(d, __ballot(there));
-      const uint32_t rank = lanes_below(mates);
-      uint32_t to = 0;
-      if (there) to = counts[wave][d] + rank;
-      __builtin_amdgcn_wave_barrier();
-      if (there && rank == 0) counts[wave][d] += static_cast<uint32_t>(__popcll(mates));
-      __builtin_amdgcn_wave_barrier();
-      if (there) {
-        if (last) {
-          keys[to] = k;
-          places[to] = p;
-        } else {
-          key[from ^ 1][to] = k;
-          place[from ^ 1][to] = static_cast<uint16_t>(p);
-        }
+#pragma unroll
+    for (uint32_t j = 0; j < kMine; ++j) {
+      if (begin + j * 64 + lane >= end) continue;
+      const uint32_t to = counts[wave][(k[j] >> shift) % kBins] + rank[j];
+      if (last) {
+        keys[to] = k[j];
+        places[to] = p[j];
+      } else {
+        key[to] = k[j];
+        place[to] = static_cast<uint16_t>(p[j]);
       }
     }
     __syncthreads();
