@@ -198,10 +198,12 @@ __device__ __forceinline__ void finish_row(const LogprobArgs& a, uint64_t row, c
 }
 
 // A lane's statistics on the way.  `r` stands for m log2 e, for m of at least
-// -kFar: what lies further down adds nothing to a row that has more.  A row
-// whose maximum itself is beyond +-kFar (masked by the type's lowest value
-// throughout, for one) is summed again by `careful` steps.
-constexpr float kFar = 0x1p126f;
+// -kFar: what lies further down is taken against -kFar.  The rounding of r goes
+// through the exponential, so it has to be small: up to |m| = kFar it is at most
+// 1, and it doubles with |m| (439 at 1e10, where 2^off is no fp32 number).  A row
+// whose maximum itself is beyond +-kFar (all of it masked by -1e9, for one) is
+// summed again, against the maximum.
+constexpr float kFar = 0x1p24f;
 struct Running {
   float m, r, s, t;
 };
@@ -219,16 +221,16 @@ __device__ __forceinline__ void add(Running& a, float z) {
   a.s += p;
   a.t = fmaf(p, fmaxf(u, kLeast), a.t);
 }
-// The same sums against m itself.
+// The same sums against m itself, or against -kFar for an m below.
 __device__ __forceinline__ Stats settled(const Running& a) {
-  if (a.m < -kFar) return {a.m, a.s, a.t};  // s is 0 or a NaN
+  if (a.m < -kFar) return {a.m == -INFINITY ? a.m : -kFar, a.s, a.t};  // r is exact there
   const float off = fmaf(a.m, kLog2e, -a.r), f = __builtin_amdgcn_exp2f(-off);
   return {a.m, a.s * f, fmaf(-off, a.s, a.t) * f};
 }
-__device__ __forceinline__ bool is_far(float m) { return fabsf(m) > kFar && fabsf(m) < INFINITY; }
-__device__ __forceinline__ void add_careful(Stats& a, float z) {
-  if (z > a.m) a = rebase(a, z);
-  const float u = (z - reference(a.m)) * kLog2e;
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) >= kFar && fabsf(m) < INFINITY; }
+// For a maximum that is known.
+__device__ __forceinline__ void add_against(Stats& a, float z) {
+  const float u = (z - a.m) * kLog2e;
   const float p = __builtin_amdgcn_exp2f(u);
   a.s += p;
   a.t = fmaf(p, fmaxf(u, kLeast), a.t);
@@ -377,15 +379,30 @@ __global__ __launch_bounds__(K * 64) void logprob_kernel(LogprobArgs a, uint32_t
 #pragma unroll
   for (int w = 1; w < K; ++w) all = merge(all, wave_stats[w]);
   if (is_far(all.m)) {  // the same for the workgroup
-    Stats c = {-INFINITY, 0.0f, 0.0f};
-    for (uint32_t i = threadIdx.x; i < n; i += K * 64) add_careful(c, static_cast<float>(z[i]));
-    c = wave_merge(c);
+    const float most = wave_max(st.m);
+    __syncthreads();
+    if (lane == 0) wave_stats[wave].m = most;
+    __syncthreads();
+    Stats c = {wave_stats[0].m, 0.0f, 0.0f};
+#pragma unroll
+    for (int w = 1; w < K; ++w) c.m = fmaxf(c.m, wave_stats[w].m);
+    for (uint32_t v = threadIdx.x; v < cut.vectors; v += K * 64) {
+      const typename X::wide f = widen<T, E>(load_kept<T, E>(cut.middle + static_cast<uint64_t>(v) * E));
+#pragma unroll
+      for (int i = 0; i < E; ++i) add_against(c, f[i]);
+    }
+    if (one < n) add_against(c, alone);
+    c.s = wave_sum(c.s);
+    c.t = wave_sum(c.t);
     __syncthreads();
     if (lane == 0) wave_stats[wave] = c;
     __syncthreads();
     all = wave_stats[0];
 #pragma unroll
-    for (int w = 1; w < K; ++w) all = merge(all, wave_stats[w]);
+    for (int w = 1; w < K; ++w) {
+      all.s += wave_stats[w].s;
+      all.t += wave_stats[w].t;
+    }
   }
   if (threadIdx.x == 0) {
     if (slices == 1)

@@ -1,0 +1,55 @@
+"""The training-step operators on the GPU at the ends of their ranges: far
+logits, large means, long rows, other streams.  Bounds as in test_steps_gpu.
+"""
+import math
+
+import pytest
+import torch
+
+import collective_reduction_ring_amd as rsx
+import step_oracle as so
+from parity_util import say
+from test_steps_gpu import BF16, DEV, F16, F32, gen
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------- logits between 2^24 and the type's end
+def far_logits(value, rows, vocab, dtype):
+    """Rows whose masked or whole logits lie at `value` (negative), among ordinary ones; some maxima at -value."""
+    g = gen(vocab)
+    z = torch.randn(8, vocab, generator=g, dtype=torch.float64) * 2
+    z[0] = value                                         # nothing but masked ones
+    z[1] = value
+    z[1, vocab // 2] = 0.5                               # one left
+    z[2, :vocab // 2] = value                            # whole lanes, waves and slices masked
+    z[3] = value * (1 + torch.arange(vocab) % 3 * torch.finfo(dtype).eps * 2)
+    z[4] = -math.inf
+    z[4, ::2] = value
+    z[5, vocab // 3] = -value                            # a far maximum
+    z[6] = -value
+    z[7, torch.rand(vocab, generator=g) < 0.7] = value
+    return z.repeat(-(-rows // 8), 1)[:rows].to(dtype)
+
+
+@pytest.mark.parametrize("rows,vocab,top", [(8, 300, 5), (1024, 300, 0), (1024, 777, 3), (8, 9001, 0), (8, 9001, 7), (8, 70001, 0),
+                                            (8, 70000, 4)])
+@pytest.mark.parametrize("zt,value", [(zt, v) for zt in (F32, BF16) for v in (-3e7, -1e9, -1e10, -1e12, -1e20, -1e30)]
+                         + [(F16, -6e4), (F32, -2.0 ** 24), (F32, -2.0 ** 24 - 2), (F32, -2.0 ** 31), (F32, -3.4e38)])
+def test_token_logprobs_of_far_logits(zt, value, rows, vocab, top):
+    z = far_logits(value, rows, vocab, zt)
+    tok = (torch.arange(rows) * 13 + vocab // 2) % vocab
+    say("token_logprobs of far logits", zt, value, rows, vocab, top)
+    zd, td = z.to(DEV), tok.to(DEV)
+    p = rsx.token_logprobs(zd, td, top)
+    ref, tol = so.token_logprobs(z, tok, top)
+    for k, r in ref.items():
+        got = getattr(p, k)
+        if k == "top_token":
+            assert torch.equal(got.cpu(), r), k
+        else:
+            so.close(got, r, tol[k] + 1.01 * so.rounding(r, F32), k)
+    g, h = torch.randn(rows, generator=gen(1)), torch.full((rows,), 0.5)
+    dz = rsx.token_logprobs_grad(zd, td, p.lse, g.to(DEV), p.entropy, h.to(DEV))
+    rz, tz = so.token_logprobs_grad(z, tok, p.lse.cpu(), p.entropy.cpu(), g, h)
+    so.close(dz, rz, tz + 1.01 * so.rounding(rz, zt), "dlogits")
