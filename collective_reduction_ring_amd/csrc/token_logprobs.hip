@@ -575,7 +575,8 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs 
   auto gradient = [&](float v, uint32_t e) {
     const float lp = v - lse;
     const float p = __builtin_amdgcn_exp2f(lp * kLog2e);
-    float d = -p * fmaf(h, fmaxf(lp, kLeast), c);
+    // Of no weight, no gradient: h log p may be past fp32, and 0 times that a NaN.
+    float d = p == 0.0f ? 0.0f : -p * fmaf(h, lp, c);
     if (mine == e) d += g;
     return none ? 0.0f : d;
   };

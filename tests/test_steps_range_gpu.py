@@ -53,3 +53,28 @@ def test_token_logprobs_of_far_logits(zt, value, rows, vocab, top):
     dz = rsx.token_logprobs_grad(zd, td, p.lse, g.to(DEV), p.entropy, h.to(DEV))
     rz, tz = so.token_logprobs_grad(z, tok, p.lse.cpu(), p.entropy.cpu(), g, h)
     so.close(dz, rz, tz + 1.01 * so.rounding(rz, zt), "dlogits")
+
+
+@pytest.mark.parametrize("zt", [F32, BF16, F16])
+@pytest.mark.parametrize("h", [-1e9, 1e20, -1e30, 3.4e38])
+@pytest.mark.parametrize("vocab", [37, 9000])
+def test_masked_logits_have_no_gradient_whatever_the_entropys(vocab, h, zt):
+    z = torch.randn(6, vocab, generator=gen(vocab))
+    z[:, 1::3] = torch.finfo(zt).min
+    z[:, 2::3] = -math.inf
+    z[:, 3::9] = -300.0                               # of no weight in 32 bits either
+    z = z.to(zt)
+    tok = torch.tensor([0, 1, 2, 3, 4, -1])
+    say("masked logits, dentropy", h, zt, vocab)
+    zd, td = z.to(DEV), tok.to(DEV)
+    p = rsx.token_logprobs(zd, td)
+    g, hs = torch.randn(6, generator=gen(2)), torch.full((6,), h)
+    dz = rsx.token_logprobs_grad(zd, td, p.lse, g.to(DEV), p.entropy, hs.to(DEV))
+    rz, tz = so.token_logprobs_grad(z, tok, p.lse.cpu(), p.entropy.cpu(), g, hs)
+    masked = z.float() <= -300
+    got = dz.cpu()
+    assert (got[masked & (torch.arange(vocab) != tok[:, None])] == 0).all()
+    own = masked.gather(1, tok.clamp(min=0)[:, None])[:, 0] & (tok >= 0)   # a masked token has its own gradient alone
+    assert torch.equal(got.gather(1, tok.clamp(min=0)[:, None])[:, 0][own], g.to(zt)[own])
+    if abs(h) < 1e38 and zt != F16:                   # else what is not masked leaves the type
+        so.close(dz, rz, tz + 1.01 * so.rounding(rz, zt), "dlogits")
