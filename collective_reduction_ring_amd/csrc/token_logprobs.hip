@@ -209,6 +209,9 @@ struct Running {
 };
 __device__ __forceinline__ float scaled(float m) { return fmaxf(m, -kFar) * kLog2e; }
 __device__ __forceinline__ void raise(Running& a, float m) {
+  // The old r against the new one as it is held, rounded: a contracted product
+  // leaves the rounding in the sums so far (up to a factor of 2^(1/4) at m = 2^22).
+#pragma clang fp contract(off)
   const float r = scaled(m), d = fmaxf(a.r - r, kLeast), f = __builtin_amdgcn_exp2f(d);
   a.t = fmaf(d, a.s, a.t) * f;
   a.s *= f;

@@ -78,3 +78,32 @@ def test_masked_logits_have_no_gradient_whatever_the_entropys(vocab, h, zt):
     assert torch.equal(got.gather(1, tok.clamp(min=0)[:, None])[:, 0][own], g.to(zt)[own])
     if abs(h) < 1e38 and zt != F16:                   # else what is not masked leaves the type
         so.close(dz, rz, tz + 1.01 * so.rounding(rz, zt), "dlogits")
+
+
+def log_probabilities(z):
+    """Of all tokens of rows without NaNs, in 64 bits, and a bound of their error that counts no rounding of z or lse."""
+    z = z.double()
+    c = z - z.amax(1, keepdim=True)
+    p = torch.exp(c)
+    s = p.sum(1, keepdim=True)
+    gap = torch.where(p > 0, p * -c, 0.0).sum(1, keepdim=True) / s
+    # as step_oracle.token_logprobs: the sum's relative error, then a difference and a logarithm
+    return c - torch.log(s), so.U * (z.shape[1] / 256 + 128 + 4 + 4 * gap) + 4 * so.U * (c.abs() + torch.log(s))
+
+
+@pytest.mark.parametrize("level", [0.0, -16384.0, 2.0 ** 20, 2.0 ** 22, -2.0 ** 22, 2.0 ** 24 - 40])
+@pytest.mark.parametrize("rows,vocab,zt", [(6, 2000, F32), (1030, 4000, F32), (5, 30001, F32), (3, 200001, F32), (300, 50000, F32),
+                                           (3, 70001, BF16)])
+def test_rising_rows_far_from_zero(rows, vocab, zt, level):
+    """The maximum rises in most steps: what was summed before it has to follow."""
+    z = torch.linspace(0, 8, vocab, dtype=torch.float64) + torch.randn(rows, vocab, generator=gen(vocab)) * 0.5 + level
+    z = z.to(zt)
+    tok = torch.arange(rows) * 7 % vocab
+    say("rising rows", rows, vocab, zt, level)
+    p = rsx.token_logprobs(z.to(DEV), tok.to(DEV))
+    lp, tol = log_probabilities(z)
+    want, tol = lp.gather(1, tok[:, None])[:, 0], tol.gather(1, tok[:, None])[:, 0]
+    so.close(p.logprob, want, tol + 1.01 * so.rounding(want, F32), "logprob")
+    ref, rtol = so.token_logprobs(z, tok, 0)
+    so.close(p.entropy, ref["entropy"], rtol["entropy"] + 1.01 * so.rounding(ref["entropy"], F32), "entropy")
+    so.close(p.lse, ref["lse"], rtol["lse"] + 1.01 * so.rounding(ref["lse"], F32), "lse")
