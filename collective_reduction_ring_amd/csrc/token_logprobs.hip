@@ -183,18 +183,27 @@ __device__ __forceinline__ Token row_token(const LogprobArgs& a, uint64_t row) {
   const bool there = tok < a.vocab;
   return {there, there ? logit_at(a, row * a.stride + tok) : 0.0f};
 }
-__device__ __forceinline__ float row_lse_of(const Stats& st) {
-  return st.s == 0.0f && st.m == -INFINITY ? -INFINITY : st.m + logf(st.s < 1.0f ? 1.0f : st.s);
+// A row's maximum and the logarithm of its sum: lse in two parts.
+struct Level {
+  float m, ln_s;
+};
+__device__ __forceinline__ bool all_masked(const Stats& st) { return st.s == 0.0f && st.m == -INFINITY; }
+__device__ __forceinline__ Level level_of(const Stats& st) {
+  // The maximum's own term is 1, but for roundings.
+  return {st.m, all_masked(st) ? -INFINITY : logf(st.s < 1.0f ? 1.0f : st.s)};
+}
+// (z - m) - ln s keeps more digits than z - lse where the maximum is large.
+__device__ __forceinline__ float log_prob(const Level& l, float z) {
+  return l.ln_s == -INFINITY ? -INFINITY : (z - l.m) - l.ln_s;
 }
 __device__ __forceinline__ void finish_row(const LogprobArgs& a, uint64_t row, const Stats& st, const Token& tok) {
-  const bool none = st.s == 0.0f && st.m == -INFINITY;  // every logit masked
-  // The maximum's own term is 1 and u is not positive, but for roundings.
+  const bool none = all_masked(st);
+  const Level l = level_of(st);
+  a.logprob[row] = tok.there ? log_prob(l, tok.z) : 0.0f;
+  a.lse[row] = none ? -INFINITY : l.m + l.ln_s;
+  // u is not positive, but for roundings
   const float s = st.s < 1.0f ? 1.0f : st.s, t = st.t > 0.0f ? 0.0f : st.t;
-  const float ln_s = logf(s);
-  // (z - m) - ln s keeps more digits than z - lse where the maximum is large
-  a.logprob[row] = !tok.there ? 0.0f : none ? -INFINITY : (tok.z - st.m) - ln_s;
-  a.lse[row] = row_lse_of(st);
-  if (a.entropy != nullptr) a.entropy[row] = none ? 0.0f : ln_s - t * kLn2 / s;
+  if (a.entropy != nullptr) a.entropy[row] = none ? 0.0f : l.ln_s - t * kLn2 / s;
 }
 
 // A lane's statistics on the way.  `r` stands for m log2 e, for m of at least
@@ -414,7 +423,7 @@ __global__ __launch_bounds__(K * 64) void logprob_kernel(LogprobArgs a, uint32_t
       partial[block] = {all.m, all.s, all.t, 0.0f};
   }
   if constexpr (TOP) {
-    const float lse = row_lse_of(all);
+    const Level level = level_of(all);
     // A candidate's rank is the number of larger ones; all are different but
     // for 0, which is none.
     for (uint32_t i = threadIdx.x; i < K * top; i += K * 64) {
@@ -430,9 +439,8 @@ __global__ __launch_bounds__(K * 64) void logprob_kernel(LogprobArgs a, uint32_t
         }
       if (c != 0 && rank < top) {
         if (slices == 1) {
-          const float v = order_value(static_cast<uint32_t>(c >> 32));
           a.top_token[row * top + rank] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(c));
-          a.top_logprob[row * top + rank] = lse == -INFINITY ? -INFINITY : v - lse;
+          a.top_logprob[row * top + rank] = log_prob(level, order_value(static_cast<uint32_t>(c >> 32)));
         } else {
           best_out[block * top + rank] = c;
         }
@@ -451,7 +459,7 @@ __global__ __launch_bounds__(kJoinThreads) void logprob_join_kernel(LogprobArgs 
                                                                     const Partial* partial, const uint64_t* best) {
   __shared__ uint64_t cand[kMaxJoin];
   __shared__ uint32_t ranks[kMaxJoin];
-  __shared__ float row_lse;
+  __shared__ Level row_level;
   const uint64_t row = block_id();
   if (row >= a.rows) return;
   const uint32_t top = a.top, n = slices * top;
@@ -468,7 +476,7 @@ __global__ __launch_bounds__(kJoinThreads) void logprob_join_kernel(LogprobArgs 
       st = {p.m, p.s, p.t};
     }
     st = wave_merge(st);
-    if (threadIdx.x == 0) row_lse = row_lse_of(st);
+    if (threadIdx.x == 0) row_level = level_of(st);
   }
   __syncthreads();
   // A candidate's rank is the number of larger ones, counted in parts.
@@ -483,14 +491,13 @@ __global__ __launch_bounds__(kJoinThreads) void logprob_join_kernel(LogprobArgs 
     if (rank != 0) atomicAdd(&ranks[who], rank);
   }
   __syncthreads();
-  const float lse = row_lse;
+  const Level level = row_level;
   for (uint32_t i = threadIdx.x; i < n; i += kJoinThreads) {
     const uint64_t c = cand[i];
     const uint32_t rank = ranks[i];
     if (c == 0 || rank >= top) continue;
     a.top_token[row * top + rank] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(c));
-    a.top_logprob[row * top + rank] =
-        lse == -INFINITY ? -INFINITY : order_value(static_cast<uint32_t>(c >> 32)) - lse;
+    a.top_logprob[row * top + rank] = log_prob(level, order_value(static_cast<uint32_t>(c >> 32)));
   }
   if (threadIdx.x == 0) finish_row(a, row, st, token);  // the token's logit is the last to come
 }

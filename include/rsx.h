@@ -481,7 +481,8 @@ rsx_status_t rsx_checkpoint_unpack(const int8_t* codes, const uint8_t* scales, v
  * lse = log sum exp z; logprob = z[token] - lse (0 for a token outside
  * [0, vocab)); entropy = -sum p log p (may be null); and the `top` largest
  * logits, in order, of equal ones the lower index first (a NaN ranks below
- * every number): top_token[row][k] and top_logprob[row][k] = z - lse.
+ * every number): top_token[row][k] and top_logprob[row][k], its log probability,
+ * the same bits as logprob has for that token.
  * top: 0..min(vocab, RSX_TOP_MAX); with 0 the two arrays may be null.
  * A logit of -inf is masked.  A row with nothing else has lse = -inf, log
  * probabilities of -inf and entropy 0; a row with a NaN or +inf has NaN.

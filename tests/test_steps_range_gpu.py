@@ -107,3 +107,30 @@ def test_rising_rows_far_from_zero(rows, vocab, zt, level):
     ref, rtol = so.token_logprobs(z, tok, 0)
     so.close(p.entropy, ref["entropy"], rtol["entropy"] + 1.01 * so.rounding(ref["entropy"], F32), "entropy")
     so.close(p.lse, ref["lse"], rtol["lse"] + 1.01 * so.rounding(ref["lse"], F32), "lse")
+
+
+def level_logits(rows, vocab, level, dtype):
+    """Logits around `level`, and tokens that are the most likely, a likely or any other one."""
+    g = gen(vocab + rows)
+    z = (torch.randn(rows, vocab, generator=g) * 2 + level).to(dtype)
+    best = torch.argsort(z.float(), dim=1, descending=True, stable=True)
+    tok = best.gather(1, torch.tensor([0, min(2, vocab - 1), vocab // 2]).repeat(rows)[:rows, None])[:, 0]
+    return z, tok
+
+
+@pytest.mark.parametrize("level", [0.0, 900.0, -16384.0, 16384.0, 2.0 ** 22])
+@pytest.mark.parametrize("rows,vocab,top,zt", [(6, 40, 8, F32), (1030, 1000, 5, F32), (5, 9001, 16, F32), (3, 70001, 64, F32),
+                                               (5, 9001, 8, BF16), (3, 131072, 8, BF16)])
+def test_alternatives_have_the_digits_of_the_log_probabilities(rows, vocab, top, zt, level):
+    z, tok = level_logits(rows, vocab, level, zt)
+    say("alternatives at a level", rows, vocab, top, zt, level)
+    p = rsx.token_logprobs(z.to(DEV), tok.to(DEV), top)
+    lp, tol = log_probabilities(z)
+    at = p.top_token.cpu().long()
+    want = lp.gather(1, at)
+    so.close(p.top_logprob, want, tol.gather(1, at) + 1.01 * so.rounding(want, F32), "top_logprob")
+    # one token, one value
+    mine = p.top_token == tok.to(DEV)[:, None]
+    row = mine.any(1)
+    assert row.any()
+    assert torch.equal(p.top_logprob[mine], p.logprob[row])
