@@ -69,7 +69,9 @@ SIGNATURES = {
     "rsx_checkpoint_unpack": (_I, [_P, _P, _P, _SZ, _SZ, _SZ, _I, _P]),
     "rsx_token_logprobs_workspace_size": (_SZ, [_SZ, _SZ, _I]),
     "rsx_token_logprobs": (_I, [_P, _SZ, _I, _P, _I, _SZ, _SZ, _I, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "rsx_token_logprobs_rest": (_I, [_P, _SZ, _I, _P, _I, _SZ, _SZ, _I, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "rsx_token_logprobs_grad": (_I, [_P, _SZ, _I, _P, _I, _P, _P, _P, _P, _P, _SZ, _SZ, _SZ, _P]),
+    "rsx_token_logprobs_grad_rest": (_I, [_P, _SZ, _I, _P, _I, _P, _P, _P, _P, _P, _P, _SZ, _SZ, _SZ, _P]),
     "rsx_segment_begin": (_SZ, [_SZ, _I, _I]),
     "rsx_dtype_size": (_SZ, [_I]),
     "rsx_status_string": (ctypes.c_char_p, [_I]),

@@ -241,6 +241,16 @@ rsx_status_t rsx_token_logprobs(const void* logits, size_t stride, rsx_dtype_t t
                                 size_t vocab, int top, float* logprob, float* entropy, float* lse,
                                 float* top_logprob, int32_t* top_token, void* workspace,
                                 size_t workspace_bytes, hipStream_t stream) {
+  return rsx_token_logprobs_rest(logits, stride, type, tokens, token_type, rows, vocab, top, logprob, entropy, lse, nullptr,
+                                 top_logprob, top_token, workspace, workspace_bytes, stream);
+}
+
+rsx_status_t rsx_token_logprobs_rest(const void* logits, size_t stride, rsx_dtype_t type,
+                                     const void* tokens, rsx_dtype_t token_type, size_t rows,
+                                     size_t vocab, int top, float* logprob, float* entropy,
+                                     float* lse, float* lse_rest, float* top_logprob,
+                                     int32_t* top_token, void* workspace, size_t workspace_bytes,
+                                     hipStream_t stream) {
   const size_t es = float_size(type), is = token_size(token_type);
   if (es == 0 || is == 0) return RSX_ERR_INVALID_TYPE;
   if (rows > kMaxSize || vocab > kMaxSize) return RSX_ERR_UNSUPPORTED;
@@ -251,6 +261,7 @@ rsx_status_t rsx_token_logprobs(const void* logits, size_t stride, rsx_dtype_t t
   m.write_flat(logprob, rows, 4);
   if (entropy != nullptr) m.write_flat(entropy, rows, 4);
   m.write_flat(lse, rows, 4);
+  if (lse_rest != nullptr) m.write_flat(lse_rest, rows, 4);
   if (top != 0) {
     m.write_flat(top_logprob, rows * static_cast<size_t>(top), 4);
     m.write_flat(top_token, rows * static_cast<size_t>(top), 4);
@@ -258,8 +269,8 @@ rsx_status_t rsx_token_logprobs(const void* logits, size_t stride, rsx_dtype_t t
   m.workspace(workspace, workspace_bytes, rsx_token_logprobs_workspace_size(rows, vocab, top));
   const rsx_status_t st = m.status();
   if (st != RSX_SUCCESS || rows == 0) return st;
-  return hip_status(launch_token_logprobs({logits, tokens, logprob, entropy, lse, top_logprob, top_token, workspace,
-                                           stride, rows, vocab, static_cast<uint32_t>(top), type,
+  return hip_status(launch_token_logprobs({logits, tokens, logprob, entropy, lse, lse_rest, top_logprob, top_token,
+                                           workspace, stride, rows, vocab, static_cast<uint32_t>(top), type,
                                            token_type == RSX_INT64},
                                           stream));
 }
@@ -269,6 +280,17 @@ rsx_status_t rsx_token_logprobs_grad(const void* logits, size_t stride, rsx_dtyp
                                      const float* entropy, const float* dlogprob,
                                      const float* dentropy, void* dlogits, size_t dlogits_stride,
                                      size_t rows, size_t vocab, hipStream_t stream) {
+  return rsx_token_logprobs_grad_rest(logits, stride, type, tokens, token_type, lse, nullptr, entropy, dlogprob, dentropy,
+                                      dlogits, dlogits_stride, rows, vocab, stream);
+}
+
+rsx_status_t rsx_token_logprobs_grad_rest(const void* logits, size_t stride, rsx_dtype_t type,
+                                          const void* tokens, rsx_dtype_t token_type,
+                                          const float* lse, const float* lse_rest,
+                                          const float* entropy, const float* dlogprob,
+                                          const float* dentropy, void* dlogits,
+                                          size_t dlogits_stride, size_t rows, size_t vocab,
+                                          hipStream_t stream) {
   const size_t es = float_size(type), is = token_size(token_type);
   if (es == 0 || is == 0) return RSX_ERR_INVALID_TYPE;
   if (rows > kMaxSize || vocab > kMaxSize) return RSX_ERR_UNSUPPORTED;
@@ -278,6 +300,7 @@ rsx_status_t rsx_token_logprobs_grad(const void* logits, size_t stride, rsx_dtyp
   m.read(logits, rows, vocab, stride, es);
   m.read_flat(tokens, rows, is);
   m.read_flat(lse, rows, 4);
+  if (lse_rest != nullptr) m.read_flat(lse_rest, rows, 4);
   m.read_flat(dlogprob, rows, 4);
   if (dentropy != nullptr) {
     m.read_flat(dentropy, rows, 4);
@@ -285,8 +308,8 @@ rsx_status_t rsx_token_logprobs_grad(const void* logits, size_t stride, rsx_dtyp
   }
   const rsx_status_t st = m.status(1);
   if (st != RSX_SUCCESS || rows == 0) return st;
-  return hip_status(launch_token_logprobs_grad({logits, tokens, lse, entropy, dlogprob, dentropy, dlogits, stride,
-                                                dlogits_stride, rows, vocab, type, token_type == RSX_INT64},
+  return hip_status(launch_token_logprobs_grad({logits, tokens, lse, lse_rest, entropy, dlogprob, dentropy, dlogits,
+                                                stride, dlogits_stride, rows, vocab, type, token_type == RSX_INT64},
                                                stream));
 }
 

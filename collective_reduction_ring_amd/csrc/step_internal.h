@@ -105,8 +105,9 @@ struct LogprobArgs {
   const void* logits;
   const void* tokens;
   float* logprob;
-  float* entropy;
+  float* entropy;      // may be null
   float* lse;
+  float* lse_rest;     // may be null
   float* top_logprob;
   int32_t* top_token;
   void* ws;
@@ -121,6 +122,7 @@ struct LogprobGradArgs {
   const void* logits;
   const void* tokens;
   const float* lse;
+  const float* lse_rest;  // may be null
   const float* entropy;   // null with dentropy
   const float* dlogprob;
   const float* dentropy;  // may be null

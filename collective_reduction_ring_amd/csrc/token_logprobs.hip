@@ -13,7 +13,9 @@
 // the reads do, so u is one: z log2 e - r, with r = m log2 e rounded; what the
 // rounding took is put back once, at the end.  A masked logit (-inf) adds nothing; a row of
 // nothing else has lse = -inf, log probabilities of -inf, entropy 0 and a
-// gradient of 0.  A row with a NaN or +inf has NaN for lse, log probabilities,
+// gradient of 0.  lse alone is a rounding of lse's size off (2^-10 at 16384), and
+// so is each p that a gradient takes from it; lse_rest keeps what that took.
+// A row with a NaN or +inf has NaN for lse, log probabilities,
 // entropy and gradient.  A token outside the row has log probability 0 and no
 // gradient through it.
 #include "step_device.h"
@@ -200,7 +202,13 @@ __device__ __forceinline__ void finish_row(const LogprobArgs& a, uint64_t row, c
   const bool none = all_masked(st);
   const Level l = level_of(st);
   a.logprob[row] = tok.there ? log_prob(l, tok.z) : 0.0f;
-  a.lse[row] = none ? -INFINITY : l.m + l.ln_s;
+  const float lse = none ? -INFINITY : l.m + l.ln_s;
+  a.lse[row] = lse;
+  if (a.lse_rest != nullptr) {
+    // What the rounding took from the sum of m and ln s, exactly.
+    const float ln_s = lse - l.m;
+    a.lse_rest[row] = fabsf(lse) < INFINITY ? (l.m - (lse - ln_s)) + (l.ln_s - ln_s) : 0.0f;
+  }
   // u is not positive, but for roundings
   const float s = st.s < 1.0f ? 1.0f : st.s, t = st.t > 0.0f ? 0.0f : st.t;
   if (a.entropy != nullptr) a.entropy[row] = none ? 0.0f : l.ln_s - t * kLn2 / s;
@@ -575,7 +583,7 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs 
       raw[j] = load_once<T, E>(cut.middle + static_cast<uint64_t>(base + j * kThreads) * E);
   const uint32_t one = tile == 0 ? cut.single(threadIdx.x) : 0xffffffffu;
   const float alone = one < vocab ? static_cast<float>(z[one]) : 0.0f;
-  const float lse = a.lse[row];
+  const float lse = a.lse[row], rest = a.lse_rest != nullptr ? a.lse_rest[row] : 0.0f;
   const uint64_t tok = token_at(a.tokens, row, a.wide);
   const uint32_t mine = tok < a.vocab ? static_cast<uint32_t>(tok) : 0xffffffffu;  // no element's index
   const float g = tok < a.vocab ? a.dlogprob[row] : 0.0f;
@@ -583,7 +591,7 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs 
   const float c = a.dentropy != nullptr ? fmaf(h, a.entropy[row], g) : g;  // dz_j = -p_j (c + h log p_j)
   const bool none = lse == -INFINITY;
   auto gradient = [&](float v, uint32_t e) {
-    const float lp = v - lse;
+    const float lp = (v - lse) - rest;
     const float p = __builtin_amdgcn_exp2f(lp * kLog2e);
     // Of no weight, no gradient: h log p may be past fp32, and 0 times that a NaN.
     float d = p == 0.0f ? 0.0f : -p * fmaf(h, lp, c);

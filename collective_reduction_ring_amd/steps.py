@@ -330,8 +330,9 @@ class LayerNormGrad(_Plan):
 class TokenLogprobs(_Plan):
     """Prepared log probabilities: for each row of ``logits`` the ``logprob`` of
     its token (0 for a token outside the row, as padding has), the ``entropy``,
-    ``lse``, and with ``top`` > 0 the ``top`` largest logits' ``top_token`` and
-    ``top_logprob``, equal ones by the lower index.  A logit of -inf is masked."""
+    ``lse`` with ``lse_rest`` (what its rounding took: the gradient needs it for
+    large logits), and with ``top`` > 0 the ``top`` largest logits' ``top_token``
+    and ``top_logprob``, equal ones by the lower index.  A logit of -inf is masked."""
 
     def __init__(self, logits, tokens, top: int = 0):
         rows, vocab, zs, zt = _rows(logits, "logits")
@@ -342,21 +343,25 @@ class TokenLogprobs(_Plan):
         if not 0 <= top <= min(vocab, L.RSX_TOP_MAX):
             raise ValueError(f"top={top} outside [0, {min(vocab, L.RSX_TOP_MAX)}]")
         new = lambda *s: torch.empty((*lead, *s), dtype=torch.float32, device=dev)  # noqa: E731
-        self.logprob, self.entropy, self.lse = new(), new(), new()
+        self.logprob, self.entropy, self.lse, self.lse_rest = new(), new(), new(), new()
         self.top_logprob = new(top) if top else None
         self.top_token = torch.empty((*lead, top), dtype=torch.int32, device=dev) if top else None
         ws, wb, self._ws = self._workspace(L.lib().rsx_token_logprobs_workspace_size(rows, vocab, top), dev)
-        self._prepare("rsx_token_logprobs", dev,
+        self._prepare("rsx_token_logprobs_rest", dev,
                       (_ptr(logits), zs, zt, _ptr(tokens), TOKENS[tokens.dtype], rows, vocab, top, _ptr(self.logprob),
-                       _ptr(self.entropy), _ptr(self.lse), _ptr(self.top_logprob), _ptr(self.top_token), ws, wb),
-                      (logits, tokens, self.logprob, self.entropy, self.lse, self.top_logprob, self.top_token, self._ws))
+                       _ptr(self.entropy), _ptr(self.lse), _ptr(self.lse_rest), _ptr(self.top_logprob), _ptr(self.top_token),
+                       ws, wb),
+                      (logits, tokens, self.logprob, self.entropy, self.lse, self.lse_rest, self.top_logprob, self.top_token,
+                       self._ws))
 
 
 class TokenLogprobsGrad(_Plan):
     """Prepared gradient in the logits for gradients ``dlogprob`` and (with
-    ``entropy``) ``dentropy``; ``dlogits`` may be ``logits`` itself."""
+    ``entropy``) ``dentropy``; ``dlogits`` may be ``logits`` itself.  ``lse_rest``
+    is the forward pass's: without it the probabilities are off by the rounding
+    of ``lse``, 2^-24 of its size."""
 
-    def __init__(self, logits, tokens, lse, dlogprob, entropy=None, dentropy=None, dlogits=None):
+    def __init__(self, logits, tokens, lse, dlogprob, entropy=None, dentropy=None, dlogits=None, lse_rest=None):
         rows, vocab, zs, zt = _rows(logits, "logits")
         dev = logits.device
         _tokens(tokens, "tokens", dev, logits.shape[:-1])
@@ -364,6 +369,8 @@ class TokenLogprobsGrad(_Plan):
             raise ValueError("logits has empty rows")
         _vector(lse, "lse", rows, torch.float32, dev)
         _vector(dlogprob, "dlogprob", rows, torch.float32, dev)
+        if lse_rest is not None:
+            _vector(lse_rest, "lse_rest", rows, torch.float32, dev)
         if dentropy is None:
             entropy = None
         else:
@@ -375,10 +382,10 @@ class TokenLogprobsGrad(_Plan):
             dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
         _, _, ds, _ = _rows(dlogits, "dlogits", device=dev, shape=logits.shape, dtype=logits.dtype, output=True)
         self.dlogits = dlogits
-        self._prepare("rsx_token_logprobs_grad", dev,
-                      (_ptr(logits), zs, zt, _ptr(tokens), TOKENS[tokens.dtype], _ptr(lse), _ptr(entropy), _ptr(dlogprob),
-                       _ptr(dentropy), _ptr(dlogits), ds, rows, vocab),
-                      (logits, tokens, lse, entropy, dlogprob, dentropy, dlogits))
+        self._prepare("rsx_token_logprobs_grad_rest", dev,
+                      (_ptr(logits), zs, zt, _ptr(tokens), TOKENS[tokens.dtype], _ptr(lse), _ptr(lse_rest), _ptr(entropy),
+                       _ptr(dlogprob), _ptr(dentropy), _ptr(dlogits), ds, rows, vocab),
+                      (logits, tokens, lse, lse_rest, entropy, dlogprob, dentropy, dlogits))
 
 
 def embedding(table, tokens, out=None, scale: float = 1.0, first: int = 0, stream=None):
@@ -429,8 +436,8 @@ def token_logprobs(logits, tokens, top: int = 0, stream=None) -> TokenLogprobs:
     return p
 
 
-def token_logprobs_grad(logits, tokens, lse, dlogprob, entropy=None, dentropy=None, dlogits=None, stream=None):
+def token_logprobs_grad(logits, tokens, lse, dlogprob, entropy=None, dentropy=None, dlogits=None, stream=None, lse_rest=None):
     """The gradient in the logits; see ``TokenLogprobsGrad``."""
-    p = TokenLogprobsGrad(logits, tokens, lse, dlogprob, entropy, dentropy, dlogits)
+    p = TokenLogprobsGrad(logits, tokens, lse, dlogprob, entropy, dentropy, dlogits, lse_rest)
     p(stream)
     return p.dlogits

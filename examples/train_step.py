@@ -44,7 +44,8 @@ class Rank:
         self.logp = rsx.TokenLogprobs(self.logits, self.targets)
         # backward of the mean of -log p; the logits' gradient takes their place
         minus = torch.full((tokens,), -1.0 / tokens, device=dev)
-        self.dlogits = rsx.TokenLogprobsGrad(self.logits, self.targets, self.logp.lse, minus, dlogits=self.logits)
+        self.dlogits = rsx.TokenLogprobsGrad(self.logits, self.targets, self.logp.lse, minus, dlogits=self.logits,
+                                             lse_rest=self.logp.lse_rest)
         self.dy = torch.empty_like(x)
         self.dnorm = rsx.LayerNormGrad(self.dy, self.norm.checkpoint, self.norm.mean, self.norm.rstd, self.weight, dx=self.dy,
                                        dweight=self.grads[1], dbias=self.grads[2])

@@ -61,7 +61,7 @@
 extern "C" {
 #endif
 
-#define RSX_VERSION 120          /* 1.2.0 */
+#define RSX_VERSION 130          /* 1.3.0 */
 #define RSX_MAX_RANKS 16         /* largest W a call accepts */
 #define RSX_NAIVE_MAX_BYTES 32768 /* RSX_ALGO_AUTO picks naive at or below this, per rank [MX] */
 #define RSX_FUSE_BATCH 248       /* tensors per pack/unpack launch */
@@ -486,6 +486,9 @@ rsx_status_t rsx_checkpoint_unpack(const int8_t* codes, const uint8_t* scales, v
  * top: 0..min(vocab, RSX_TOP_MAX); with 0 the two arrays may be null.
  * A logit of -inf is masked.  A row with nothing else has lse = -inf, log
  * probabilities of -inf and entropy 0; a row with a NaN or +inf has NaN.
+ * The _rest form also keeps lse_rest (`rows` fp32, or null): what the rounding of
+ * lse took, so that lse + lse_rest has the digits of log sum exp z whatever its
+ * size.  0 where lse is no number.
  */
 size_t rsx_token_logprobs_workspace_size(size_t rows, size_t vocab, int top);
 rsx_status_t rsx_token_logprobs(const void* logits, size_t stride, rsx_dtype_t type,
@@ -493,6 +496,12 @@ rsx_status_t rsx_token_logprobs(const void* logits, size_t stride, rsx_dtype_t t
                                 size_t vocab, int top, float* logprob, float* entropy, float* lse,
                                 float* top_logprob, int32_t* top_token, void* workspace,
                                 size_t workspace_bytes, hipStream_t stream);
+rsx_status_t rsx_token_logprobs_rest(const void* logits, size_t stride, rsx_dtype_t type,
+                                     const void* tokens, rsx_dtype_t token_type, size_t rows,
+                                     size_t vocab, int top, float* logprob, float* entropy,
+                                     float* lse, float* lse_rest, float* top_logprob,
+                                     int32_t* top_token, void* workspace, size_t workspace_bytes,
+                                     hipStream_t stream);
 
 /*
  * Gradient of the log probability and of the entropy in the logits:
@@ -501,12 +510,23 @@ rsx_status_t rsx_token_logprobs(const void* logits, size_t stride, rsx_dtype_t t
  * dentropy may be null (then entropy may be too).  A token outside [0, vocab)
  * has no gradient through its log probability; a row of masked logits alone
  * has a gradient of 0.  dlogits == logits with one stride is allowed.
+ * log p_j = z_j - lse, in the _rest form (z_j - lse) - lse_rest.  Without the
+ * rest each p is off by lse's rounding, 2^-24 |lse| of itself: little for logits
+ * of ordinary size, 1e-3 at 16384, and past 2^24 a row of equal logits has p = 1
+ * for each.  lse_rest: as rsx_token_logprobs_rest keeps it, or null.
  */
 rsx_status_t rsx_token_logprobs_grad(const void* logits, size_t stride, rsx_dtype_t type,
                                      const void* tokens, rsx_dtype_t token_type, const float* lse,
                                      const float* entropy, const float* dlogprob,
                                      const float* dentropy, void* dlogits, size_t dlogits_stride,
                                      size_t rows, size_t vocab, hipStream_t stream);
+rsx_status_t rsx_token_logprobs_grad_rest(const void* logits, size_t stride, rsx_dtype_t type,
+                                          const void* tokens, rsx_dtype_t token_type,
+                                          const float* lse, const float* lse_rest,
+                                          const float* entropy, const float* dlogprob,
+                                          const float* dentropy, void* dlogits,
+                                          size_t dlogits_stride, size_t rows, size_t vocab,
+                                          hipStream_t stream);
 
 /*
  * First element of segment k in RSX_ALGO_RING all-reduce of `count`

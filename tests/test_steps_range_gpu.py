@@ -134,3 +134,51 @@ def test_alternatives_have_the_digits_of_the_log_probabilities(rows, vocab, top,
     row = mine.any(1)
     assert row.any()
     assert torch.equal(p.top_logprob[mine], p.logprob[row])
+
+
+@pytest.mark.parametrize("level", [0.0, 900.0, -16384.0, 16384.0, 2.0 ** 22])
+@pytest.mark.parametrize("rows,vocab,zt", [(6, 40, F32), (1030, 1000, F32), (5, 9001, F32), (3, 70001, F32), (5, 9001, BF16)])
+def test_gradient_has_the_digits_of_the_log_probabilities(rows, vocab, zt, level):
+    """Against the logits alone: no rounding of lse's size counts."""
+    z, tok = level_logits(rows, vocab, level, zt)
+    g, h = torch.randn(rows, generator=gen(1)), torch.randn(rows, generator=gen(2))
+    say("gradient at a level", rows, vocab, zt, level)
+    zd, td = z.to(DEV), tok.to(DEV)
+    p = rsx.token_logprobs(zd, td)
+    lp, tol = log_probabilities(z)
+    ent = -(lp.exp() * lp).sum(1)
+    whole, e_lse = z.double().amax(1) - lp.amax(1), tol.amin(1)
+    two = p.lse.cpu().double() + p.lse_rest.cpu().double()
+    assert ((two - whole).abs() <= e_lse + 2 * so.U ** 2 * whole.abs() + 2.0 ** -52 * whole.abs()).all()
+    dz = rsx.token_logprobs_grad(zd, td, p.lse, g.to(DEV), p.entropy, h.to(DEV), lse_rest=p.lse_rest)
+    e_ent = so.token_logprobs(z, tok, 0)[1]["entropy"][:, None] + so.rounding(ent, F32)[:, None]
+    prob, g, h, ent = lp.exp(), g.double()[:, None], h.double()[:, None], ent[:, None]
+    hit = torch.zeros_like(lp).scatter_(1, tok[:, None], 1.0)
+    want = g * hit - prob * (g + h * (lp + ent))
+    # p's relative error is lp's; lp and the entropy again as factors of h; then the products' roundings
+    size = prob * (g.abs() + h.abs() * (lp.abs() + ent))
+    e = size * (tol + so.U * (12 + 4 * lp.abs())) + prob * h.abs() * (tol + e_ent) + 2 * so.U * g.abs() * hit + 2.0 ** -120
+    so.close(dz, want, e + 1.01 * so.rounding(want, zt), "dlogits")
+
+
+@pytest.mark.parametrize("vocab", [64, 9000])
+@pytest.mark.parametrize("zt,value", [(F32, -3.4e38), (F32, -1e10), (F32, 1e30), (BF16, -1e9), (BF16, torch.finfo(BF16).min),
+                                      (F16, torch.finfo(F16).min)])
+def test_rows_of_one_far_value_are_uniform(zt, value, vocab):
+    """The softmax of equal logits is 1 / vocab, and so is its gradient, also where lse itself is the value."""
+    z = torch.full((3, vocab), value).to(zt)
+    z[1, 1::2] = -math.inf
+    tok = torch.tensor([0, 2, -1])
+    say("rows of one far value", zt, value, vocab)
+    p = rsx.token_logprobs(z.to(DEV), tok.to(DEV))
+    g, h = torch.tensor([1.0, -0.5, 2.0]), torch.tensor([0.0, 0.3, 0.7])
+    dz = rsx.token_logprobs_grad(z.to(DEV), tok.to(DEV), p.lse, g.to(DEV), p.entropy, h.to(DEV), lse_rest=p.lse_rest)
+    n = torch.tensor([vocab, vocab // 2, vocab], dtype=torch.float64)[:, None]
+    there = (z != -math.inf).double()
+    ok = (tok >= 0).double()[:, None]
+    hit = torch.zeros(3, vocab, dtype=torch.float64).scatter_(1, tok.clamp(min=0)[:, None], 1.0) * ok
+    want = g.double()[:, None] * (hit - there / n * ok)  # all alike: the entropy is at its largest and has no slope
+    # ln n has two roundings, p one exponential; log p + H leaves those of ln n, each of a size of at most ln 9000
+    e = there / n * so.U * 16 * (3 + 10) + 2 * so.U * hit
+    so.close(dz, want, e + 1.01 * so.rounding(want, zt), "dlogits")
+    assert torch.equal(p.entropy.cpu() > 0, torch.ones(3, dtype=torch.bool))
