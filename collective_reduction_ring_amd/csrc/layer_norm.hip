@@ -6,11 +6,12 @@
 //   dw = sum over rows of dy xhat,  db = sum over rows of dy.
 //
 // Everything is held in fp32 and rounded once, at the store.  All kernels
-// here are bound by HBM: a row is read once into registers, both its sums are
-// taken there (the variance from the differences, so no digits are lost to a
-// large mean), and the result is written from them.  Measured: 32768 rows of
-// 4096 bf16 forward 91 us (5.9 TB/s), backward 139 us (5.8 TB/s); rows that are
-// no multiple of 16 bytes share cache lines and run at 4.3 to 5 TB/s.
+// here are bound by HBM: a row is read once into registers, its sums are taken
+// there (the variance from the differences, and for a large mean the mean's own
+// error too, so no digits are lost to it), and the result is written from them.
+// Measured: 32768 rows of 4096 bf16 forward 91 us (5.9 TB/s), backward 139 us
+// (5.8 TB/s); rows that are no multiple of 16 bytes share cache lines and run at
+// 4.3 to 5 TB/s.
 #include "step_device.h"
 
 namespace rsx {
@@ -26,12 +27,38 @@ constexpr float kScaleDown = 0x1p-80f;
 __device__ __forceinline__ bool squares_overflow(float sq, float mean, float factor) {
   return sq == INFINITY && fabsf(mean) < INFINITY && factor == 1.0f;
 }
+// The mean as one sum gives it; the product as it is rounded, everywhere:
+// contracted into a difference it would be another mean there.
+__device__ __forceinline__ float first_mean(float sum, float inv_dim) { return fresh(sum * inv_dim); }
+// That mean is off by roundings of its own size: the 30 values 1e4 had a mean of
+// 10000.001, and y 0.3 for 0.  Where it is larger than the spread, the mean of
+// the differences from it, whose roundings are of the spread's size, is taken out
+// of it and of them.  Smaller means are off by no more than the differences are
+// (16384 rows of 4096 bf16: 46.9 us, with that sum in every row 49.0; rows that
+// all need it: 16384 of 8000 bf16 100 us for 95, 8192 of 30000 248 for 225).
+__device__ __forceinline__ bool mean_is_large(float first, float sq, float inv_dim, float factor) {
+  const float m = first * factor;
+  return m * m > sq * inv_dim;
+}
+struct Centre {
+  float mean, rstd;
+  float shift;  // xhat = (x - first mean) * rstd + shift
+};
+// sq: of the differences scaled by `factor`; off: the mean of the differences.
+__device__ __forceinline__ Centre centre(float first, float off, float sq, float inv_dim, float eps, float factor) {
+  const float d = off * factor;
+  const float left = fmaf(-d, d, sq * inv_dim), var = left < 0.0f ? 0.0f : left;  // a NaN stays
+  const float rstd = factor / sqrtf(var + eps * factor * factor);
+  return {first + off, rstd, -off * rstd};
+}
 
 // G lanes share R rows; each holds EPL elements of each, vectors of E at
 // (j * G + lane) * E.  Up to G = 64 a row is in one wave: no barrier, and
 // several groups in a workgroup.  A lane's rows share the weights' loads.
+// Single rows of 16 elements a lane are the few ones: eight waves to a SIMD, all
+// of a CU's at once (2048 rows of 4096 fp32: 11.7 us, with seven 14.2).
 template <class T, class W, int G, int EPL, int R>
-__global__ __launch_bounds__(G > 64 ? G : kThreads) void norm_kernel(NormArgs a) {
+__global__ __launch_bounds__(G > 64 ? G : kThreads, R == 1 && EPL == 16 && G <= 256 ? 8 : 1) void norm_kernel(NormArgs a) {
   constexpr int E = 16 / sizeof(T);
   constexpr int V = EPL / E;
   constexpr int kGroups = G > 64 ? 1 : kThreads / G;
@@ -65,21 +92,23 @@ __global__ __launch_bounds__(G > 64 ? G : kThreads) void norm_kernel(NormArgs a)
     }
   }
   group_sum<G, R>(sum, slots[0]);
-  float mean[R], sq[R], factor[R];
+  float first[R], sq[R], off[R], factor[R];
 #pragma unroll
   for (int k = 0; k < R; ++k) {
-    mean[k] = sum[k] * inv_dim;
+    first[k] = first_mean(sum[k], inv_dim);
     factor[k] = 1.0f;
+    off[k] = 0.0f;
   }
 
-  for (int turn = 1;; turn = 0) {
+  int turn = 1;
+  for (;; turn = 0) {
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       sq[k] = 0.0f;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const uint32_t e = (j * G + lane) * E;
-        const typename X::wide f = (widen<T, E>(raw[k][j]) - mean[k]) * factor[k];
+        const typename X::wide f = (widen<T, E>(raw[k][j]) - first[k]) * factor[k];
         if (e + E <= dim) {
 #pragma unroll
           for (int i = 0; i < E; ++i) sq[k] = fmaf(f[i], f[i], sq[k]);
@@ -94,19 +123,44 @@ __global__ __launch_bounds__(G > 64 ? G : kThreads) void norm_kernel(NormArgs a)
     bool over = false;
 #pragma unroll
     for (int k = 0; k < R; ++k)
-      if (squares_overflow(sq[k], mean[k], factor[k])) {
+      if (squares_overflow(sq[k], first[k], factor[k])) {
         factor[k] = kScaleDown;
         over = true;
       }
     if (!over) break;
   }
-  float rstd[R];
+  // The same for all the lanes of a row, and for a workgroup where they exchange.
+  bool any = false;
+#pragma unroll
+  for (int k = 0; k < R; ++k) any = any || mean_is_large(first[k], sq[k], inv_dim, factor[k]);
+  if (any) {
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const typename X::wide f = widen<T, E>(raw[k][j]) - first[k];
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          if ((j * G + lane) * E + i < dim) off[k] += f[i];
+      }
+    group_sum<G, R>(off, slots[turn ^ 1]);
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      off[k] = mean_is_large(first[k], sq[k], inv_dim, factor[k]) ? off[k] * inv_dim : 0.0f;
+  }
+  // Widened anew from here on: kept over the branch in 32 bits, a row takes twice
+  // the registers (16384 rows of 8000 bf16: 102 us, so 95).
+#pragma unroll
+  for (int k = 0; k < R; ++k)
+#pragma unroll
+    for (int j = 0; j < V; ++j) raw[k][j] = fresh(raw[k][j]);
+  Centre c[R];
 #pragma unroll
   for (int k = 0; k < R; ++k) {
-    rstd[k] = factor[k] / sqrtf(sq[k] * inv_dim + a.eps * factor[k] * factor[k]);
+    c[k] = centre(first[k], off[k], sq[k], inv_dim, a.eps, factor[k]);
     if (lane == 0 && row + k < a.rows) {
-      if (a.mean != nullptr) a.mean[row + k] = mean[k];
-      if (a.rstd != nullptr) a.rstd[row + k] = rstd[k];
+      if (a.mean != nullptr) a.mean[row + k] = c[k].mean;
+      if (a.rstd != nullptr) a.rstd[row + k] = c[k].rstd;
     }
   }
 
@@ -136,7 +190,7 @@ __global__ __launch_bounds__(G > 64 ? G : kThreads) void norm_kernel(NormArgs a)
           a.scales[(row + k) * ck_blocks(a.dim) + e / kCkBlock] = static_cast<uint8_t>(byte);
       }
 #pragma unroll
-      for (int i = 0; i < E; ++i) f[i] = (f[i] - mean[k]) * rstd[k] * weight[i] + bias[i];
+      for (int i = 0; i < E; ++i) f[i] = fmaf(f[i] - first[k], c[k].rstd, c[k].shift) * weight[i] + bias[i];
       store_row<T, E>(static_cast<T*>(a.y) + (row + k) * a.y_stride, e, dim, narrow<T, E>(f));
     }
   }
@@ -163,25 +217,36 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
     for (int i = 0; i < E; ++i) sum[0] += f[i];
   }
   group_sum<1024, 1>(sum, slots[0]);
-  const float mean = sum[0] * inv_dim;
+  const float first = first_mean(sum[0], inv_dim);
 
-  float sq[1], factor = 1.0f;
-  for (int turn = 1;; turn = 0) {
+  float sq[1], off[1] = {0.0f}, factor = 1.0f;
+  int turn = 1;
+  for (;; turn = 0) {
     sq[0] = 0.0f;
     for (uint32_t e = threadIdx.x * E; e < dim; e += kStep) {
-      const typename X::wide f = (widen<T, E>(load_row<T, E, false>(x, e, dim)) - mean) * factor;
+      const typename X::wide f = (widen<T, E>(load_row<T, E, false>(x, e, dim)) - first) * factor;
 #pragma unroll
       for (int i = 0; i < E; ++i)
         if (e + i < dim) sq[0] = fmaf(f[i], f[i], sq[0]);
     }
     group_sum<1024, 1>(sq, slots[turn]);
-    if (!squares_overflow(sq[0], mean, factor)) break;
+    if (!squares_overflow(sq[0], first, factor)) break;
     factor = kScaleDown;
   }
-  const float rstd = factor / sqrtf(sq[0] * inv_dim + a.eps * factor * factor);
+  if (mean_is_large(first, sq[0], inv_dim, factor)) {  // the same for the workgroup
+    for (uint32_t e = threadIdx.x * E; e < dim; e += kStep) {
+      const typename X::wide f = widen<T, E>(load_row<T, E, false>(x, e, dim)) - first;
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (e + i < dim) off[0] += f[i];
+    }
+    group_sum<1024, 1>(off, slots[turn ^ 1]);
+    off[0] *= inv_dim;
+  }
+  const Centre c = centre(first, off[0], sq[0], inv_dim, a.eps, factor);
   if (threadIdx.x == 0) {
-    if (a.mean != nullptr) a.mean[row] = mean;
-    if (a.rstd != nullptr) a.rstd[row] = rstd;
+    if (a.mean != nullptr) a.mean[row] = c.mean;
+    if (a.rstd != nullptr) a.rstd[row] = c.rstd;
   }
   const W* w = static_cast<const W*>(a.weight);
   const W* b = static_cast<const W*>(a.bias);
@@ -203,7 +268,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
       if (e % kCkBlock == 0 && e < dim) a.scales[row * ck_blocks(a.dim) + e / kCkBlock] = static_cast<uint8_t>(byte);
     }
 #pragma unroll
-    for (int i = 0; i < E; ++i) f[i] = (f[i] - mean) * rstd;
+    for (int i = 0; i < E; ++i) f[i] = fmaf(f[i] - first, c.rstd, c.shift);
     if (w != nullptr) f *= widen<W, E>(load_row<W, E, false>(w, e, dim));
     if (b != nullptr) f += widen<W, E>(load_row<W, E, false>(b, e, dim));
     store_row<T, E>(y, e, dim, narrow<T, E>(f));

@@ -182,3 +182,61 @@ def test_rows_of_one_far_value_are_uniform(zt, value, vocab):
     e = there / n * so.U * 16 * (3 + 10) + 2 * so.U * hit
     so.close(dz, want, e + 1.01 * so.rounding(want, zt), "dlogits")
     assert torch.equal(p.entropy.cpu() > 0, torch.ones(3, dtype=torch.bool))
+
+
+# --------------------------------------------------- rows around a large mean
+def layer_norm_bounds(x, w, b, eps):
+    """((y, mean, rstd), their bounds) in which the mean's size counts in its own last rounding and in products with U^2 alone."""
+    x = x.double()
+    d = x.shape[1]
+    n = d / 64 + 64                                          # additions one after another
+    eps = float(torch.tensor(eps, dtype=F32))
+    mean = x.mean(1, keepdim=True)
+    c = x - mean
+    var = c.square().mean(1, keepdim=True)
+    rstd = (var + eps).rsqrt()
+    w = torch.ones(d, dtype=torch.float64) if w is None else w.double()
+    b = torch.zeros(d, dtype=torch.float64) if b is None else b.double()
+    y = c * rstd * w + b
+    e0 = (n + 3) * so.U * x.abs().mean(1, keepdim=True)      # a mean from one sum is off by that
+    e_mean = (n + 4) * so.U * (c.abs().mean(1, keepdim=True) + e0)       # the mean of the differences from it
+    e_c = e_mean + 3 * so.U * (c.abs() + e0)
+    e_var = (n + 6) * so.U * (var + e0.square()) + 2 * e0 * e_mean + e_mean.square()
+    most, least = ((var - e_var).clamp(min=0) + eps).rsqrt(), (var + e_var + eps).rsqrt()
+    e_rstd = torch.maximum(most - rstd, rstd - least) + 4 * so.U * most
+    e_y = w.abs() * (c.abs() * e_rstd + e_c * (rstd + e_rstd)) + 3 * so.U * ((w * c * rstd).abs() + b.abs())
+    return (y, mean[:, 0], rstd[:, 0]), (e_y, e_mean[:, 0], e_rstd[:, 0])
+
+
+@pytest.mark.parametrize("rows,dim", [(5, 2), (9, 26), (9, 30), (6, 61), (4200, 117), (7, 300), (5, 1000), (6, 2047), (4097, 3001),
+                                      (3, 6000), (3, 11000), (2, 16385), (2, 40001)])
+@pytest.mark.parametrize("xt,level,spread", [(F32, 1e4, 0.0), (F32, 1e4, 0.01), (F32, -3e6, 2.0), (F32, 0.1, 0.0), (F32, 1e17, 1e16), (F32, 1e20, 1e19),
+                                             (F16, 6e4, 0.0), (F16, 1000.0, 1.0), (BF16, 59904.0, 0.0), (BF16, -256.0, 2.0)])
+def test_layer_norm_around_a_large_mean(xt, level, spread, rows, dim):
+    g = gen(dim)
+    few = min(rows, 9)  # more rows repeat these
+    x = (level + torch.randn(few, dim, generator=g, dtype=torch.float64) * spread).to(xt)
+    w, b = (torch.randn(dim, generator=g) * 0.3 + 1).to(xt), (torch.randn(dim, generator=g) * 0.3).to(xt)
+    say("layer_norm around a mean", xt, level, spread, rows, dim)
+    y, mean, rstd = rsx.layer_norm(x.repeat(-(-rows // few), 1)[:rows].contiguous().to(DEV), w.to(DEV), b.to(DEV))
+    (ry, rm, rr), (ty, tm, tr) = layer_norm_bounds(x, w, b, 1e-5)
+    for at in (0, rows - few):
+        part = slice(at, at + few)
+        back = torch.arange(at, at + few) % few
+        so.close(mean[part], rm[back], (tm + 1.01 * so.rounding(rm, F32))[back], "mean")
+        so.close(rstd[part], rr[back], (tr + 1.01 * so.rounding(rr, F32))[back], "rstd")
+        so.close(y[part], ry[back], (ty + 1.01 * so.rounding(ry, xt))[back], "y")
+
+
+@pytest.mark.parametrize("rows,dim", [(4, 3), (4, 40), (4099, 200), (4, 3000), (4, 9000), (3, 33000)])
+def test_layer_norm_statistics_of_rows_without_a_mean(rows, dim):
+    x = torch.randn(rows, dim, generator=gen(dim))
+    x[0, dim // 2], x[1, 0], x[2, dim - 1] = math.inf, math.nan, -math.inf
+    say("layer_norm with infinities", rows, dim)
+    y, mean, rstd = rsx.layer_norm(x.to(DEV))
+    assert torch.isnan(y[:3]).all() and torch.isnan(rstd[:3]).all()
+    assert mean[:3].tolist()[::2] == [math.inf, -math.inf] and math.isnan(mean[1].item())
+    (ry, rm, rr), (ty, tm, tr) = layer_norm_bounds(x[3:], None, None, 1e-5)
+    if rows > 3:
+        so.close(y[3:], ry, ty + 1.01 * so.rounding(ry, F32), "y")
+        so.close(rstd[3:], rr, tr + 1.01 * so.rounding(rr, F32), "rstd")
