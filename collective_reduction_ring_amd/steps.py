@@ -91,6 +91,14 @@ def _current_stream(index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(index)
 
 
+def _as_stream(stream, device):
+    """The stream object of a handle."""
+    if not isinstance(stream, int):
+        return stream
+    # ExternalStream takes a handle of 0 for none, and makes a stream of its own.
+    return torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -133,10 +141,7 @@ class _Plan:
     def _use_on(self, stream, handle: int) -> None:
         # Memory freed after this call may be given out again on the stream it
         # was allocated on: the allocator has to know of this one's work.
-        if stream is None:
-            stream = torch.cuda.current_stream()
-        elif isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(handle, device=self.device)
+        stream = torch.cuda.current_stream() if stream is None else _as_stream(stream, self.device)
         for t in self.keep:
             t.record_stream(stream)
 

@@ -1,7 +1,8 @@
 """The training-step operators without a GPU: further refusals, and what a plan does before its call."""
 import pytest
+import torch
 
-from collective_reduction_ring_amd import _lib as L
+from collective_reduction_ring_amd import _lib as L, steps
 from test_abi import fake_ptrs
 from test_steps import A, BAD, ALIAS, F32, I64, OK, call
 
@@ -22,3 +23,26 @@ def grad_rest(z=A(1), tokens=A(2), lse=A(3), lse_rest=A(8), ent=A(4), g=A(5), h=
                          ids=lambda v: v.__name__ if callable(v) else str(v))
 def test_refusals_of_the_forms_that_keep_the_rest(fn, kw, want):
     assert fn(**kw) == want
+
+
+# ---- streams, with stand-ins for them and for tensors
+class FakeTensor:
+    device = torch.device("cuda:0")
+
+    def __init__(self):
+        self.recorded = []
+
+    def record_stream(self, s):
+        self.recorded.append(s)
+
+
+@pytest.mark.parametrize("handle", [0, 77])
+def test_a_handle_of_0_is_the_default_stream(handle, monkeypatch):
+    """A plan's memory is held for the stream of the call, not for one that 0 would make anew."""
+    default, other = object(), object()
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: default)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda ptr, device=None: other)
+    plan = steps._Plan()
+    plan.device, plan.keep = FakeTensor.device, [FakeTensor()]
+    plan._use_on(handle, handle)
+    assert plan.keep[0].recorded == [default if handle == 0 else other]
