@@ -9,6 +9,12 @@ kernels on the current stream (or ``stream``) and returns at once.  Tensors
 may be refilled between calls.  The functions of the same names in lower case
 prepare, call once and return the outputs.
 
+What a plan allocates belongs to the stream that is current when it is made: a
+first call on another stream has to be ordered after that one, as for any tensor
+made there.  A plan has one workspace, so its calls are not for two streams at
+once.  The functions with ``stream`` make their outputs and workspaces on that
+stream; inputs have to be ready there.
+
 Matrices are tensors whose last dimension is the row; the leading ones have to
 fold into one row stride, so a column slice of a wider matrix is fine.  Rows
 that are only read may be expanded (stride 0).  Nothing here records autograd
@@ -144,6 +150,27 @@ class _Plan:
         stream = torch.cuda.current_stream() if stream is None else _as_stream(stream, self.device)
         for t in self.keep:
             t.record_stream(stream)
+
+
+def _once(tensor, stream, make) -> _Plan:
+    """The plan that ``make`` gives, called on ``stream``; ``tensor`` is on its device."""
+    device = getattr(tensor, "device", None)
+    if stream is None or device is None or device.type != "cuda":  # the latter two are refused
+        plan = make()
+        plan(stream)
+        return plan
+    # Memory from the current stream's pool may have its last user still to run
+    # there: outputs and workspace come from the pool of the stream that writes
+    # them.  Either stream's work holds on to all of it.
+    home = torch.cuda.current_stream(device)
+    stream = _as_stream(stream, device)
+    with torch.cuda.stream(stream):
+        plan = make()
+        plan(stream)
+    for t in plan.keep:
+        t.record_stream(stream)
+        t.record_stream(home)
+    return plan
 
 
 class Embedding(_Plan):
@@ -395,54 +422,42 @@ class TokenLogprobsGrad(_Plan):
 
 def embedding(table, tokens, out=None, scale: float = 1.0, first: int = 0, stream=None):
     """The rows of ``table`` that ``tokens`` name, scaled; see ``Embedding``."""
-    p = Embedding(table, tokens, out, scale, first)
-    p(stream)
-    return p.out
+    return _once(table, stream, lambda: Embedding(table, tokens, out, scale, first)).out
 
 
 def embedding_grad(dout, tokens, grad, scale: float = 1.0, first: int = 0, accumulate: bool = False, stream=None):
     """The table's gradient, into ``grad``; see ``EmbeddingGrad``."""
-    EmbeddingGrad(dout, tokens, grad, scale, first, accumulate)(stream)
-    return grad
+    return _once(grad, stream, lambda: EmbeddingGrad(dout, tokens, grad, scale, first, accumulate)).grad
 
 
 def layer_norm(x, weight=None, bias=None, out=None, eps: float = 1e-5, checkpoint: Checkpoint | None = None, stream=None):
     """(out, mean, rstd) of a layer norm; see ``LayerNorm``."""
-    p = LayerNorm(x, weight, bias, out, eps, checkpoint)
-    p(stream)
+    p = _once(x, stream, lambda: LayerNorm(x, weight, bias, out, eps, checkpoint))
     return p.out, p.mean, p.rstd
 
 
 def layer_norm_grad(dout, x, mean, rstd, weight=None, dx=None, dweight=None, dbias=None, weights: bool = True, stream=None):
     """(dx, dweight, dbias) of a layer norm; see ``LayerNormGrad``."""
-    p = LayerNormGrad(dout, x, mean, rstd, weight, dx, dweight, dbias, weights)
-    p(stream)
+    p = _once(dout, stream, lambda: LayerNormGrad(dout, x, mean, rstd, weight, dx, dweight, dbias, weights))
     return p.dx, p.dweight, p.dbias
 
 
 def checkpoint_pack(x, checkpoint: Checkpoint | None = None, stream=None) -> Checkpoint:
     """x in 8 bits; see ``Checkpoint``."""
-    p = CheckpointPack(x, checkpoint)
-    p(stream)
-    return p.checkpoint
+    return _once(x, stream, lambda: CheckpointPack(x, checkpoint)).checkpoint
 
 
 def checkpoint_unpack(checkpoint: Checkpoint, out=None, dtype=None, stream=None):
     """The values of a checkpoint, float32 unless ``out`` or ``dtype`` says otherwise."""
-    p = CheckpointUnpack(checkpoint, out, dtype)
-    p(stream)
-    return p.out
+    return _once(checkpoint, stream, lambda: CheckpointUnpack(checkpoint, out, dtype)).out
 
 
 def token_logprobs(logits, tokens, top: int = 0, stream=None) -> TokenLogprobs:
     """One pass over ``logits``; returns the plan, whose fields hold the results."""
-    p = TokenLogprobs(logits, tokens, top)
-    p(stream)
-    return p
+    return _once(logits, stream, lambda: TokenLogprobs(logits, tokens, top))
 
 
 def token_logprobs_grad(logits, tokens, lse, dlogprob, entropy=None, dentropy=None, dlogits=None, stream=None, lse_rest=None):
     """The gradient in the logits; see ``TokenLogprobsGrad``."""
-    p = TokenLogprobsGrad(logits, tokens, lse, dlogprob, entropy, dentropy, dlogits, lse_rest)
-    p(stream)
-    return p.dlogits
+    return _once(logits, stream, lambda: TokenLogprobsGrad(logits, tokens, lse, dlogprob, entropy, dentropy, dlogits,
+                                                           lse_rest)).dlogits

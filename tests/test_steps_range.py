@@ -1,4 +1,6 @@
 """The training-step operators without a GPU: further refusals, and what a plan does before its call."""
+import contextlib
+
 import pytest
 import torch
 
@@ -25,7 +27,7 @@ def test_refusals_of_the_forms_that_keep_the_rest(fn, kw, want):
     assert fn(**kw) == want
 
 
-# ---- streams, with stand-ins for them and for tensors
+# ---- streams, with stand-ins for them, for tensors and for plans
 class FakeTensor:
     device = torch.device("cuda:0")
 
@@ -46,3 +48,57 @@ def test_a_handle_of_0_is_the_default_stream(handle, monkeypatch):
     plan.device, plan.keep = FakeTensor.device, [FakeTensor()]
     plan._use_on(handle, handle)
     assert plan.keep[0].recorded == [default if handle == 0 else other]
+
+
+class FakePlan:
+    """Notes the stream that is current when it is made, and the one that it is called on."""
+
+    def __init__(self, *args, **kw):
+        self.made_on, self.called_on = FakePlan.current, None
+        self.keep = [FakePlan.mine]
+        self.out = self.grad = self.mean = self.rstd = self.dx = self.dweight = self.dbias = self.checkpoint = self.dlogits = None
+        FakePlan.plans.append(self)
+
+    def __call__(self, stream=None):
+        self.called_on = stream
+
+
+FUNCTIONS = {"embedding": ("Embedding", 2), "embedding_grad": ("EmbeddingGrad", 3), "layer_norm": ("LayerNorm", 1),
+             "layer_norm_grad": ("LayerNormGrad", 4), "checkpoint_pack": ("CheckpointPack", 1),
+             "checkpoint_unpack": ("CheckpointUnpack", 1), "token_logprobs": ("TokenLogprobs", 2),
+             "token_logprobs_grad": ("TokenLogprobsGrad", 4)}
+
+
+@pytest.mark.parametrize("given", ["object", "handle", "default"])
+@pytest.mark.parametrize("name", FUNCTIONS)
+def test_a_functions_memory_is_of_the_stream_it_runs_on(name, given, monkeypatch):
+    """Outputs and workspace from another stream's pool could still be in use there."""
+    class Stream:
+        cuda_stream = 77
+
+    home, default, wanted = object(), object(), Stream()
+
+    @contextlib.contextmanager
+    def use(s):
+        FakePlan.current, before = s, FakePlan.current
+        yield
+        FakePlan.current = before
+
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: home)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: default)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda ptr, device=None: wanted if ptr == 77 else None)
+    cls, n = FUNCTIONS[name]
+    monkeypatch.setattr(steps, cls, FakePlan)
+    FakePlan.current, FakePlan.plans, FakePlan.mine = home, [], FakeTensor()
+    args = [FakeTensor() for _ in range(n)]
+    stream, want = {"object": (wanted, wanted), "handle": (77, wanted), "default": (0, default)}[given]
+    getattr(steps, name)(*args, stream=stream)
+    p, = FakePlan.plans
+    assert p.made_on is want and p.called_on is want
+    assert want in p.keep[0].recorded and home in p.keep[0].recorded
+    # without a stream, the current one: nothing to record
+    FakePlan.plans, FakePlan.mine = [], FakeTensor()
+    getattr(steps, name)(*args)
+    p, = FakePlan.plans
+    assert p.made_on is home and p.called_on is None and not p.keep[0].recorded

@@ -240,3 +240,39 @@ def test_layer_norm_statistics_of_rows_without_a_mean(rows, dim):
     if rows > 3:
         so.close(y[3:], ry, ty + 1.01 * so.rounding(ry, F32), "y")
         so.close(rstd[3:], rr, tr + 1.01 * so.rounding(rr, F32), "rstd")
+
+
+# ------------------------------------------------------- another stream's memory
+@pytest.mark.parametrize("given", ["object", "handle"])
+def test_functions_on_a_stream_take_no_memory_from_the_current_one(given):
+    """A block just freed on the current stream may still be written there; a call on another one must not be given it."""
+    rows, dim = 3000, 1000
+    g = gen(6)
+    x, dy = torch.randn(rows, dim, generator=g).to(DEV), torch.randn(rows, dim, generator=g).to(DEV)
+    tok = torch.randint(0, dim, (rows,), generator=g).to(DEV)
+    want = rsx.layer_norm(x)
+    back = rsx.layer_norm_grad(dy, x, *want[1:])
+    lp = rsx.token_logprobs(x, tok, 3)
+    dz = rsx.token_logprobs_grad(x, tok, lp.lse, lp.logprob, lse_rest=lp.lse_rest)
+    rows_of = rsx.embedding(x, tok)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    arg = s if given == "object" else s.cuda_stream
+    torch.cuda.synchronize()
+    freed = [torch.empty(rows, dim, device=DEV) for _ in range(3)]
+    taken = {t.data_ptr() for t in freed}
+    del freed
+    got = rsx.layer_norm(x, stream=arg)
+    b = rsx.layer_norm_grad(dy, x, *got[1:], stream=arg)
+    l2 = rsx.token_logprobs(x, tok, 3, stream=arg)
+    d2 = rsx.token_logprobs_grad(x, tok, l2.lse, l2.logprob, stream=arg, lse_rest=l2.lse_rest)
+    r2 = rsx.embedding(x, tok, stream=arg)
+    assert not taken & {t.data_ptr() for t in (got[0], b[0], d2, r2)}
+    torch.cuda.current_stream().wait_stream(s)
+    for a, c in zip((*want, *back, lp.logprob, lp.top_token, dz, rows_of), (*got, *b, l2.logprob, l2.top_token, d2, r2)):
+        assert torch.equal(a, c)
+    # handle 0 is the default stream, from any other
+    with torch.cuda.stream(s):
+        y = rsx.layer_norm(x, stream=0)[0]
+    torch.cuda.synchronize()
+    assert torch.equal(y, want[0])
