@@ -525,8 +525,10 @@ __global__ __launch_bounds__(kThreads) void norm_columns_kernel(NormGradArgs a, 
   constexpr int E = 16 / sizeof(T);
   typedef Vec<T, E> X;
   const uint32_t dim = static_cast<uint32_t>(a.dim);
-  const uint32_t e = (blockIdx.x % column_groups * kThreads + threadIdx.x) * E;
-  const uint32_t p = blockIdx.x / column_groups;
+  const uint32_t block = static_cast<uint32_t>(block_id());  // below 2^30
+  const uint32_t e = (block % column_groups * kThreads + threadIdx.x) * E;
+  const uint32_t p = block / column_groups;
+  if (p >= parts) return;
   typename X::wide dw = 0.0f, db = 0.0f;
   for (uint64_t row = p; row < a.rows; row += parts) {
     const typename X::wide d = widen<T, E>(load_row<T, E>(static_cast<const T*>(a.dy) + row * a.dy_stride, e, dim));
@@ -541,19 +543,20 @@ __global__ __launch_bounds__(kThreads) void norm_columns_kernel(NormGradArgs a, 
   store_row<float, E>(part + pitch, e, dim, db);
 }
 
-// dw and db from the workgroups' partial rows: 32 columns a workgroup, in 32
-// parts of the rows; no rows at all give zeros.
+// dw (the first half of the workgroups) and db from the partial rows: 32 columns
+// a workgroup, in 32 parts of the rows; no rows at all give zeros.
 template <class W>
 __global__ __launch_bounds__(1024) void norm_sum_kernel(const float* partial, uint32_t pitch, uint32_t parts,
                                                         uint32_t dim, W* dweight, W* dbias) {
   __shared__ float join[32][33];
-  W* out = blockIdx.y == 0 ? dweight : dbias;
+  const uint32_t block = static_cast<uint32_t>(block_id()), groups = (dim + 31) / 32, which = block < groups ? 0u : 1u;
+  W* out = which == 0 ? dweight : dbias;
   if (out == nullptr) return;
   const uint32_t column = threadIdx.x % 32, slice = threadIdx.x / 32;
-  const uint32_t e = blockIdx.x * 32 + column;
+  const uint32_t e = (block - which * groups) * 32 + column;
   float t = 0.0f;
   if (e < dim) {
-    const float* p = partial + blockIdx.y * pitch + e;
+    const float* p = partial + static_cast<uint64_t>(which) * pitch + e;
 #pragma unroll 16
     for (uint32_t r = slice; r < parts; r += 32) t += p[static_cast<uint64_t>(r) * 2 * pitch];
   }
@@ -718,7 +721,8 @@ hipError_t grad_long(const NormGradArgs& a, uint32_t pitch, uint32_t* parts, hip
   *parts = grad_parts(a.rows);
   const uint32_t per = kThreads * (16 / sizeof(T));
   const uint32_t columns = static_cast<uint32_t>((a.dim + per - 1) / per);
-  const hipError_t e = launch(norm_columns_kernel<T, CK>, dim3(columns * *parts), kThreads, 0, s, a, pitch, *parts, columns);
+  const hipError_t e = launch(norm_columns_kernel<T, CK>, grid_of(static_cast<uint64_t>(columns) * *parts), kThreads, 0, s, a,
+                              pitch, *parts, columns);
   if (e != hipSuccess) return e;
   return launch(norm_grad_long_kernel<T, W, CK>, grid_of(a.rows), 1024, 0, s, a);
 }
@@ -753,8 +757,8 @@ hipError_t norm_grad(const NormGradArgs& a, hipStream_t s) {
     }
   }
   if (e != hipSuccess || (a.dweight == nullptr && a.dbias == nullptr)) return e;
-  return launch(norm_sum_kernel<W>, dim3(static_cast<uint32_t>((a.dim + 31) / 32), 2), 1024, 0, s, a.partial, pitch,
-                parts, static_cast<uint32_t>(a.dim), static_cast<W*>(a.dweight), static_cast<W*>(a.dbias));
+  return launch(norm_sum_kernel<W>, grid_of((a.dim + 31) / 32 * 2), 1024, 0, s, a.partial, pitch, parts,
+                static_cast<uint32_t>(a.dim), static_cast<W*>(a.dweight), static_cast<W*>(a.dbias));
 }
 
 template <class T, class W>

@@ -276,3 +276,51 @@ def test_functions_on_a_stream_take_no_memory_from_the_current_one(given):
         y = rsx.layer_norm(x, stream=0)[0]
     torch.cuda.synchronize()
     assert torch.equal(y, want[0])
+
+
+# ------------------------------------------------------- rows of 2^25 and more elements
+def test_layer_norm_gradient_of_a_row_beyond_2_27_elements():
+    """The launches' work-items pass 32 bits."""
+    dim = 2 ** 27 + 5
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x, dy = torch.randn(1, dim, generator=g, device=DEV).bfloat16(), torch.randn(1, dim, generator=g, device=DEV).bfloat16()
+    say("layer_norm_grad of", dim)
+    dx, dw, db = rsx.layer_norm_grad(dy, x, torch.full((1,), 0.5, device=DEV), torch.full((1,), 2.0, device=DEV))
+    assert torch.equal(db, dy[0])                            # a sum of one; zeros of either sign are equal
+    xhat = (x[0].float() - 0.5) * 2
+    assert torch.equal(dw, (dy[0].float() * xhat).bfloat16())
+    c1, c2 = dy[0].double().mean(), (dy[0].double() * xhat.double()).mean()
+    want = 2 * (dy[0].float() - c1.float() - xhat * c2.float())
+    # additions one after another: the row's share of a lane, and the lanes; means of terms of about 1 and 4
+    tol = (dim / 2 ** 13 + 80) * so.U * 2 * (1 + 4 * xhat.abs()) + 8 * so.U * (1 + dy[0].float().abs() + xhat.abs())
+    assert ((dx[0].float() - want).abs() <= tol + 1.01 * so.rounding(want, BF16)).all()
+
+
+@pytest.mark.skipif(not torch.cuda.is_available() or torch.cuda.mem_get_info()[1] < 240 << 30, reason="needs 205 GiB")
+def test_layer_norm_gradient_of_many_rows_of_2_25_elements():
+    """512 rows, expanded: the columns' pass has more work-items than 32 bits count."""
+    rows, dim = 512, 2 ** 25 + 3
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 205 << 30:
+        pytest.skip("needs 205 GiB free")
+    g = torch.Generator(device=DEV).manual_seed(4)
+    x, dy = torch.randn(1, dim, generator=g, device=DEV), torch.randn(1, dim, generator=g, device=DEV)
+    rstd = torch.linspace(0.5, 1.5, rows, device=DEV)
+    say("layer_norm_grad of", rows, dim)
+    dx, dw, db = rsx.layer_norm_grad(dy.expand(rows, dim), x.expand(rows, dim), torch.zeros(rows, device=DEV), rstd)
+    total = rstd.double().sum()
+    for a in range(0, dim, 1 << 22):                         # in pieces: 64 bits
+        part = slice(a, min(a + (1 << 22), dim))
+        d, v = dy[0, part].double(), x[0, part].double()
+        assert ((dw[part] - d * v * total).abs() <= (rows + 8) * so.U * (d * v).abs() * total).all()
+        assert ((db[part] - d * rows).abs() <= (rows + 4) * so.U * d.abs() * rows).all()
+    c1, c2 = dy.double().mean(), (dy.double() * x.double()).mean()
+    for r in (0, 1, 255, rows - 1):
+        k = rstd[r].double()
+        for a in (0, dim // 2, dim - (1 << 20)):
+            d, v = dy[0, a:a + (1 << 20)].double(), x[0, a:a + (1 << 20)].double() * k
+            want = k * (d - c1 - v * c2 * k)
+            tol = (dim / 2 ** 12 + 80) * so.U * k * (1 + 2 * v.abs()) + 8 * so.U * (1 + d.abs() + v.abs())
+            assert ((dx[r, a:a + (1 << 20)] - want).abs() <= tol + so.rounding(want, F32)).all()
+    del dx, dw, db
+    torch.cuda.empty_cache()
