@@ -12,6 +12,9 @@ size_t float_size(int t) {
 }
 size_t token_size(int t) { return t == RSX_INT32 ? 4 : t == RSX_INT64 ? 8 : 0; }
 
+// Ids first .. first + vocab - 1 are token ids; past the largest they would wrap.
+bool ids_wrap(int64_t first, size_t vocab) { return vocab != 0 && first > INT64_MAX - static_cast<int64_t>(vocab - 1); }
+
 // A buffer as rows of `width` bytes, `pitch` bytes apart.
 struct Area {
   uintptr_t lo, hi;
@@ -100,6 +103,7 @@ rsx_status_t rsx_embedding(const void* table, size_t table_stride, size_t vocab,
   const size_t ts = float_size(table_type), os = float_size(out_type), is = token_size(token_type);
   if (ts == 0 || os == 0 || is == 0) return RSX_ERR_INVALID_TYPE;
   if (vocab > kMaxSize || dim > kMaxSize || ntokens > kMaxSize) return RSX_ERR_UNSUPPORTED;
+  if (ids_wrap(first, vocab)) return RSX_ERR_INVALID_ARGUMENT;
   Areas m;
   m.read(table, vocab, dim, table_stride, ts);
   m.read_flat(tokens, ntokens, is);
@@ -124,6 +128,7 @@ rsx_status_t rsx_embedding_grad(const void* dout, size_t dout_stride, rsx_dtype_
   const size_t ds = float_size(dout_type), gs = float_size(grad_type), is = token_size(token_type);
   if (ds == 0 || gs == 0 || is == 0) return RSX_ERR_INVALID_TYPE;
   if (vocab > kMaxSize || dim > kMaxSize || ntokens > kMaxSize) return RSX_ERR_UNSUPPORTED;
+  if (ids_wrap(first, vocab)) return RSX_ERR_INVALID_ARGUMENT;
   Areas m;
   m.write(grad, vocab, dim, grad_stride, gs);
   m.read(dout, ntokens, dim, dout_stride, ds);

@@ -91,6 +91,13 @@ def _tokens(t, what: str, device, shape=None):
     return t
 
 
+def _first(first, vocab: int) -> int:
+    first = int(first)
+    if not -2 ** 63 <= first <= 2 ** 63 - max(vocab, 1):
+        raise ValueError(f"first={first}: the ids of {vocab} rows from there leave 64 bits")
+    return first
+
+
 def _current_stream(index: int) -> int:
     # The handle alone: torch.cuda.current_stream() makes an object of it, which
     # took 2.7 of a small call's 6.4 us (this: 0.1).
@@ -195,7 +202,7 @@ class Embedding(_Plan):
         _, _, os_, ot = _rows(out, "out", device=dev, shape=shape, output=True)
         self.out = out
         self._prepare("rsx_embedding", dev, (_ptr(table), ts, vocab, dim, tt, _ptr(tokens), tokens.numel(),
-                                             TOKENS[tokens.dtype], int(first), float(scale), _ptr(out), os_, ot),
+                                             TOKENS[tokens.dtype], _first(first, vocab), float(scale), _ptr(out), os_, ot),
                       (table, tokens, out))
 
 
@@ -216,9 +223,9 @@ class EmbeddingGrad(_Plan):
         n = tokens.numel()
         ws, wb, self._ws = self._workspace(L.lib().rsx_embedding_grad_workspace_size(n, vocab, dim), dev)
         self.grad = grad
-        self._prepare("rsx_embedding_grad", dev, (_ptr(dout), ds, dt, _ptr(tokens), n, TOKENS[tokens.dtype], int(first),
-                                                  float(scale), _ptr(grad), gs, vocab, dim, gt, int(bool(accumulate)),
-                                                  ws, wb),
+        self._prepare("rsx_embedding_grad", dev, (_ptr(dout), ds, dt, _ptr(tokens), n, TOKENS[tokens.dtype],
+                                                  _first(first, vocab), float(scale), _ptr(grad), gs, vocab, dim, gt,
+                                                  int(bool(accumulate)), ws, wb),
                       (dout, tokens, grad, self._ws))
 
 

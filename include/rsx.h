@@ -409,7 +409,7 @@ int rsx_fusion_plan(const size_t* counts, const rsx_dtype_t* dtypes, int ntensor
  * out[i] = scale * table[t] for 0 <= t < vocab, else a row of zeros.
  * `first` is the token id of the table's first row: a table cut by rows over
  * the ranks is looked up part by part, and the sum all-reduce of the outputs
- * is the whole table's lookup.
+ * is the whole table's lookup.  first + vocab is at most 2^63.
  */
 rsx_status_t rsx_embedding(const void* table, size_t table_stride, size_t vocab, size_t dim,
                            rsx_dtype_t table_type, const void* tokens, size_t ntokens,

@@ -102,3 +102,30 @@ def test_a_functions_memory_is_of_the_stream_it_runs_on(name, given, monkeypatch
     getattr(steps, name)(*args)
     p, = FakePlan.plans
     assert p.made_on is home and p.called_on is None and not p.keep[0].recorded
+
+
+# ---- ids of a table's rows that 64 bits do not hold
+def lookup(first, vocab=100):
+    return call("rsx_embedding", A(1), 64, vocab, 64, F32, A(2), 0, I64, first, 1.0, A(3), 64, F32)
+
+
+def lookup_grad(first, vocab=100):
+    return call("rsx_embedding_grad", A(1), 64, F32, A(2), 0, I64, first, 1.0, A(3), 64, vocab, 64, F32, 0, None, 0)
+
+
+@fake_ptrs
+def test_rows_past_the_last_token_id_are_refused():
+    """Their ids would wrap, and the smallest tokens name them."""
+    most = 2 ** 63
+    assert lookup(most - 100) == OK and lookup(-most) == OK
+    assert lookup(most - 99) == BAD and lookup(most - 1, vocab=2) == BAD
+    assert lookup_grad(most - 99) == BAD and lookup_grad(most - 1, vocab=2) == BAD
+    assert lookup(most - 1, vocab=0) == OK and lookup_grad(most - 1, vocab=0) == OK
+
+
+@pytest.mark.parametrize("first", [2 ** 64 + 5, 2 ** 63, 2 ** 63 - 3, -2 ** 63 - 1])
+def test_python_refuses_firsts_beyond_64_bits(first):
+    """ctypes cuts them to 64 bits without a word."""
+    with pytest.raises(ValueError, match="first"):
+        steps._first(first, 4)
+    assert steps._first(2 ** 63 - 4, 4) == 2 ** 63 - 4 and steps._first(-2 ** 63, 4) == -2 ** 63
