@@ -322,8 +322,10 @@ class LayerNorm(_Plan):
         if c is not None:
             _checkpoint(c, "checkpoint", x.shape, x.device)
         self.out, self.checkpoint = out, c
-        self.mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        self.rstd = torch.empty_like(self.mean)
+        # Rows without elements have no mean, and the call nothing to write.
+        new = torch.empty if dim else lambda *a, **kw: torch.full(*a, math.nan, **kw)
+        self.mean = new(x.shape[:-1], dtype=torch.float32, device=x.device)
+        self.rstd = new(x.shape[:-1], dtype=torch.float32, device=x.device)
         codes, scales = (None, None) if c is None else (c.codes, c.scales)
         self._prepare("rsx_layer_norm", x.device,
                       (_ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(out), os_, _ptr(self.mean), _ptr(self.rstd),

@@ -324,3 +324,14 @@ def test_layer_norm_gradient_of_many_rows_of_2_25_elements():
             assert ((dx[r, a:a + (1 << 20)] - want).abs() <= tol + so.rounding(want, F32)).all()
     del dx, dw, db
     torch.cuda.empty_cache()
+
+
+def test_layer_norm_of_rows_without_elements():
+    """The mean of nothing is no number, and not what the memory held."""
+    for _ in range(3):
+        held = [torch.zeros(1000, device=DEV) for _ in range(4)]
+        del held
+        y, mean, rstd = rsx.layer_norm(torch.empty(1000, 0, device=DEV))
+        assert y.shape == (1000, 0) and torch.isnan(mean).all() and torch.isnan(rstd).all()
+    dx, dw, db = rsx.layer_norm_grad(y, y, mean, rstd)
+    assert dx.shape == (1000, 0) and dw.numel() == 0 and db.numel() == 0
