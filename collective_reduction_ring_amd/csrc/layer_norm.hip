@@ -21,12 +21,15 @@ constexpr int kThreads = 256;
 
 // ---------------------------------------------------------------- forward
 // A row of values from about 1e16 on may have finite differences whose squares
-// overflow: their sum is then taken again over differences scaled by 2^-80.
-// The test is the same for every lane of the row.
-constexpr float kScaleDown = 0x1p-80f;
-__device__ __forceinline__ bool squares_overflow(float sq, float mean, float factor) {
-  return sq == INFINITY && fabsf(mean) < INFINITY && factor == 1.0f;
+// overflow: their sum is then taken again over differences scaled by 2^-80, which
+// all are numbers.  A sum that is none is taken again of values scaled by 2^-32.
+// The tests are the same for every lane of the row; a row that has an infinity or
+// a NaN stays without a number.
+constexpr float kScaleDown = 0x1p-80f, kSumDown = 0x1p-32f;
+__device__ __forceinline__ bool squares_overflow(float sq, float mean) {
+  return sq == INFINITY && fabsf(mean) < INFINITY;
 }
+__device__ __forceinline__ bool is_number(float v) { return fabsf(v) < INFINITY; }
 // The mean as one sum gives it; the product as it is rounded, everywhere:
 // contracted into a difference it would be another mean there.
 __device__ __forceinline__ float first_mean(float sum, float inv_dim) { return fresh(sum * inv_dim); }
@@ -40,21 +43,20 @@ __device__ __forceinline__ bool mean_is_large(float first, float sq, float inv_d
   const float m = first * factor;
   return m * m > sq * inv_dim;
 }
+// The difference from the first mean, scaled; `first` is scaled already.  Exact
+// scalings by powers of two, so one rounding.
+__device__ __forceinline__ float difference(float x, float factor, float first) { return fmaf(x, factor, -first); }
 struct Centre {
   float mean, rstd;
-  float shift;  // xhat = (x - first mean) * rstd + shift
+  float scale, shift;  // xhat = difference * scale + shift
 };
-// sq: of the differences scaled by `factor`; off: the mean of the differences.
+// off: the mean of the differences, sq: the sum of their squares.
 __device__ __forceinline__ Centre centre(float first, float off, float sq, float inv_dim, float eps, float factor) {
-  const float d = off * factor;
-  const float left = fmaf(-d, d, sq * inv_dim), var = left < 0.0f ? 0.0f : left;  // a NaN stays
-  const float rstd = factor / sqrtf(var + eps * factor * factor);
-  return {first + off, rstd, -off * rstd};
+  const float left = fmaf(-off, off, sq * inv_dim), var = left < 0.0f ? 0.0f : left;  // a NaN stays
+  const float scale = 1.0f / sqrtf(var + eps * factor * factor);
+  return {first + (factor == 1.0f ? off : off * (1.0f / kScaleDown)), scale * factor, scale, -off * scale};
 }
 
-// G lanes share R rows; each holds EPL elements of each, vectors of E at
-// (j * G + lane) * E.  Up to G = 64 a row is in one wave: no barrier, and
-// several groups in a workgroup.  A lane's rows share the weights' loads.
 // Single rows of 16 elements a lane are the few ones: eight waves to a SIMD, all
 // of a CU's at once (2048 rows of 4096 fp32: 11.7 us, with seven 14.2).
 template <class T, class W, int G, int EPL, int R>
@@ -91,24 +93,58 @@ __global__ __launch_bounds__(G > 64 ? G : kThreads, R == 1 && EPL == 16 && G <= 
       for (int i = 0; i < E; ++i) sum[k] += f[i];
     }
   }
-  group_sum<G, R>(sum, slots[0]);
+  int turn = 0;
+  group_sum<G, R>(sum, slots[turn]);
   float first[R], sq[R], off[R], factor[R];
+  bool lost = false;
 #pragma unroll
   for (int k = 0; k < R; ++k) {
     first[k] = first_mean(sum[k], inv_dim);
     factor[k] = 1.0f;
     off[k] = 0.0f;
+    lost = lost || !is_number(sum[k]);
   }
+  // Behind a branch: kept over it in 32 bits, a row takes twice the registers
+  // (16384 rows of 8000 bf16: 102 us, so 95).
+  auto widen_anew = [&] {
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int j = 0; j < V; ++j) raw[k][j] = fresh(raw[k][j]);
+  };
+  if (lost) {
+    float part[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      part[k] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const typename X::wide f = widen<T, E>(raw[k][j]);
+#pragma unroll
+        for (int i = 0; i < E; ++i) part[k] = fmaf(f[i], kSumDown, part[k]);
+      }
+    }
+    turn ^= 1;
+    group_sum<G, R>(part, slots[turn]);
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      if (!is_number(sum[k])) first[k] = first_mean(part[k], inv_dim) * (1.0f / kSumDown);
+  }
+  // Not of the longest rows, of which a CU has one workgroup anyway (8192 rows of
+  // 30000 bf16: 236 us, so 226).
+  if constexpr (EPL < 32 && sizeof(T) == 2) widen_anew();
 
-  int turn = 1;
-  for (;; turn = 0) {
+  // The first time without the factors: they are 1.
+  auto squares = [&](bool scaled) {
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       sq[k] = 0.0f;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const uint32_t e = (j * G + lane) * E;
-        const typename X::wide f = (widen<T, E>(raw[k][j]) - first[k]) * factor[k];
+        typename X::wide f = widen<T, E>(raw[k][j]);
+#pragma unroll
+        for (int i = 0; i < E; ++i) f[i] = scaled ? difference(f[i], factor[k], first[k] * factor[k]) : f[i] - first[k];
         if (e + E <= dim) {
 #pragma unroll
           for (int i = 0; i < E; ++i) sq[k] = fmaf(f[i], f[i], sq[k]);
@@ -119,15 +155,20 @@ __global__ __launch_bounds__(G > 64 ? G : kThreads, R == 1 && EPL == 16 && G <= 
         }
       }
     }
+    turn ^= 1;
     group_sum<G, R>(sq, slots[turn]);
-    bool over = false;
+  };
+  squares(false);
+  bool over = false;
 #pragma unroll
-    for (int k = 0; k < R; ++k)
-      if (squares_overflow(sq[k], first[k], factor[k])) {
-        factor[k] = kScaleDown;
-        over = true;
-      }
-    if (!over) break;
+  for (int k = 0; k < R; ++k)
+    if (squares_overflow(sq[k], first[k])) {
+      factor[k] = kScaleDown;
+      over = true;
+    }
+  if (over) {
+    widen_anew();
+    squares(true);
   }
   // The same for all the lanes of a row, and for a workgroup where they exchange.
   bool any = false;
@@ -138,22 +179,17 @@ __global__ __launch_bounds__(G > 64 ? G : kThreads, R == 1 && EPL == 16 && G <= 
     for (int k = 0; k < R; ++k)
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const typename X::wide f = widen<T, E>(raw[k][j]) - first[k];
+        const typename X::wide f = widen<T, E>(raw[k][j]);
 #pragma unroll
         for (int i = 0; i < E; ++i)
-          if ((j * G + lane) * E + i < dim) off[k] += f[i];
+          if ((j * G + lane) * E + i < dim) off[k] += difference(f[i], factor[k], first[k] * factor[k]);
       }
     group_sum<G, R>(off, slots[turn ^ 1]);
 #pragma unroll
     for (int k = 0; k < R; ++k)
       off[k] = mean_is_large(first[k], sq[k], inv_dim, factor[k]) ? off[k] * inv_dim : 0.0f;
   }
-  // Widened anew from here on: kept over the branch in 32 bits, a row takes twice
-  // the registers (16384 rows of 8000 bf16: 102 us, so 95).
-#pragma unroll
-  for (int k = 0; k < R; ++k)
-#pragma unroll
-    for (int j = 0; j < V; ++j) raw[k][j] = fresh(raw[k][j]);
+  widen_anew();
   Centre c[R];
 #pragma unroll
   for (int k = 0; k < R; ++k) {
@@ -190,7 +226,8 @@ __global__ __launch_bounds__(G > 64 ? G : kThreads, R == 1 && EPL == 16 && G <= 
           a.scales[(row + k) * ck_blocks(a.dim) + e / kCkBlock] = static_cast<uint8_t>(byte);
       }
 #pragma unroll
-      for (int i = 0; i < E; ++i) f[i] = fmaf(f[i] - first[k], c[k].rstd, c[k].shift) * weight[i] + bias[i];
+      for (int i = 0; i < E; ++i)
+        f[i] = fmaf(difference(f[i], factor[k], first[k] * factor[k]), c[k].scale, c[k].shift) * weight[i] + bias[i];
       store_row<T, E>(static_cast<T*>(a.y) + (row + k) * a.y_stride, e, dim, narrow<T, E>(f));
     }
   }
@@ -216,29 +253,43 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < E; ++i) sum[0] += f[i];
   }
-  group_sum<1024, 1>(sum, slots[0]);
-  const float first = first_mean(sum[0], inv_dim);
+  int turn = 0;
+  group_sum<1024, 1>(sum, slots[turn]);
+  float first = first_mean(sum[0], inv_dim);
+  if (!is_number(sum[0])) {
+    float part[1] = {0.0f};
+    for (uint32_t e = threadIdx.x * E; e < dim; e += kStep) {
+      const typename X::wide f = widen<T, E>(load_row<T, E, false>(x, e, dim));
+#pragma unroll
+      for (int i = 0; i < E; ++i) part[0] = fmaf(f[i], kSumDown, part[0]);
+    }
+    turn ^= 1;
+    group_sum<1024, 1>(part, slots[turn]);
+    first = first_mean(part[0], inv_dim) * (1.0f / kSumDown);
+  }
 
   float sq[1], off[1] = {0.0f}, factor = 1.0f;
-  int turn = 1;
-  for (;; turn = 0) {
+  for (;;) {
     sq[0] = 0.0f;
     for (uint32_t e = threadIdx.x * E; e < dim; e += kStep) {
-      const typename X::wide f = (widen<T, E>(load_row<T, E, false>(x, e, dim)) - first) * factor;
+      const typename X::wide f = widen<T, E>(load_row<T, E, false>(x, e, dim));
 #pragma unroll
-      for (int i = 0; i < E; ++i)
-        if (e + i < dim) sq[0] = fmaf(f[i], f[i], sq[0]);
+      for (int i = 0; i < E; ++i) {
+        const float d = difference(f[i], factor, first * factor);
+        if (e + i < dim) sq[0] = fmaf(d, d, sq[0]);
+      }
     }
+    turn ^= 1;
     group_sum<1024, 1>(sq, slots[turn]);
-    if (!squares_overflow(sq[0], first, factor)) break;
+    if (factor != 1.0f || !squares_overflow(sq[0], first)) break;
     factor = kScaleDown;
   }
   if (mean_is_large(first, sq[0], inv_dim, factor)) {  // the same for the workgroup
     for (uint32_t e = threadIdx.x * E; e < dim; e += kStep) {
-      const typename X::wide f = widen<T, E>(load_row<T, E, false>(x, e, dim)) - first;
+      const typename X::wide f = widen<T, E>(load_row<T, E, false>(x, e, dim));
 #pragma unroll
       for (int i = 0; i < E; ++i)
-        if (e + i < dim) off[0] += f[i];
+        if (e + i < dim) off[0] += difference(f[i], factor, first * factor);
     }
     group_sum<1024, 1>(off, slots[turn ^ 1]);
     off[0] *= inv_dim;
@@ -268,7 +319,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
       if (e % kCkBlock == 0 && e < dim) a.scales[row * ck_blocks(a.dim) + e / kCkBlock] = static_cast<uint8_t>(byte);
     }
 #pragma unroll
-    for (int i = 0; i < E; ++i) f[i] = fmaf(f[i] - first, c.rstd, c.shift);
+    for (int i = 0; i < E; ++i) f[i] = fmaf(difference(f[i], factor, first * factor), c.scale, c.shift);
     if (w != nullptr) f *= widen<W, E>(load_row<W, E, false>(w, e, dim));
     if (b != nullptr) f += widen<W, E>(load_row<W, E, false>(b, e, dim));
     store_row<T, E>(y, e, dim, narrow<T, E>(f));

@@ -437,8 +437,7 @@ rsx_status_t rsx_embedding_grad(const void* dout, size_t dout_stride, rsx_dtype_
  * null (1 and 0).  mean, rstd: `rows` fp32, or null.
  * codes, scales: null, or an 8-bit checkpoint of x written on the way, as
  * rsx_checkpoint_pack does.  y == x with one stride is allowed.
- * dim = 0 writes nothing, mean and rstd neither.  A row whose sum leaves fp32
- * has no finite mean here, and gives NaN.
+ * dim = 0 writes nothing, mean and rstd neither.
  */
 rsx_status_t rsx_layer_norm(const void* x, size_t x_stride, const void* weight, const void* bias,
                             void* y, size_t y_stride, float* mean, float* rstd, int8_t* codes,

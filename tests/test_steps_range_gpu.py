@@ -335,3 +335,26 @@ def test_layer_norm_of_rows_without_elements():
         assert y.shape == (1000, 0) and torch.isnan(mean).all() and torch.isnan(rstd).all()
     dx, dw, db = rsx.layer_norm_grad(y, y, mean, rstd)
     assert dx.shape == (1000, 0) and dw.numel() == 0 and db.numel() == 0
+
+
+@pytest.mark.parametrize("rows,dim", [(5, 3), (5, 40), (4099, 200), (5, 700), (5, 3000), (4, 9000), (3, 33000)])
+@pytest.mark.parametrize("kind", ["signs", "level", "uniform", "one"])
+@pytest.mark.parametrize("xt", [F32, BF16])
+def test_layer_norm_of_rows_whose_sums_leave_32_bits(xt, kind, rows, dim):
+    """Finite values, with a finite mean and differences that fp32 does not all hold."""
+    few, g = min(rows, 5), gen(dim)
+    x = {"signs": lambda: torch.where(torch.arange(dim) % 2 == 0, 3e38, -2e38).expand(few, dim).double(),
+         "level": lambda: 1e38 + 1e37 * torch.randn(few, dim, generator=g, dtype=torch.float64),
+         "uniform": lambda: 3e38 * torch.rand(few, dim, generator=g, dtype=torch.float64),
+         "one": lambda: torch.cat([torch.full((few, 1), -3.3e38), torch.full((few, dim - 1), 3.3e38)], 1).double()}[kind]().to(xt)
+    w, b = (torch.randn(dim, generator=g) * 0.3 + 1).to(xt), (torch.randn(dim, generator=g) * 0.3).to(xt)
+    say("layer_norm of sums past fp32", xt, kind, rows, dim)
+    xd = x.repeat(-(-rows // few), 1)[:rows].contiguous().to(DEV)
+    ck = rsx.Checkpoint(xd.shape, DEV)
+    y, mean, rstd = rsx.layer_norm(xd, w.to(DEV), b.to(DEV), checkpoint=ck)
+    (ry, rm, rr), (ty, tm, tr) = layer_norm_bounds(x, w, b, 1e-5)
+    so.close(mean[:few], rm, tm + 1.01 * so.rounding(rm, F32), "mean")
+    so.close(rstd[:few], rr, tr + 1.01 * so.rounding(rr, F32), "rstd")
+    so.close(y[:few], ry, ty + 1.01 * so.rounding(ry, xt), "y")
+    codes, scales = so.checkpoint(x)
+    assert torch.equal(ck.codes[:few].cpu(), codes) and torch.equal(ck.scales[:few].cpu(), scales)
