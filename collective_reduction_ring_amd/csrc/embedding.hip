@@ -1,4 +1,5 @@
-// Embedding lookup with scaling, and its gradient by sorted tokens.
+// Embedding lookup with scaling, and its gradient: by sorted tokens, or for few
+// tokens each by its own search.
 //
 //   out[i, :]  = scale * table[t_i, :]          t_i = tokens[i] - first
 //   grad[v, :] = (grad[v, :] +) scale * sum of dout[i, :] over the i with t_i = v

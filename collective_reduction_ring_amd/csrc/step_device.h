@@ -267,12 +267,13 @@ __device__ __forceinline__ float ck_step(uint32_t byte) {
   const uint32_t b = byte == 0u ? 0x00400000u : byte == kCkBad ? 0x7fc00000u : byte << 23;
   return __builtin_bit_cast(float, b);
 }
-// 1 / ck_step; 0 for a bad block (its codes are 0).
+// 1 / ck_step; 0 for a bad block.
 __device__ __forceinline__ float ck_inverse(uint32_t byte) {
   return byte == kCkBad ? 0.0f : __builtin_bit_cast(float, (254u - byte) << 23);
 }
 __device__ __forceinline__ int8_t ck_code(float x, float inverse) {
-  // A bad block's infinity or NaN times 0 is a NaN, which the clamp drops.
+  // A bad block has codes of 0, and -127 for its infinities and NaNs, which times 0
+  // are NaN and left to the clamp; its byte says that no code of it counts.
   return static_cast<int8_t>(fminf(fmaxf(__builtin_rintf(x * inverse), -127.0f), 127.0f));
 }
 

@@ -209,8 +209,8 @@ class Embedding(_Plan):
 class EmbeddingGrad(_Plan):
     """Prepared gradient of the lookup in its table: ``grad[v] = (grad[v] if
     accumulate else 0) + scale * (sum of dout[i] over tokens[i] - first == v)``.
-    Rows are summed in fp32, in the order of their positions, after a sort of
-    the tokens: the same bits on every run."""
+    Rows are summed in fp32, in parts and in the order of their positions (many
+    tokens are sorted for it): the same bits on every run."""
 
     def __init__(self, dout, tokens, grad, scale: float = 1.0, first: int = 0, accumulate: bool = False):
         _tensor(grad, "grad")
