@@ -195,11 +195,19 @@ __device__ void scan_counts(uint32_t (*counts)[kBins], uint32_t* totals, const u
 // stores, so each hides the other.  A workgroup takes a group of `rows` rows;
 // those that a token names are marked as bits of `named`.
 constexpr uint32_t kNamedWords = kSortWaves * kBins;  // marks that a workgroup holds in LDS
-constexpr uint32_t kScanGroup = 3u << 17;  // bytes of a group that scans, about
+// Bytes of a group that scans, about: half of it and twice of it take 49.3 and
+// 51.7 us for 8192 x 1024 bf16 into 50000 fp32 rows (this 49.3), 119.4 and 120 for
+// 4000 x 4096 fp32 into 32000 (117.4), 30.0 and 31.1 for 700 x 1024 bf16 into 50000
+// (29.8).
+constexpr uint32_t kScanGroup = 3u << 17;
 constexpr uint32_t kZeroGroup = 1u << 15;  // bytes of one that does not
-// Bytes that a small sort has time for, about, and the joins; the rest is
-// zeroed beside the sums (8192 rows of 1024 into 50000 fp32 rows: all of it
-// beside the sort 52 us, so 50).
+// Bytes that a small sort has time for, about, and the joins; the rest is zeroed
+// beside the sums.  For 8192 tokens (us, with 64 MB, 128 and 256): 1024 columns into
+// 50000 fp32 rows 53.7, 49.3, 52.7; 2048 bf16 into 130000 126.8, 122.0, 120.0; 512
+// into 400000 fp32 rows 179.3, 170.8, 168.8.  Fewer tokens sort in less time, and 32
+// MB would be better: 700 x 1024 into 50000 bf16 rows 25.8 for 29.8, 2000 into 32000
+// fp32 rows 32.7 for 35.5.  The joins with none, 24 and 48 MB: 65536 x 4096 into
+// 131072 bf16 rows 322, 319.5, 318.3; 8192 x 1024 into 50000 50.8, 49.3, 49.6.
 constexpr uint64_t kSortZeros = 128000000;
 constexpr uint64_t kJoinZeros = 24000000;
 constexpr uint32_t kPlanes = 4;            // sets of marks of the whole table, each from a part of the tokens
