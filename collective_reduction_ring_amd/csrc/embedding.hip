@@ -202,7 +202,7 @@ constexpr uint32_t kNamedWords = kSortWaves * kBins;  // marks that a workgroup 
 constexpr uint32_t kScanGroup = 3u << 17;
 constexpr uint32_t kZeroGroup = 1u << 15;  // bytes of one that does not
 // Bytes that a small sort has time for, about, and the joins; the rest is zeroed
-// beside the sums.  For 8192 tokens (us, with 64 MB, 128 and 256): 1024 columns into
+// beside the sums.  For 8000 tokens and more (us, with 64 MB, 128 and 256): 1024 columns into
 // 50000 fp32 rows 53.7, 49.3, 52.7; 2048 bf16 into 130000 126.8, 122.0, 120.0; 512
 // into 400000 fp32 rows 179.3, 170.8, 168.8.  Fewer tokens sort in less time, and 32
 // MB would be better: 700 x 1024 into 50000 bf16 rows 25.8 for 29.8, 2000 into 32000

@@ -57,6 +57,9 @@ __device__ __forceinline__ Centre centre(float first, float off, float sq, float
   return {first + (factor == 1.0f ? off : off * (1.0f / kScaleDown)), scale * factor, scale, -off * scale};
 }
 
+// G lanes share R rows; each holds EPL elements of each, vectors of E at
+// (j * G + lane) * E.  Up to G = 64 a row is in one wave: no barrier, and
+// several groups in a workgroup.  A lane's rows share the weights' loads.
 // Single rows of 16 elements a lane are the few ones: eight waves to a SIMD, all
 // of a CU's at once (2048 rows of 4096 fp32: 11.7 us, with seven 14.2).
 template <class T, class W, int G, int EPL, int R>
@@ -233,8 +236,8 @@ __global__ __launch_bounds__(G > 64 ? G : kThreads, R == 1 && EPL == 16 && G <= 
   }
 }
 
-// Rows too long for the registers, or too short for a vector: a workgroup reads its row three times,
-// after the first from the caches.
+// Rows too long for the registers, or too short for a vector: a workgroup reads
+// its row three times, with a large mean four, after the first from the caches.
 template <class T, class W>
 __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
   constexpr int E = 16 / sizeof(T);
