@@ -17,4 +17,8 @@ from .steps import (  # noqa: F401
     TokenLogprobsGrad, checkpoint_pack, checkpoint_unpack, embedding, embedding_grad, layer_norm, layer_norm_grad,
     token_logprobs, token_logprobs_grad,
 )
+from .products import (  # noqa: F401
+    ACTIVATIONS, FeedForward, FeedForwardGrad, LinearLogprobs, LinearLogprobsGrad, NewtonSchulz, feed_forward, feed_forward_grad,
+    linear_logprobs, linear_logprobs_grad, newton_schulz,
+)
 from ._lib import RsxError  # noqa: F401

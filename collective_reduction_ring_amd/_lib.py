@@ -24,6 +24,7 @@ RSX_NAIVE_MAX_BYTES = 32768
 RSX_FUSE_BATCH = 248
 RSX_TOP_MAX = 64
 RSX_CHECKPOINT_BLOCK = 32
+RSX_ACT_SILU, RSX_ACT_GELU, RSX_ACT_GELU_TANH, RSX_ACT_RELU = 0, 1, 2, 3
 RSX_FUSION_THRESHOLD_DEFAULT = 64 * 1024 * 1024   # Horovod's default tensor_fusion_threshold
 
 STATUS = {
@@ -72,6 +73,19 @@ SIGNATURES = {
     "rsx_token_logprobs_rest": (_I, [_P, _SZ, _I, _P, _I, _SZ, _SZ, _I, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "rsx_token_logprobs_grad": (_I, [_P, _SZ, _I, _P, _I, _P, _P, _P, _P, _P, _SZ, _SZ, _SZ, _P]),
     "rsx_token_logprobs_grad_rest": (_I, [_P, _SZ, _I, _P, _I, _P, _P, _P, _P, _P, _P, _SZ, _SZ, _SZ, _P]),
+    "rsx_feed_forward_workspace_size": (_SZ, [_SZ, _SZ, _SZ, _I, _I]),
+    "rsx_feed_forward": (_I, [_P, _SZ, _P, _SZ, _P, _SZ, _P, _SZ, _P, _SZ, _P, _P, _SZ, _SZ, _SZ, _I, _I, _P, _SZ, _P]),
+    "rsx_feed_forward_grad_workspace_size": (_SZ, [_SZ, _SZ, _SZ, _I, _I]),
+    "rsx_feed_forward_grad": (_I, [_P, _SZ, _P, _SZ, _P, _SZ, _P, _SZ, _P, _SZ, _P, _P, _P, _SZ, _P, _SZ, _P, _SZ, _P, _SZ,
+                                   _SZ, _SZ, _SZ, _I, _I, _I, _I, _P, _SZ, _P]),
+    "rsx_linear_logprobs_workspace_size": (_SZ, [_SZ, _SZ, _SZ, _I, _I]),
+    "rsx_linear_logprobs": (_I, [_P, _SZ, _P, _SZ, _I, _P, _I, _SZ, _SZ, _SZ, ctypes.c_float, _P, _P, _P, _P, _P, _SZ, _P]),
+    "rsx_linear_logprobs_grad_workspace_size": (_SZ, [_SZ, _SZ, _SZ, _I, _I]),
+    "rsx_linear_logprobs_grad": (_I, [_P, _SZ, _P, _SZ, _I, _P, _I, _P, _P, _P, _P, _P, _P, _SZ, _P, _SZ, _I, _I, _SZ, _SZ, _SZ,
+                                      ctypes.c_float, _P, _SZ, _P]),
+    "rsx_newton_schulz_workspace_size": (_SZ, [_SZ, _SZ, _SZ]),
+    "rsx_newton_schulz": (_I, [_P, _SZ, _SZ, _P, _SZ, _SZ, _SZ, _SZ, _SZ, _I, ctypes.c_float, ctypes.c_float, ctypes.c_float,
+                               ctypes.c_float, _I, _P, _SZ, _P]),
     "rsx_segment_begin": (_SZ, [_SZ, _I, _I]),
     "rsx_dtype_size": (_SZ, [_I]),
     "rsx_status_string": (ctypes.c_char_p, [_I]),

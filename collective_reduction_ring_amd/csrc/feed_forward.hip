@@ -1,0 +1,310 @@
+// The gated feed-forward block and its gradients.
+//
+//   g = x Wg^T, u = x Wu^T, s = act(g) * u, y = s Wd^T
+//   ds = dy Wd, dg = ds * u * act'(g), du = ds * act(g)
+//   dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x, dWd = dy^T s
+//
+// Both projections, the activation and the product are one launch: a tile of
+// the double product has the same columns of g and of u in one lane's registers.
+// So are ds and what it makes: its epilogue reads g and u, and leaves dg, du and
+// s.  dx is one product whose k runs through both matrices.  No matrix is
+// transposed in memory.
+//
+// What is rounded: s (and dg, du) to the matrices' type, as the next product's
+// operand, and g and u to the type of x where they are kept for the gradient.
+// In fp32 all three are kept whole, as three bf16 parts.
+#include "few_rows.h"
+#include "product_store.h"
+
+namespace rsx {
+namespace {
+
+template <int N>
+struct Slope {
+  typename Vec<float, N>::type value, slope;
+};
+
+// act(x) and act'(x), elementwise, in fp32.
+template <bool SLOPE, int N>
+__device__ __forceinline__ Slope<N> activation(int act, typename Vec<float, N>::type x) {
+  Slope<N> r;
+  switch (act) {
+    case RSX_ACT_RELU:
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        r.value[e] = x[e] > 0.0f || x[e] != x[e] ? x[e] : 0.0f;
+        if (SLOPE) r.slope[e] = x[e] > 0.0f ? 1.0f : x[e] != x[e] ? x[e] : 0.0f;
+      }
+      break;
+    case RSX_ACT_GELU:  // x Phi(x); erfc keeps the digits of Phi far below 0
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float phi = 0.5f * erfcf(x[e] * -0.70710678118654752f);
+        r.value[e] = x[e] * phi;
+        if (SLOPE) r.slope[e] = phi + x[e] * (0.39894228040143268f * expf(-0.5f * x[e] * x[e]));
+      }
+      break;
+    case RSX_ACT_GELU_TANH:  // (1 + tanh z) / 2 = 1 / (1 + exp(-2z))
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float q = x[e] * x[e], z2 = 1.5957691216057308f * x[e] * (1.0f + 0.044715f * q);
+        const float p = 1.0f / (1.0f + expf(-z2));
+        r.value[e] = x[e] * p;
+        if (SLOPE) {
+          // p (1 - p) z2' x: 1 - p from the other exponential, without cancellation; far out it is 0 and x^3 may not be finite
+          const float t = p * (1.0f / (1.0f + expf(z2)));
+          r.slope[e] = t == 0.0f ? p : p + x[e] * t * (1.5957691216057308f * (1.0f + 3.0f * 0.044715f * q));
+        }
+      }
+      break;
+    default:  // RSX_ACT_SILU
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float p = 1.0f / (1.0f + expf(-x[e]));
+        r.value[e] = x[e] * p;
+        if (SLOPE) r.slope[e] = p + x[e] * p * (1.0f / (1.0f + expf(x[e])));
+      }
+  }
+  return r;
+}
+
+struct GateArgs {
+  Parts s;
+  float* s32;  // the few-row form in fp32 keeps s as it is, rows of p.rows
+  void* gate;  // null: not kept
+  void* up;
+  int act, type;
+};
+
+struct Gate {
+  typedef GateArgs Args;
+  template <class T, int N>
+  static __device__ __forceinline__ void one(const GateArgs& e, uint64_t m, uint32_t c, uint32_t n, typename Vec<float, N>::type g,
+                                             typename Vec<float, N>::type u) {
+    if (e.gate) {
+      put_as<N>(e.type, e.gate, m * n, c, n, g);
+      put_as<N>(e.type, e.up, m * n, c, n, u);
+    }
+    auto s = activation<false, N>(e.act, g).value;
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] *= u[i];
+    if constexpr (sizeof(T) == 4) put<float, N>(e.s32 + m * n, c, n, s);
+    else put_parts<T, N>(e.s, m, c, n, s);
+  }
+  template <class T, class TILE>
+  static __device__ __forceinline__ void run(const ProductArgs& p, const Where& w, const GateArgs& e,
+                                             const f32x4 (&acc)[TILE::TN][TILE::TM], RSX_LDS char* lds) {
+    staged<TILE, true>(w, acc, lds, [&](uint32_t m, uint32_t c, f32x8 g, f32x8 u) {
+      if (m < p.m) one<T, 8>(e, m, c, p.n, g, u);
+    });
+  }
+  template <class T, int RG>
+  static __device__ __forceinline__ void few(const FewArgs& p, const GateArgs& e, uint32_t row, uint32_t c, const f32x4 (&v)[2 * RG]) {
+    if (row >= p.n) return;
+#pragma unroll
+    for (int r = 0; r < RG; ++r) one<T, 4>(e, row, c + 16 * r, p.rows, v[r], v[r + RG]);
+  }
+};
+
+struct GateGradArgs {
+  const void* gate;
+  const void* up;
+  Parts s, dg, du;  // count 0: not wanted
+  int act, type;
+};
+
+struct GateGrad {
+  typedef GateGradArgs Args;
+  template <class T, class TILE>
+  static __device__ __forceinline__ void run(const ProductArgs& p, const Where& w, const GateGradArgs& e,
+                                             const f32x4 (&acc)[TILE::TN][TILE::TM], RSX_LDS char* lds) {
+    staged<TILE, false>(w, acc, lds, [&](uint32_t m, uint32_t c, f32x8 ds) {
+      if (m >= p.m || c >= ((p.n + 7) & ~7u)) return;
+      const uint64_t row = static_cast<uint64_t>(m) * p.n;
+      const f32x8 g = get_as<8>(e.type, e.gate, row, c, p.n), u = get_as<8>(e.type, e.up, row, c, p.n);
+      const Slope<8> a = activation<true, 8>(e.act, g);
+      f32x8 s, dg, du;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        s[x] = a.value[x] * u[x];
+        dg[x] = ds[x] * u[x] * a.slope[x];
+        du[x] = ds[x] * a.value[x];
+      }
+      put_parts<T, 8>(e.s, m, c, p.n, s);
+      put_parts<T, 8>(e.dg, m, c, p.n, dg);
+      put_parts<T, 8>(e.du, m, c, p.n, du);
+    });
+  }
+};
+
+struct FewStore {
+  typedef StoreArgs Args;
+  template <class T, int RG>
+  static __device__ __forceinline__ void few(const FewArgs& p, const StoreArgs& e, uint32_t row, uint32_t c, const f32x4 (&v)[RG]) {
+    if (row >= p.n) return;
+#pragma unroll
+    for (int r = 0; r < RG; ++r)
+      if (c + 16 * r < p.rows) put_as<4>(e.type, e.out, row * e.ld, c + 16 * r, p.rows, v[r]);
+  }
+};
+
+// Parts of a matrix of `type` as an operand: fp32 is three bf16 values exactly.
+int parts_of(int type) { return type == RSX_FLOAT32 ? 3 : 1; }
+
+ProductArgs sizes(uint64_t m, uint64_t n, uint64_t k) {
+  ProductArgs p = {};
+  p.m = static_cast<uint32_t>(m);
+  p.n = static_cast<uint32_t>(n);
+  p.k = static_cast<uint32_t>(k);
+  p.batch = 1;
+  return p;
+}
+
+#define RSX_TRY(x)                        \
+  do {                                    \
+    const hipError_t st_ = (x);           \
+    if (st_ != hipSuccess) return st_;    \
+  } while (0)
+
+template <class T>
+hipError_t few(const FeedForwardArgs& a, void* s, hipStream_t stream) {
+  GateArgs e = {{{s, nullptr, nullptr}, copy_ld(a.hidden), 1}, static_cast<float*>(s), a.gate, a.up, a.act, a.type};
+  FewArgs p = {a.x.p, a.w_gate.p, a.w_up.p, a.x.ld, a.w_gate.ld, a.w_up.ld, static_cast<uint32_t>(a.rows),
+               static_cast<uint32_t>(a.hidden), static_cast<uint32_t>(a.dim)};
+  if (a.hidden) RSX_TRY((launch_few<T, 1, true, Gate>(p, e, stream)));
+  p = {s, a.w_down.p, nullptr, sizeof(T) == 4 ? a.hidden : copy_ld(a.hidden), a.w_down.ld, 0, static_cast<uint32_t>(a.rows),
+       static_cast<uint32_t>(a.dim), static_cast<uint32_t>(a.hidden)};
+  return launch_few<T, 1, false, FewStore>(p, {a.out, a.out_ld, a.type, nullptr, 0, nullptr}, stream);
+}
+
+struct Forward {
+  Prepared x, wg, wu, wd;
+  Parts s;
+  void* split;
+};
+Forward plan(const FeedForwardArgs& a, Arena& ws) {
+  Forward f = {};
+  const int n = parts_of(a.type);
+  const bool half = a.type == RSX_FLOAT16;
+  f.x = take_operand(ws, a.x, a.type, n, half, a.copies);
+  f.wg = take_operand(ws, a.w_gate, a.type, n, half, a.copies);
+  f.wu = take_operand(ws, a.w_up, a.type, n, half, a.copies);
+  f.wd = take_operand(ws, a.w_down, a.type, n, half, a.copies);
+  f.s = take_parts(ws, a.rows, a.hidden, n);
+  f.split = ws.take(store_ws(a.rows, a.dim, a.hidden, n * (n + 1) / 2));
+  return f;
+}
+
+template <class T>
+hipError_t gate(const ProductArgs& p, const GateArgs& e, hipStream_t s) {
+  return large_tiles(p.m, 2ull * p.n, 1, false) ? launch_tiles<T, Large, kRow, kRow, true, false, Gate>(p, e, s)
+                                                : launch_tiles<T, Middle, kRow, kRow, true, false, Gate>(p, e, s);
+}
+template <class T>
+hipError_t gate_grad(const ProductArgs& p, const GateGradArgs& e, hipStream_t s) {
+  return large_tiles(p.m, p.n, 1, false) ? launch_tiles<T, Large, kRow, kCol, false, false, GateGrad>(p, e, s)
+                                         : launch_tiles<T, Middle, kRow, kCol, false, false, GateGrad>(p, e, s);
+}
+
+struct Backward {
+  Prepared dout, x, wg, wu, wd;
+  Parts s, dg, du;
+  void* split;
+};
+Backward plan(const FeedForwardGradArgs& a, Arena& ws) {
+  Backward b = {};
+  const int n = parts_of(a.type);
+  const bool half = a.type == RSX_FLOAT16;
+  b.dout = take_operand(ws, a.dout, a.type, n, half, a.copies);
+  b.wd = take_operand(ws, a.w_down, a.type, n, half, a.copies);
+  if (a.dw_gate) {
+    b.x = take_operand(ws, a.x, a.type, n, half, a.copies);
+    b.s = take_parts(ws, a.rows, a.hidden, n);
+  }
+  if (a.dx) {
+    b.wg = take_operand(ws, a.w_gate, a.type, n, half, a.copies);
+    b.wu = take_operand(ws, a.w_up, a.type, n, half, a.copies);
+  }
+  b.dg = take_parts(ws, a.rows, a.hidden, n);
+  b.du = take_parts(ws, a.rows, a.hidden, n);
+  const uint64_t segs = n * (n + 1) / 2;
+  uint64_t split = a.dx ? store_ws(a.rows, a.dim, a.hidden, 2 * segs) : 0;
+  if (a.dw_gate) {
+    const uint64_t g = store_ws(a.hidden, a.dim, a.rows, segs), d = store_ws(a.dim, a.hidden, a.rows, segs);
+    split = split < g ? g : split;
+    split = split < d ? d : split;
+  }
+  b.split = ws.take(split);
+  return b;
+}
+
+}  // namespace
+
+uint64_t feed_forward_ws(const FeedForwardArgs& a) {
+  if (a.rows <= kFewRows) return a.rows * copy_ld(a.hidden) * 4;
+  Arena ws(nullptr);
+  plan(a, ws);
+  return ws.at;
+}
+
+hipError_t launch_feed_forward(const FeedForwardArgs& a, hipStream_t s) {
+  if (a.rows <= kFewRows)
+    return a.type == RSX_FLOAT32 ? few<float>(a, a.ws, s) : a.type == RSX_BFLOAT16 ? few<bf16_t>(a, a.ws, s) : few<f16_t>(a, a.ws, s);
+  const bool half = a.type == RSX_FLOAT16;
+  const int n = parts_of(a.type);
+  Arena ws(a.ws);
+  const Forward f = plan(a, ws);
+  RSX_TRY(fill_operand(f.x, a.x, a.type, half, s));
+  RSX_TRY(fill_operand(f.wg, a.w_gate, a.type, half, s));
+  RSX_TRY(fill_operand(f.wu, a.w_up, a.type, half, s));
+  RSX_TRY(fill_operand(f.wd, a.w_down, a.type, half, s));
+  ProductArgs p = sizes(a.rows, a.hidden, a.dim);
+  add_segments(p, f.x.op, f.wg.op, n, &f.wu.op);
+  const GateArgs e = {f.s, nullptr, a.gate, a.up, a.act, a.type};
+  RSX_TRY(half ? gate<f16_t>(p, e, s) : gate<bf16_t>(p, e, s));
+  p = sizes(a.rows, a.dim, a.hidden);
+  add_segments(p, operand(f.s), f.wd.op, n);
+  return launch_store(half, kNT, p, {a.out, a.out_ld, a.type, nullptr, 0, nullptr}, f.split, s);
+}
+
+uint64_t feed_forward_grad_ws(const FeedForwardGradArgs& a) {
+  Arena ws(nullptr);
+  plan(a, ws);
+  return ws.at;
+}
+
+hipError_t launch_feed_forward_grad(const FeedForwardGradArgs& a, hipStream_t s) {
+  const bool half = a.type == RSX_FLOAT16;
+  const int n = parts_of(a.type);
+  Arena ws(a.ws);
+  const Backward b = plan(a, ws);
+  RSX_TRY(fill_operand(b.dout, a.dout, a.type, half, s));
+  RSX_TRY(fill_operand(b.wd, a.w_down, a.type, half, s));
+  if (a.dw_gate) RSX_TRY(fill_operand(b.x, a.x, a.type, half, s));
+  if (a.dx) {
+    RSX_TRY(fill_operand(b.wg, a.w_gate, a.type, half, s));
+    RSX_TRY(fill_operand(b.wu, a.w_up, a.type, half, s));
+  }
+  ProductArgs p = sizes(a.rows, a.hidden, a.dim);
+  add_segments(p, b.dout.op, b.wd.op, n);
+  const GateGradArgs e = {a.gate, a.up, b.s, b.dg, b.du, a.act, a.type};
+  if (a.rows && a.hidden) RSX_TRY(half ? gate_grad<f16_t>(p, e, s) : gate_grad<bf16_t>(p, e, s));
+  if (a.dx) {
+    p = sizes(a.rows, a.dim, a.hidden);
+    add_segments(p, operand(b.dg), b.wg.op, n);
+    add_segments(p, operand(b.du), b.wu.op, n);
+    RSX_TRY(launch_store(half, kNN, p, {a.dx, a.dx_ld, a.type, nullptr, 0, nullptr}, b.split, s));
+  }
+  if (!a.dw_gate) return hipSuccess;
+  p = sizes(a.hidden, a.dim, a.rows);
+  add_segments(p, operand(b.dg), b.x.op, n);
+  RSX_TRY(launch_store(half, kTN, p, {a.dw_gate, a.dw_gate_ld, a.weight_type, nullptr, a.accumulate, nullptr}, b.split, s));
+  p = sizes(a.hidden, a.dim, a.rows);
+  add_segments(p, operand(b.du), b.x.op, n);
+  RSX_TRY(launch_store(half, kTN, p, {a.dw_up, a.dw_up_ld, a.weight_type, nullptr, a.accumulate, nullptr}, b.split, s));
+  p = sizes(a.dim, a.hidden, a.rows);
+  add_segments(p, b.dout.op, operand(b.s), n);
+  return launch_store(half, kTN, p, {a.dw_down, a.dw_down_ld, a.weight_type, nullptr, a.accumulate, nullptr}, b.split, s);
+}
+
+}  // namespace rsx

@@ -1,0 +1,118 @@
+// Products of few rows with a large matrix, a decoding step's: the matrix is
+// read once, straight into the lanes that multiply it, and the time is the
+// memory's.
+//
+// A workgroup takes 16 * RG of the matrix's rows and its four waves share k out
+// in turns of U steps; their sums meet in LDS.  A step is one matrix
+// instruction of 32 k (16 bits) or four of 4 k (fp32, whose products stay fp32
+// here): a lane's 16 bytes of a row are its k, in the matrix and in x alike.
+#pragma once
+
+#include "product.h"
+
+namespace rsx {
+
+struct FewArgs {
+  const void* x;
+  const void* w;
+  const void* w2;  // second matrix of a double product
+  uint64_t ldx, ldw, ldw2;
+  uint32_t n, rows, k;  // rows of x, of the matrix; length of either
+};
+
+constexpr int kFewWaves = 4;
+constexpr uint32_t kFewRows = 64;  // rows of x that this form takes
+
+template <class T>
+struct FewFrag {
+  static constexpr int N = 16 / sizeof(T);
+  typedef typename Vec<T, N>::type type;
+};
+__device__ __forceinline__ f32x4 few_mma(FewFrag<float>::type w, FewFrag<float>::type x, f32x4 c) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(w[i], x[i], c, 0, 0, 0);
+  return c;
+}
+__device__ __forceinline__ f32x4 few_mma(FewFrag<bf16_t>::type w, FewFrag<bf16_t>::type x, f32x4 c) { return mma(w, x, c); }
+__device__ __forceinline__ f32x4 few_mma(FewFrag<f16_t>::type w, FewFrag<f16_t>::type x, f32x4 c) { return mma(w, x, c); }
+
+// v[g][t] for the waves t' = t mod 4: lane l has x row 16 t + l % 16 and matrix
+// rows first + 16 g + 4 (l / 16) .. + 3 (g from RG on: the second matrix's).
+template <class T, int NT, int RG, bool DUAL, class EPILOGUE>
+__global__ __launch_bounds__(64 * kFewWaves, 2) void few_rows_kernel(const FewArgs p, const typename EPILOGUE::Args e) {
+  constexpr int NM = DUAL ? 2 * RG : RG, N = FewFrag<T>::N, S = 4 * N, U = NT * NM >= 8 ? 4 : 8;
+  typedef typename FewFrag<T>::type V;
+  __shared__ f32x4 sums[kFewWaves][NM][NT][64];
+  const uint32_t l = threadIdx.x % 64, wave = uniform(threadIdx.x / 64), r = l % 16, g = l / 16;
+  const uint32_t first = static_cast<uint32_t>(block_id()) * (16 * RG);
+  if (first >= p.rows) return;
+  const T* wr[NM];
+  const T* xr[NT];
+#pragma unroll
+  for (int m = 0; m < NM; ++m) {
+    const uint64_t row = min(first + m % RG * 16 + r, p.rows - 1);
+    wr[m] = (m < RG ? static_cast<const T*>(p.w) + row * p.ldw : static_cast<const T*>(p.w2) + row * p.ldw2) + g * N;
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) xr[t] = static_cast<const T*>(p.x) + static_cast<uint64_t>(min(t * 16 + r, p.n - 1)) * p.ldx + g * N;
+  f32x4 acc[NM][NT];
+#pragma unroll
+  for (int m = 0; m < NM; ++m)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const uint32_t turns = p.k / (U * S);
+  for (uint32_t turn = wave; turn < turns; turn += kFewWaves) {
+    V w[U][NM], x[U][NT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int m = 0; m < NM; ++m) w[u][m] = load_once<T, N>(wr[m] + (turn * U + u) * S);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) x[u][t] = load_kept<T, N>(xr[t] + (turn * U + u) * S);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int m = 0; m < NM; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[m][t] = few_mma(w[u][m], x[u][t], acc[m][t]);
+  }
+  for (uint32_t step = turns * U + wave; step * S < p.k; step += kFewWaves) {
+    // what is left of a row, element by element where it ends in a lane's 16 bytes
+    const uint32_t k = step * S + g * N;
+    V x[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) x[t] = load_row<T, N, false>(xr[t] - g * N, k, p.k);
+#pragma unroll
+    for (int m = 0; m < NM; ++m) {
+      const V w = load_row<T, N, false>(wr[m] - g * N, k, p.k);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[m][t] = few_mma(w, x[t], acc[m][t]);
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < NM; ++m)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) sums[wave][m][t][l] = acc[m][t];
+  __syncthreads();
+  for (int t = wave; t < NT; t += kFewWaves) {
+    f32x4 v[NM];
+#pragma unroll
+    for (int m = 0; m < NM; ++m) {
+      v[m] = sums[0][m][t][l];
+#pragma unroll
+      for (int i = 1; i < kFewWaves; ++i) v[m] += sums[i][m][t][l];
+    }
+    EPILOGUE::template few<T, RG>(p, e, t * 16 + r, first + g * 4, v);
+  }
+}
+
+template <class T, int RG, bool DUAL, class EPILOGUE>
+hipError_t launch_few(const FewArgs& p, const typename EPILOGUE::Args& e, hipStream_t s) {
+  const dim3 grid = grid_of((static_cast<uint64_t>(p.rows) + 16 * RG - 1) / (16 * RG));
+  if (p.n <= 16) return launch(few_rows_kernel<T, 1, RG, DUAL, EPILOGUE>, grid, 64 * kFewWaves, 0, s, p, e);
+  if (p.n <= 32) return launch(few_rows_kernel<T, 2, RG, DUAL, EPILOGUE>, grid, 64 * kFewWaves, 0, s, p, e);
+  return launch(few_rows_kernel<T, 4, RG, DUAL, EPILOGUE>, grid, 64 * kFewWaves, 0, s, p, e);
+}
+
+}  // namespace rsx

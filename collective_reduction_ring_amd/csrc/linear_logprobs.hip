@@ -1,0 +1,394 @@
+// Log probabilities of tokens from hidden states, z = scale * h W^T, and their
+// gradient, without the logits in memory.
+//
+// Forward: each tile of the product leaves, for each of its rows, the largest
+// logit, the sum of exp(z - largest) and that sum weighted by z - largest; a
+// second launch joins a row's tiles.
+//
+// Gradient: the vocabulary is taken in pieces.  A piece's logits are multiplied
+// again, and the tile's epilogue makes of them
+//   dz_j = scale * (g (delta(j, token) - p_j) - d p_j (log p_j + entropy)),
+// the operand of two products, dW = dz^T h for the piece's rows (each complete)
+// and dh += dz W.  That is 4/3 of the operations of keeping all logits, and
+// memory for one piece.
+//
+// What is rounded: dz, as an operand, to bf16 (half a step of 2^-9 of each, with
+// errors that add up as those of the hidden states do).  With fp16 matrices dz
+// is two bf16 parts, and so are the matrices: probabilities of large
+// vocabularies lie below fp16's range.  With fp32 all is three.
+#include "few_rows.h"
+#include "product_store.h"
+
+namespace rsx {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ int64_t token_at(const void* tokens, int wide, uint32_t i) {
+  return wide ? static_cast<const int64_t*>(tokens)[i] : static_cast<const int32_t*>(tokens)[i];
+}
+
+// Of some of a row's logits: the largest, and the sums over them of e and of
+// e * (z - largest), e = exp(z - largest).
+struct Some {
+  float most, sum, gap;
+};
+__device__ __forceinline__ float less(float z, float most) { return most == -INFINITY ? z : z - most; }
+__device__ __forceinline__ Some joined(const Some& a, const Some& b) {
+  const float m = fmaxf(a.most, b.most);
+  const float da = less(a.most, m), db = less(b.most, m);
+  const float ea = __builtin_amdgcn_exp2f(da * kLog2e), eb = __builtin_amdgcn_exp2f(db * kLog2e);
+  // an empty part has sums of 0 (or of NaN, which stay in the sum); so far below the other that e is 0, d may be -inf
+  Some r = {m, 0.0f, 0.0f};
+  r.sum = (a.most == -INFINITY ? a.sum : a.sum * ea) + (b.most == -INFINITY ? b.sum : b.sum * eb);
+  r.gap = (ea == 0.0f ? 0.0f : (a.gap + a.sum * da) * ea) + (eb == 0.0f ? 0.0f : (b.gap + b.sum * db) * eb);
+  return r;
+}
+__device__ __forceinline__ Some across(const Some& a, int lanes) {
+  return joined(a, {__shfl_xor(a.most, lanes), __shfl_xor(a.sum, lanes), __shfl_xor(a.gap, lanes)});
+}
+
+struct SoftmaxArgs {
+  float4* some;   // [row][tile]
+  float* picked;  // the token's logit, of rows that have one
+  const void* tokens;
+  uint32_t tiles;
+  int wide;
+  float scale;
+};
+
+struct Softmax {
+  typedef SoftmaxArgs Args;
+  // N groups of four logits of one row, at columns c(j); those from `vocab` on do not count.
+  template <int N, class C>
+  static __device__ __forceinline__ Some take(const SoftmaxArgs& e, const f32x4 (&v)[N], C c, uint32_t vocab, int64_t token,
+                                              uint32_t row) {
+    float z[4 * N];
+    Some s = {-INFINITY, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint32_t at = c(j) + x;
+        z[4 * j + x] = at < vocab ? v[j][x] * e.scale : -INFINITY;
+        s.most = fmaxf(s.most, z[4 * j + x]);
+        if (at < vocab && at == token) e.picked[row] = z[4 * j + x];
+      }
+#pragma unroll
+    for (int i = 0; i < 4 * N; ++i) {
+      const float d = less(z[i], s.most), x = __builtin_amdgcn_exp2f(d * kLog2e);
+      s.sum += x;
+      s.gap += x == 0.0f ? 0.0f : x * d;
+    }
+    return s;
+  }
+  template <class T, class TILE>
+  static __device__ __forceinline__ void run(const ProductArgs& p, const Where& w, const SoftmaxArgs& e,
+                                             const f32x4 (&acc)[TILE::TN][TILE::TM], RSX_LDS char* lds) {
+    const Place<TILE> at(w);
+    const uint32_t l = threadIdx.x % 64, wave = threadIdx.x / 64;
+    RSX_LDS float* part = reinterpret_cast<RSX_LDS float*>(lds);  // [wave column][row of the tile][3]
+    __builtin_amdgcn_s_waitcnt(0);  // loads of steps past the last one
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < TILE::TM; ++i) {
+      const uint32_t row = at.row(i);
+      const int64_t token = row < p.m ? token_at(e.tokens, e.wide, row) : -1;
+      f32x4 v[TILE::TN];
+#pragma unroll
+      for (int j = 0; j < TILE::TN; ++j) v[j] = acc[j][i];
+      Some s = take(e, v, [&](int j) { return at.col(j); }, row < p.m ? p.n : 0, token, row);
+      s = across(across(s, 16), 32);
+      if (l < 16) {
+        RSX_LDS float* to = part + ((wave % TILE::WN) * TILE::BM + (row - w.m0)) * 3;
+        to[0] = s.most;
+        to[1] = s.sum;
+        to[2] = s.gap;
+      }
+    }
+    __syncthreads();
+    for (uint32_t r = threadIdx.x; r < TILE::BM && w.m0 + r < p.m; r += TILE::kThreads) {
+      Some s = {part[r * 3], part[r * 3 + 1], part[r * 3 + 2]};
+#pragma unroll
+      for (int i = 1; i < TILE::WN; ++i) {
+        RSX_LDS const float* q = part + (i * TILE::BM + r) * 3;
+        s = joined(s, {q[0], q[1], q[2]});
+      }
+      e.some[static_cast<uint64_t>(w.m0 + r) * e.tiles + w.n0 / TILE::BN] = float4{s.most, s.sum, s.gap, 0.0f};
+    }
+  }
+  template <class T, int RG>
+  static __device__ __forceinline__ void few(const FewArgs& p, const SoftmaxArgs& e, uint32_t row, uint32_t c, const f32x4 (&v)[RG]) {
+    const int64_t token = row < p.n ? token_at(e.tokens, e.wide, row) : -1;
+    Some s = take(e, v, [&](int j) { return c + 16 * j; }, row < p.n ? p.rows : 0, token, row);
+    s = across(across(s, 16), 32);
+    if (row < p.n && threadIdx.x % 64 < 16)
+      e.some[static_cast<uint64_t>(row) * e.tiles + c / (16 * RG)] = float4{s.most, s.sum, s.gap, 0.0f};
+  }
+};
+
+struct JoinArgs {
+  const float4* some;
+  const float* picked;
+  const void* tokens;
+  float* logprob;
+  float* entropy;
+  float* lse;
+  float* lse_rest;
+  uint32_t rows, tiles;
+  uint64_t vocab;
+  int wide;
+};
+
+// One workgroup a row.
+__global__ __launch_bounds__(256) void join_tiles(const JoinArgs a) {
+  const uint64_t row = block_id();
+  if (row >= a.rows) return;
+  __shared__ float part[4][3];
+  Some s = {-INFINITY, 0.0f, 0.0f};
+  for (uint32_t i = threadIdx.x; i < a.tiles; i += 256) {
+    const float4 q = a.some[row * a.tiles + i];
+    s = joined(s, {q.x, q.y, q.z});
+  }
+#pragma unroll
+  for (int lanes = 1; lanes < 64; lanes *= 2) s = across(s, lanes);
+  if (threadIdx.x % 64 == 0) {
+    part[threadIdx.x / 64][0] = s.most;
+    part[threadIdx.x / 64][1] = s.sum;
+    part[threadIdx.x / 64][2] = s.gap;
+  }
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+#pragma unroll
+  for (int i = 1; i < 4; ++i) s = joined(s, {part[i][0], part[i][1], part[i][2]});
+  const int64_t token = token_at(a.tokens, a.wide, static_cast<uint32_t>(row));
+  const bool there = token >= 0 && static_cast<uint64_t>(token) < a.vocab;
+  const bool none = s.most == -INFINITY && s.sum == 0.0f;
+  const float ln = logf(s.sum);
+  const float lse = none ? -INFINITY : s.most + ln;
+  a.lse[row] = lse;
+  if (a.lse_rest) {  // what the rounding of the sum took, from the larger and the smaller of the two
+    const float big = fabsf(s.most) >= fabsf(ln) ? s.most : ln, small = fabsf(s.most) >= fabsf(ln) ? ln : s.most;
+    a.lse_rest[row] = fabsf(lse) < INFINITY ? small - (lse - big) : 0.0f;
+  }
+  a.logprob[row] = !there ? 0.0f : none ? -INFINITY : (a.picked[row] - s.most) - ln;
+  if (a.entropy) a.entropy[row] = none ? 0.0f : ln - s.gap / s.sum;
+}
+
+struct DzArgs {
+  const void* tokens;
+  const float* lse;
+  const float* lse_rest;
+  const float* entropy;
+  const float* dlogprob;
+  const float* dentropy;
+  Parts dz;
+  uint64_t first, vocab;  // the piece's first row of the matrix; all rows
+  float scale;
+  int wide;
+};
+
+struct Dz {
+  typedef DzArgs Args;
+  template <class T, class TILE>
+  static __device__ __forceinline__ void run(const ProductArgs& p, const Where& w, const DzArgs& e,
+                                             const f32x4 (&acc)[TILE::TN][TILE::TM], RSX_LDS char* lds) {
+    staged<TILE, false>(w, acc, lds, [&](uint32_t row, uint32_t c, f32x8 v) {
+      if (row >= p.m) return;
+      const int64_t token = token_at(e.tokens, e.wide, row);
+      const bool there = token >= 0 && static_cast<uint64_t>(token) < e.vocab;
+      const uint64_t hit = there ? static_cast<uint64_t>(token) - e.first : ~0ull;
+      const float lse = e.lse[row], rest = e.lse_rest ? e.lse_rest[row] : 0.0f;
+      const float g = there ? e.dlogprob[row] : 0.0f;
+      const float d = e.dentropy ? e.dentropy[row] : 0.0f, h = e.dentropy ? e.entropy[row] : 0.0f;
+      const bool none = lse == -INFINITY;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const float lp = (v[x] * e.scale - lse) - rest, q = __builtin_amdgcn_exp2f(lp * kLog2e);
+        const float own = c + x == hit ? g : 0.0f;
+        const float dz = q == 0.0f ? own : own - q * (g + d * (lp + h));
+        v[x] = none ? 0.0f : e.scale * dz;
+      }
+      put_parts<bf16_t, 8>(e.dz, row, c, p.n, v);
+    });
+  }
+};
+
+#define RSX_TRY(x)                        \
+  do {                                    \
+    const hipError_t st_ = (x);           \
+    if (st_ != hipSuccess) return st_;    \
+  } while (0)
+
+ProductArgs sizes(uint64_t m, uint64_t n, uint64_t k) {
+  ProductArgs p = {};
+  p.m = static_cast<uint32_t>(m);
+  p.n = static_cast<uint32_t>(n);
+  p.k = static_cast<uint32_t>(k);
+  p.batch = 1;
+  return p;
+}
+
+constexpr int kFewGroups = 2;  // of 16 matrix rows: with one, x is read from L2 as often as the matrix from memory
+
+struct Forward {
+  Prepared hidden, weight;
+  float4* some;
+  float* picked;
+  uint32_t tiles;
+  bool few, large;
+};
+Forward plan(const LinearLogprobArgs& a, Arena& ws) {
+  Forward f = {};
+  const int n = a.type == RSX_FLOAT32 ? 3 : 1;
+  const bool half = a.type == RSX_FLOAT16;
+  f.few = a.rows <= kFewRows;
+  f.large = large_tiles(a.rows, a.vocab, 1, false);
+  const uint64_t width = f.few ? 16 * kFewGroups : f.large ? Large::BN : Middle::BN;
+  f.tiles = static_cast<uint32_t>((a.vocab + width - 1) / width);
+  if (!f.few) {
+    f.hidden = take_operand(ws, a.hidden, a.type, n, half, a.copies);
+    f.weight = take_operand(ws, a.weight, a.type, n, half, a.copies);
+  }
+  f.some = static_cast<float4*>(ws.take(a.rows * f.tiles * sizeof(float4)));
+  f.picked = static_cast<float*>(ws.take(a.rows * 4));
+  return f;
+}
+
+// Columns of a piece: 2^27 elements of dz (256 MB of bf16: the Infinity Cache's
+// size), at least 16 tiles, and at most what the tile loads' offsets reach over.
+uint64_t piece(uint64_t rows, uint64_t vocab) {
+  uint64_t n = ((1ull << 27) / (rows ? rows : 1)) & ~4095ull;
+  n = n < 4096 ? 4096 : n > (1ull << 20) ? 1ull << 20 : n;
+  return n < vocab ? n : vocab;
+}
+
+struct Backward {
+  Prepared hidden, weight;    // of the logits' product
+  Prepared hidden2, weight2;  // of the gradients' products
+  Parts dz;
+  float* sum;  // dhidden so far
+  void* split;
+  uint64_t piece;
+};
+Backward plan(const LinearLogprobGradArgs& a, Arena& ws) {
+  Backward b = {};
+  const bool half = a.type == RSX_FLOAT16;
+  const int n = a.type == RSX_FLOAT32 ? 3 : 1, n2 = half ? 2 : n;
+  b.hidden = take_operand(ws, a.hidden, a.type, n, half, a.copies);
+  b.weight = take_operand(ws, a.weight, a.type, n, half, a.copies);
+  b.hidden2 = b.hidden;
+  b.weight2 = b.weight;
+  if (half) {
+    if (a.dweight) b.hidden2 = take_operand(ws, a.hidden, a.type, n2, false, a.copies);
+    if (a.dhidden) b.weight2 = take_operand(ws, a.weight, a.type, n2, false, a.copies);
+  }
+  b.piece = piece(a.rows, a.vocab);
+  b.dz = take_parts(ws, a.rows, b.piece, n2);
+  if (a.dhidden && b.piece < a.vocab) b.sum = static_cast<float*>(ws.take(a.rows * a.dim * 4));
+  const uint64_t segs = n2 * (n2 + 1) / 2;
+  uint64_t split = 0;
+  const uint64_t last = b.piece ? a.vocab % b.piece : 0;  // the last piece is cut in its own way
+  for (const uint64_t v : {b.piece, last}) {
+    if (v == 0) continue;
+    const uint64_t h = a.dhidden ? store_ws(a.rows, a.dim, v, segs) : 0, w = a.dweight ? store_ws(v, a.dim, a.rows, segs) : 0;
+    split = split < h ? h : split;
+    split = split < w ? w : split;
+  }
+  b.split = ws.take(split);
+  return b;
+}
+
+template <class T>
+hipError_t softmax(const ProductArgs& p, const SoftmaxArgs& e, bool large, hipStream_t s) {
+  return large ? launch_tiles<T, Large, kRow, kRow, false, false, Softmax>(p, e, s)
+               : launch_tiles<T, Middle, kRow, kRow, false, false, Softmax>(p, e, s);
+}
+template <class T>
+hipError_t dlogits(const ProductArgs& p, const DzArgs& e, hipStream_t s) {
+  return large_tiles(p.m, p.n, 1, false) ? launch_tiles<T, Large, kRow, kRow, false, false, Dz>(p, e, s)
+                                         : launch_tiles<T, Middle, kRow, kRow, false, false, Dz>(p, e, s);
+}
+
+}  // namespace
+
+uint64_t linear_logprobs_ws(const LinearLogprobArgs& a) {
+  Arena ws(nullptr);
+  plan(a, ws);
+  return ws.at;
+}
+
+hipError_t launch_linear_logprobs(const LinearLogprobArgs& a, hipStream_t s) {
+  Arena ws(a.ws);
+  const Forward f = plan(a, ws);
+  const bool half = a.type == RSX_FLOAT16;
+  const SoftmaxArgs e = {f.some, f.picked, a.tokens, f.tiles, a.wide, a.scale};
+  if (f.few) {
+    const FewArgs p = {a.hidden.p, a.weight.p, nullptr, a.hidden.ld, a.weight.ld, 0, static_cast<uint32_t>(a.rows),
+                       static_cast<uint32_t>(a.vocab), static_cast<uint32_t>(a.dim)};
+    RSX_TRY((a.type == RSX_FLOAT32 ? launch_few<float, kFewGroups, false, Softmax>(p, e, s)
+             : half                ? launch_few<f16_t, kFewGroups, false, Softmax>(p, e, s)
+                                   : launch_few<bf16_t, kFewGroups, false, Softmax>(p, e, s)));
+  } else {
+    RSX_TRY(fill_operand(f.hidden, a.hidden, a.type, half, s));
+    RSX_TRY(fill_operand(f.weight, a.weight, a.type, half, s));
+    ProductArgs p = sizes(a.rows, a.vocab, a.dim);
+    add_segments(p, f.hidden.op, f.weight.op, a.type == RSX_FLOAT32 ? 3 : 1);
+    RSX_TRY(half ? softmax<f16_t>(p, e, f.large, s) : softmax<bf16_t>(p, e, f.large, s));
+  }
+  return launch(join_tiles, grid_of(a.rows), 256, 0, s,
+                {f.some, f.picked, a.tokens, a.logprob, a.entropy, a.lse, a.lse_rest, static_cast<uint32_t>(a.rows), f.tiles,
+                 a.vocab, a.wide});
+}
+
+uint64_t linear_logprobs_grad_ws(const LinearLogprobGradArgs& a) {
+  Arena ws(nullptr);
+  plan(a, ws);
+  return ws.at;
+}
+
+hipError_t launch_linear_logprobs_grad(const LinearLogprobGradArgs& a, hipStream_t s) {
+  const bool half = a.type == RSX_FLOAT16;
+  const int n = a.type == RSX_FLOAT32 ? 3 : 1, n2 = half ? 2 : n;
+  Arena ws(a.ws);
+  const Backward b = plan(a, ws);
+  RSX_TRY(fill_operand(b.hidden, a.hidden, a.type, half, s));
+  RSX_TRY(fill_operand(b.weight, a.weight, a.type, half, s));
+  if (half) {
+    if (a.dweight) RSX_TRY(fill_operand(b.hidden2, a.hidden, a.type, false, s));
+    if (a.dhidden) RSX_TRY(fill_operand(b.weight2, a.weight, a.type, false, s));
+  }
+  const uint64_t es = a.weight_type == RSX_FLOAT32 ? 4 : 2;
+  for (uint64_t first = 0; first < a.vocab; first += b.piece) {
+    const uint64_t v = a.vocab - first < b.piece ? a.vocab - first : b.piece;
+    auto rows_from = [&](Operand o) {
+      for (const void*& part : o.part)
+        if (part) part = static_cast<const char*>(part) + first * o.ld * 2;
+      return o;
+    };
+    if (a.rows) {
+      ProductArgs p = sizes(a.rows, v, a.dim);
+      add_segments(p, b.hidden.op, rows_from(b.weight.op), n);
+      const DzArgs e = {a.tokens, a.lse, a.lse_rest, a.entropy, a.dlogprob, a.dentropy, b.dz, first, a.vocab, a.scale, a.wide};
+      RSX_TRY(half ? dlogits<f16_t>(p, e, s) : dlogits<bf16_t>(p, e, s));
+    }
+    if (a.dweight) {
+      ProductArgs p = sizes(v, a.dim, a.rows);
+      add_segments(p, operand(b.dz), b.hidden2.op, n2);
+      void* to = static_cast<char*>(a.dweight) + first * a.dweight_ld * es;
+      RSX_TRY(launch_store(false, kTN, p, {to, a.dweight_ld, a.weight_type, nullptr, a.accumulate, nullptr}, b.split, s));
+    }
+    if (a.dhidden) {
+      ProductArgs p = sizes(a.rows, a.dim, v);
+      add_segments(p, operand(b.dz), rows_from(b.weight2.op), n2);
+      const bool last = first + v == a.vocab;
+      const float* add = first ? b.sum : nullptr;
+      const StoreArgs e = last ? StoreArgs{a.dhidden, a.dhidden_ld, a.type, add, 0, nullptr}
+                               : StoreArgs{b.sum, a.dim, RSX_FLOAT32, add, 0, nullptr};
+      RSX_TRY(launch_store(false, kNN, p, e, b.split, s));
+    }
+  }
+  return hipSuccess;
+}
+
+}  // namespace rsx

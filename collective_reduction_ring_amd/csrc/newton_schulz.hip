@@ -1,0 +1,281 @@
+// Orthogonalised updates: X0 = G / (|G| + eps), |G| the Frobenius norm, then
+// `steps` times A = X X^T, B = b A + c A A, X = a X + B X, with X the matrix or
+// its transpose, whichever is wider than tall, so that A is the smaller square.
+//
+// Each step draws the singular values towards 1 by an odd polynomial; small ones
+// grow by a factor of a in each step, 485 in five of the usual coefficients, and
+// errors with them: with X, A and B in one 16-bit value each, the update of a
+// matrix of low rank and little noise comes out 2% off.  So each is the sum of two
+// fp16 values, 22 bits, and a product three products of parts: as near to the
+// exact result as fp32 products throughout (rms 5e-5 and 5e-5 of that matrix),
+// at the rate of 16-bit matrix instructions.  All three are bounded, and are kept
+// times 2^12, the parts' exponents far from either end: values up to 16 fit.
+//
+// A and B are symmetric: only tiles on and below the diagonal are multiplied,
+// and stored to both sides.
+#include "product_store.h"
+
+namespace rsx {
+namespace {
+
+constexpr float kScale = 4096.0f, kUnscale = 1.0f / 4096.0f;
+constexpr uint32_t kNormGroups = 512;  // workgroups that sum a matrix's squares, at most
+
+#define RSX_TRY(x)                        \
+  do {                                    \
+    const hipError_t st_ = (x);           \
+    if (st_ != hipSuccess) return st_;    \
+  } while (0)
+
+// A stack of matrices as two parts.
+struct Stack {
+  Parts p;
+  uint64_t each;  // elements from one to the next
+  __device__ __forceinline__ Parts at(uint32_t i) const {
+    Parts r = p;
+    r.part[0] = static_cast<f16_t*>(p.part[0]) + i * each;
+    r.part[1] = static_cast<f16_t*>(p.part[1]) + i * each;
+    return r;
+  }
+};
+
+// Sums of squares in fp64: no update's values leave its range.
+template <class S>
+__global__ __launch_bounds__(256) void square_sums(const S* x, uint64_t ld, uint64_t each, uint32_t rows, uint32_t cols, double* sums) {
+  const uint32_t chunks = (cols + 7) / 8;
+  const uint64_t all = static_cast<uint64_t>(rows) * chunks;
+  const S* m = x + blockIdx.y * each;
+  double s = 0.0;
+  for (uint64_t t = blockIdx.x * 256ull + threadIdx.x; t < all; t += gridDim.x * 256ull) {
+    const auto v = load_row<S, 8, false>(m + t / chunks * ld, static_cast<uint32_t>(t % chunks) * 8, cols);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s += static_cast<double>(static_cast<float>(v[e])) * static_cast<double>(static_cast<float>(v[e]));
+  }
+#pragma unroll
+  for (int lanes = 1; lanes < 64; lanes *= 2) s += __shfl_xor(s, lanes);
+  __shared__ double part[4];
+  if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) sums[blockIdx.y * kNormGroups + blockIdx.x] = (part[0] + part[1]) + (part[2] + part[3]);
+}
+
+// X0 as parts, of G or (TALL) of its transpose: tiles of 64 x 64 through LDS.
+// The rows of A and B are as long as X0 has rows, filled up to 8 with zeros here.
+template <class S, bool TALL>
+__global__ __launch_bounds__(256) void first_parts(const S* x, uint64_t ld, uint64_t each, uint32_t rows, uint32_t cols,
+                                                   const double* sums, uint32_t groups, float eps, Stack to, Stack gram, Stack poly) {
+  __shared__ float tile[64][65];
+  __shared__ double part[4];
+  const uint32_t t = threadIdx.x, m = blockIdx.z;
+  double s = 0.0;
+  for (uint32_t i = t; i < groups; i += 256) s += sums[m * kNormGroups + i];
+#pragma unroll
+  for (int lanes = 1; lanes < 64; lanes *= 2) s += __shfl_xor(s, lanes);
+  if (t % 64 == 0) part[t / 64] = s;
+  const S* g = x + m * each;
+  const uint32_t n = TALL ? cols : rows, wide = TALL ? rows : cols;  // of X0
+  const uint32_t r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;         // of X0
+  for (uint32_t i = t / 64; i < 64; i += 4) {
+    const uint32_t r = (TALL ? c0 : r0) + i, c = (TALL ? r0 : c0) + t % 64;  // of G
+    const float v = r < rows && c < cols ? static_cast<float>(g[r * ld + c]) : 0.0f;
+    if (TALL) tile[t % 64][i] = v;
+    else tile[i][t % 64] = v;
+  }
+  __syncthreads();
+  // in fp64 up to the last rounding: |G| and G may both be far from 1
+  const double by = static_cast<double>(kScale) / (sqrt((part[0] + part[1]) + (part[2] + part[3])) + static_cast<double>(eps));
+  const Parts p = to.at(m);
+  for (uint32_t i = t / 16; i < 64; i += 16) {
+    const uint32_t r = r0 + i, c = c0 + t % 16 * 4;
+    if (r >= n) break;
+    f32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = static_cast<float>(static_cast<double>(tile[i][t % 16 * 4 + e]) * by);
+    put_parts<f16_t, 4>(p, r, c, wide, v);
+  }
+  if (blockIdx.x == 0 && n % 8 != 0 && t < 64 && r0 + t < n) {
+    const Parts ga = gram.at(m), po = poly.at(m);
+    for (uint32_t c = n; c < ((n + 7) & ~7u); ++c)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        static_cast<f16_t*>(ga.part[i])[(r0 + t) * ga.ld + c] = 0.0f;
+        static_cast<f16_t*>(po.part[i])[(r0 + t) * po.ld + c] = 0.0f;
+      }
+  }
+}
+
+// v to (m, n ..) and to (n .., m) of a symmetric matrix.  Of a tile on the
+// diagonal the sums above it are left: their parts' products add up in another
+// order, and a value is written once.
+__device__ __forceinline__ void put_both(const Parts& p, uint32_t m, uint32_t n, uint32_t size, f32x8 v) {
+  typedef Vec<f16_t, 8>::type V;
+  if (n > m || m >= size) return;
+  const V hi = __builtin_convertvector(v, V);
+  const f32x8 back = __builtin_convertvector(hi, f32x8);
+  f32x8 rest;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) rest[e] = fabsf(back[e]) < INFINITY ? v[e] - back[e] : 0.0f;
+  const V lo = __builtin_convertvector(rest, V);
+  f16_t* a = static_cast<f16_t*>(p.part[0]);
+  f16_t* b = static_cast<f16_t*>(p.part[1]);
+  const uint64_t at = m * p.ld + n;
+  const bool whole = n + 7 <= m;
+  if (whole) {
+    *reinterpret_cast<V*>(a + at) = hi;
+    *reinterpret_cast<V*>(b + at) = lo;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if (n + e > m) break;
+    if (!whole) {
+      a[at + e] = hi[e];
+      b[at + e] = lo[e];
+    }
+    if (n + e < m) {
+      a[(n + e) * p.ld + m] = hi[e];
+      b[(n + e) * p.ld + m] = lo[e];
+    }
+  }
+}
+
+struct GramArgs {
+  Stack to;
+};
+struct Gram {
+  typedef GramArgs Args;
+  template <class T, class TILE>
+  static __device__ __forceinline__ void run(const ProductArgs& p, const Where& w, const GramArgs& e,
+                                             const f32x4 (&acc)[TILE::TN][TILE::TM], RSX_LDS char* lds) {
+    const Parts to = e.to.at(w.batch);
+    staged<TILE, false>(w, acc, lds, [&](uint32_t m, uint32_t n, f32x8 v) { put_both(to, m, n, p.m, v * kUnscale); });
+  }
+};
+
+struct PolyArgs {
+  Stack gram, to;
+  float b, c;
+};
+struct Poly {
+  typedef PolyArgs Args;
+  template <class T, class TILE>
+  static __device__ __forceinline__ void run(const ProductArgs& p, const Where& w, const PolyArgs& e,
+                                             const f32x4 (&acc)[TILE::TN][TILE::TM], RSX_LDS char* lds) {
+    const Parts gram = e.gram.at(w.batch), to = e.to.at(w.batch);
+    staged<TILE, false>(w, acc, lds, [&](uint32_t m, uint32_t n, f32x8 v) {
+      if (m >= p.m || n > m) return;
+      const f32x8 g = get_parts<f16_t, 8>(gram, m, n);  // rows are filled to 8
+      put_both(to, m, n, p.m, g * e.b + v * (e.c * kUnscale));
+    });
+  }
+};
+
+struct ApplyArgs {
+  Stack x, to;
+  void* out;  // the last step's: null before
+  uint64_t ld, each;
+  int type, tall;
+  float a;
+};
+struct Apply {
+  typedef ApplyArgs Args;
+  template <class T, class TILE>
+  static __device__ __forceinline__ void run(const ProductArgs& p, const Where& w, const ApplyArgs& e,
+                                             const f32x4 (&acc)[TILE::TN][TILE::TM], RSX_LDS char* lds) {
+    const Parts x = e.x.at(w.batch), to = e.to.at(w.batch);
+    const uint64_t first = w.batch * e.each;
+    staged<TILE, false>(w, acc, lds, [&](uint32_t m, uint32_t n, f32x8 sum) {
+      if (m >= p.m || n >= ((p.n + 7) & ~7u)) return;
+      const f32x8 v = get_parts<f16_t, 8>(x, m, n) * e.a + sum * kUnscale;
+      if (e.out == nullptr) {
+        put_parts<f16_t, 8>(to, m, n, p.n, v);
+      } else if (!e.tall) {
+        if (n < p.n) put_as<8>(e.type, e.out, first + m * e.ld, n, p.n, v * kUnscale);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (n + q < p.n) put_as<1>(e.type, e.out, first + (n + q) * e.ld, m, m + 1, typename Vec<float, 1>::type{v[q] * kUnscale});
+      }
+    });
+  }
+};
+
+struct Space {
+  double* sums;
+  Stack x, y, gram, poly;
+};
+Stack take_stack(Arena& ws, uint64_t batch, uint64_t rows, uint64_t cols) {
+  Stack s = {};
+  s.p = take_parts(ws, batch * rows, cols, 2);
+  s.each = rows * s.p.ld;
+  return s;
+}
+Space plan(Arena& ws, uint64_t batch, uint64_t n, uint64_t wide) {
+  Space p;
+  p.sums = static_cast<double*>(ws.take(batch * kNormGroups * sizeof(double)));
+  p.x = take_stack(ws, batch, n, wide);
+  p.y = take_stack(ws, batch, n, wide);
+  p.gram = take_stack(ws, batch, n, n);
+  p.poly = take_stack(ws, batch, n, n);
+  return p;
+}
+
+// Middle tiles where large ones leave CUs without work, small ones where middle ones do.
+template <int LB, bool TRIANGLE, class EPILOGUE>
+hipError_t multiply(ProductArgs p, const Stack& a, const Stack& b, const typename EPILOGUE::Args& e, hipStream_t s) {
+  add_segments(p, operand(a.p), operand(b.p), 2);
+  p.batch_a = a.each;
+  p.batch_b = b.each;
+  if (large_tiles(p.m, p.n, p.batch, TRIANGLE)) return launch_tiles<f16_t, Large, kRow, LB, false, TRIANGLE, EPILOGUE>(p, e, s);
+  const uint64_t tm = (p.m + 127) / 128, tn = (p.n + 127) / 128;
+  if ((TRIANGLE ? tm * (tm + 1) / 2 : tm * tn) * p.batch >= kCus)
+    return launch_tiles<f16_t, Middle, kRow, LB, false, TRIANGLE, EPILOGUE>(p, e, s);
+  return launch_tiles<f16_t, Small, kRow, LB, false, TRIANGLE, EPILOGUE>(p, e, s);
+}
+
+template <class S>
+hipError_t start(const NewtonSchulzArgs& a, const Space& w, uint64_t n, uint64_t wide, bool tall, hipStream_t s) {
+  const uint64_t chunks = (a.rows * ((a.cols + 7) / 8) + 255) / 256;
+  const uint32_t groups = static_cast<uint32_t>(chunks < kNormGroups ? chunks : kNormGroups);
+  const S* x = static_cast<const S*>(a.x);
+  const uint32_t rows = static_cast<uint32_t>(a.rows), cols = static_cast<uint32_t>(a.cols);
+  RSX_TRY(launch(square_sums<S>, dim3(groups, static_cast<uint32_t>(a.batch)), 256, 0, s, x, a.x_ld, a.x_batch, rows, cols, w.sums));
+  const dim3 grid(static_cast<uint32_t>((wide + 63) / 64), static_cast<uint32_t>((n + 63) / 64), static_cast<uint32_t>(a.batch));
+  return tall ? launch(first_parts<S, true>, grid, 256, 0, s, x, a.x_ld, a.x_batch, rows, cols, w.sums, groups, a.eps, w.x, w.gram, w.poly)
+              : launch(first_parts<S, false>, grid, 256, 0, s, x, a.x_ld, a.x_batch, rows, cols, w.sums, groups, a.eps, w.x, w.gram, w.poly);
+}
+
+}  // namespace
+
+uint64_t newton_schulz_ws(uint64_t batch, uint64_t rows, uint64_t cols) {
+  Arena ws(nullptr);
+  plan(ws, batch, rows < cols ? rows : cols, rows < cols ? cols : rows);
+  return ws.at;
+}
+
+hipError_t launch_newton_schulz(const NewtonSchulzArgs& a, hipStream_t s) {
+  const bool tall = a.rows > a.cols;
+  const uint64_t n = tall ? a.cols : a.rows, wide = tall ? a.rows : a.cols;
+  Arena ws(a.ws);
+  const Space w = plan(ws, a.batch, n, wide);
+  RSX_TRY(a.type == RSX_FLOAT32    ? start<float>(a, w, n, wide, tall, s)
+          : a.type == RSX_BFLOAT16 ? start<bf16_t>(a, w, n, wide, tall, s) : start<f16_t>(a, w, n, wide, tall, s));
+  Stack x = w.x, y = w.y;
+  for (int step = 0; step < a.steps; ++step) {
+    const bool last = step + 1 == a.steps;
+    ProductArgs p = {};
+    p.batch = static_cast<uint32_t>(a.batch);
+    p.m = p.n = static_cast<uint32_t>(n);
+    p.k = static_cast<uint32_t>(wide);
+    RSX_TRY((multiply<kRow, true, Gram>(p, x, x, {w.gram}, s)));
+    p.k = static_cast<uint32_t>(n);
+    RSX_TRY((multiply<kRow, true, Poly>(p, w.gram, w.gram, {w.gram, w.poly, a.b, a.c}, s)));
+    p.n = static_cast<uint32_t>(wide);
+    RSX_TRY((multiply<kCol, false, Apply>(p, w.poly, x, {x, y, last ? a.out : nullptr, a.out_ld, a.out_batch, a.type, tall, a.a}, s)));
+    const Stack t = x;
+    x = y;
+    y = t;
+  }
+  return hipSuccess;
+}
+
+}  // namespace rsx

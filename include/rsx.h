@@ -530,6 +530,123 @@ rsx_status_t rsx_token_logprobs_grad_rest(const void* logits, size_t stride, rsx
                                           hipStream_t stream);
 
 /*
+ * The step's matrix products: the feed-forward block, the output matrix with
+ * its loss, and the orthogonalised update.  Rows, types, aliasing, workspaces
+ * and streams as above, with these differences.
+ * Sums are held in fp32.  fp32 matrices are multiplied as sums of three bf16
+ * values, which hold every bit of them (products of few rows: in fp32); a row
+ * or column with an infinity may come out as NaN.  Widths (elements of a row
+ * but the vocabulary) are below 2^22.
+ * Where a 16-bit matrix lies so that its rows are whole 16-byte chunks (address,
+ * stride and width multiples of 16 bytes, no stride of 0) it is read in place;
+ * from any other a copy is made in the workspace, in every call.  The
+ * _workspace_size functions have `copies` for that: 0 if every matrix that the
+ * call reads lies so, else 1.  A workspace for 1 is right for 0 too.
+ */
+
+/* Activations, in fp32: x / (1 + exp(-x)); x * Phi(x), Phi the normal
+ * distribution's; the same by x / (1 + exp(-2 sqrt(2 / pi) (x + 0.044715 x^3)));
+ * max(x, 0), with a slope of 0 at 0. */
+typedef enum {
+  RSX_ACT_SILU = 0,
+  RSX_ACT_GELU = 1,
+  RSX_ACT_GELU_TANH = 2,
+  RSX_ACT_RELU = 3
+} rsx_activation_t;
+
+/*
+ * Gated feed-forward block: with g = x w_gate^T and u = x w_up^T,
+ * out = (act(g) * u) w_down^T.
+ * x, out: [rows][dim]; w_gate, w_up: [hidden][dim]; w_down: [dim][hidden].
+ * gate, up: [rows][hidden] of `type`, dense: g and u for the gradient; or both
+ * null.  act(g) * u is rounded to `type` (fp32: kept whole) between the products.
+ * out overlaps nothing that is read.
+ */
+size_t rsx_feed_forward_workspace_size(size_t rows, size_t dim, size_t hidden, rsx_dtype_t type,
+                                       int copies);
+rsx_status_t rsx_feed_forward(const void* x, size_t x_stride, const void* w_gate,
+                              size_t gate_stride, const void* w_up, size_t up_stride,
+                              const void* w_down, size_t down_stride, void* out, size_t out_stride,
+                              void* gate, void* up, size_t rows, size_t dim, size_t hidden,
+                              rsx_activation_t activation, rsx_dtype_t type, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradients of rsx_feed_forward for dout, from the gate and up that it kept:
+ * ds = dout w_down, dg = ds * up * act'(gate), du = ds * act(gate);
+ * dx = dg w_gate + du w_up, dw_gate = dg^T x, dw_up = du^T x and
+ * dw_down = dout^T (act(gate) * up), the three added to what is there with
+ * `accumulate`.  dx may be null, and so may the three dw together.
+ * dg, du and act(gate) * up are rounded to `type` (fp32: kept whole).  The dw are
+ * of weight_grad_type: `type` or RSX_FLOAT32.
+ */
+size_t rsx_feed_forward_grad_workspace_size(size_t rows, size_t dim, size_t hidden,
+                                            rsx_dtype_t type, int copies);
+rsx_status_t rsx_feed_forward_grad(const void* dout, size_t dout_stride, const void* x,
+                                   size_t x_stride, const void* w_gate, size_t gate_stride,
+                                   const void* w_up, size_t up_stride, const void* w_down,
+                                   size_t down_stride, const void* gate, const void* up, void* dx,
+                                   size_t dx_stride, void* dw_gate, size_t dw_gate_stride,
+                                   void* dw_up, size_t dw_up_stride, void* dw_down,
+                                   size_t dw_down_stride, size_t rows, size_t dim, size_t hidden,
+                                   rsx_activation_t activation, rsx_dtype_t type,
+                                   rsx_dtype_t weight_grad_type, int accumulate, void* workspace,
+                                   size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * rsx_token_logprobs_rest of the logits scale * hidden weight^T, which are not
+ * stored: hidden [rows][dim], weight [vocab][dim] of one type.  The logits are
+ * fp32 here.  entropy and lse_rest may be null.  dim = 0: logits of 0.
+ */
+size_t rsx_linear_logprobs_workspace_size(size_t rows, size_t vocab, size_t dim, rsx_dtype_t type,
+                                          int copies);
+rsx_status_t rsx_linear_logprobs(const void* hidden, size_t hidden_stride, const void* weight,
+                                 size_t weight_stride, rsx_dtype_t type, const void* tokens,
+                                 rsx_dtype_t token_type, size_t rows, size_t vocab, size_t dim,
+                                 float scale, float* logprob, float* entropy, float* lse,
+                                 float* lse_rest, void* workspace, size_t workspace_bytes,
+                                 hipStream_t stream);
+
+/*
+ * Gradients of rsx_linear_logprobs: with dz as rsx_token_logprobs_grad_rest
+ * gives it (lse_rest may be null), times scale, dhidden = dz weight and
+ * dweight = dz^T hidden (with `accumulate` added to what is there).  Either may
+ * be null.  dweight is of dweight_type: `type` or RSX_FLOAT32.
+ * The vocabulary is taken in pieces, of which the logits are multiplied again.
+ * dz is rounded to bf16 (fp16 matrices: to 16 bits, with the range of fp32;
+ * fp32: kept whole).
+ */
+size_t rsx_linear_logprobs_grad_workspace_size(size_t rows, size_t vocab, size_t dim,
+                                               rsx_dtype_t type, int copies);
+rsx_status_t rsx_linear_logprobs_grad(const void* hidden, size_t hidden_stride, const void* weight,
+                                      size_t weight_stride, rsx_dtype_t type, const void* tokens,
+                                      rsx_dtype_t token_type, const float* lse,
+                                      const float* lse_rest, const float* entropy,
+                                      const float* dlogprob, const float* dentropy, void* dhidden,
+                                      size_t dhidden_stride, void* dweight, size_t dweight_stride,
+                                      rsx_dtype_t dweight_type, int accumulate, size_t rows,
+                                      size_t vocab, size_t dim, float scale, void* workspace,
+                                      size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Orthogonalised updates by Newton-Schulz products, of a stack of `batch`
+ * matrices [rows][cols], x_matrix (out_matrix) elements from one to the next:
+ * X = x / (|x| + eps) with the Frobenius norm |x|, then `steps` (at least 1) times
+ * A = X X^T, X = a X + (b A + c A A) X; for rows > cols the same of the transpose.
+ * out = X, of `type`; out == x with the same strides is allowed.
+ * X, A and b A + c A A are held to 22 bits and products summed in fp32; their
+ * values may not pass 16 (the singular values of X begin at 1 or less, and stay
+ * below 1.3 with the usual coefficients 3.4445, -4.775, 2.0315).
+ * A matrix of zeros gives zeros if eps > 0.  batch is below 2^16.
+ */
+size_t rsx_newton_schulz_workspace_size(size_t batch, size_t rows, size_t cols);
+rsx_status_t rsx_newton_schulz(const void* x, size_t x_stride, size_t x_matrix, void* out,
+                               size_t out_stride, size_t out_matrix, size_t batch, size_t rows,
+                               size_t cols, int steps, float a, float b, float c, float eps,
+                               rsx_dtype_t type, void* workspace, size_t workspace_bytes,
+                               hipStream_t stream);
+
+/*
  * First element of segment k in RSX_ALGO_RING all-reduce of `count`
  * elements over `nranks` ranks: min(k * ceil(count/nranks), count).
  * k may be 0..nranks (k = nranks gives count).  Returns 0 for nranks < 1.
