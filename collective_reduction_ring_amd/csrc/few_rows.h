@@ -2,8 +2,10 @@
 // read once, straight into the lanes that multiply it, and the time is the
 // memory's.
 //
-// A workgroup takes 16 * RG of the matrix's rows and its four waves share k out
-// in turns of U steps; their sums meet in LDS.  A step is one matrix
+// A workgroup takes 16 * RG of the matrix's rows and its waves share k out
+// in turns of U steps; their sums meet in LDS.  (131072 x 4096 bf16: eight waves and
+// turns of four steps 185 us; four and eight 191, with streamed loads, which fetch
+// a cache line again for its other half, 221.)  A step is one matrix
 // instruction of 32 k (16 bits) or four of 4 k (fp32, whose products stay fp32
 // here): a lane's 16 bytes of a row are its k, in the matrix and in x alike.
 #pragma once
@@ -20,7 +22,7 @@ struct FewArgs {
   uint32_t n, rows, k;  // rows of x, of the matrix; length of either
 };
 
-constexpr int kFewWaves = 4;
+constexpr int kFewWaves = 8;
 constexpr uint32_t kFewRows = 64;  // rows of x that this form takes
 
 template <class T>
@@ -36,11 +38,12 @@ __device__ __forceinline__ f32x4 few_mma(FewFrag<float>::type w, FewFrag<float>:
 __device__ __forceinline__ f32x4 few_mma(FewFrag<bf16_t>::type w, FewFrag<bf16_t>::type x, f32x4 c) { return mma(w, x, c); }
 __device__ __forceinline__ f32x4 few_mma(FewFrag<f16_t>::type w, FewFrag<f16_t>::type x, f32x4 c) { return mma(w, x, c); }
 
-// v[g][t] for the waves t' = t mod 4: lane l has x row 16 t + l % 16 and matrix
+// v[g][t] for the waves t mod kFewWaves: lane l has x row 16 t + l % 16 and matrix
 // rows first + 16 g + 4 (l / 16) .. + 3 (g from RG on: the second matrix's).
 template <class T, int NT, int RG, bool DUAL, class EPILOGUE>
-__global__ __launch_bounds__(64 * kFewWaves, 2) void few_rows_kernel(const FewArgs p, const typename EPILOGUE::Args e) {
-  constexpr int NM = DUAL ? 2 * RG : RG, N = FewFrag<T>::N, S = 4 * N, U = NT * NM >= 8 ? 4 : 8;
+__global__ __launch_bounds__(64 * kFewWaves, 4) void few_rows_kernel(const FewArgs p, const typename EPILOGUE::Args e) {
+  constexpr int NM = DUAL ? 2 * RG : RG, N = FewFrag<T>::N, S = 4 * N;
+  constexpr int U = NM + NT <= 5 ? 4 : 2;  // a turn's loads in registers: 80 at most, beside the sums
   typedef typename FewFrag<T>::type V;
   __shared__ f32x4 sums[kFewWaves][NM][NT][64];
   const uint32_t l = threadIdx.x % 64, wave = uniform(threadIdx.x / 64), r = l % 16, g = l / 16;
@@ -60,16 +63,22 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void few_rows_kernel(const FewAr
   for (int m = 0; m < NM; ++m)
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const uint32_t turns = p.k / (U * S);
-  for (uint32_t turn = wave; turn < turns; turn += kFewWaves) {
+  const uint32_t turns = p.k / (U * S), mine = turns > wave ? (turns - wave + kFewWaves - 1) / kFewWaves : 0;
+  // Workgroups begin in different places of the rows: row strides are often powers of two, and in step all would
+  // ask the same memory channels.
+  uint32_t at = mine ? static_cast<uint32_t>(block_id()) % mine : 0;
+  for (uint32_t i = 0; i < mine; ++i) {
+    const uint32_t turn = wave + at * kFewWaves;
+    at = at + 1 < mine ? at + 1 : 0;
     V w[U][NM], x[U][NT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
 #pragma unroll
-      for (int m = 0; m < NM; ++m) w[u][m] = load_once<T, N>(wr[m] + (turn * U + u) * S);
+      for (int m = 0; m < NM; ++m) w[u][m] = load_kept<T, N>(wr[m] + (turn * U + u) * S);
 #pragma unroll
       for (int t = 0; t < NT; ++t) x[u][t] = load_kept<T, N>(xr[t] + (turn * U + u) * S);
     }
+    __builtin_amdgcn_sched_barrier(0);  // a turn's loads are all on their way before the first is waited for
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
