@@ -91,10 +91,10 @@ struct Gate {
     if constexpr (sizeof(T) == 4) put<float, N>(e.s32 + m * n, c, n, s);
     else put_parts<T, N>(e.s, m, c, n, s);
   }
-  template <class T, class TILE>
+  template <class T, class TILE, int N>
   static __device__ __forceinline__ void run(const ProductArgs& p, const Where& w, const GateArgs& e,
-                                             const f32x4 (&acc)[TILE::TN][TILE::TM], RSX_LDS char* lds) {
-    staged<TILE, true>(w, acc, lds, [&](uint32_t m, uint32_t c, f32x8 g, f32x8 u) {
+                                             const f32x4 (&acc)[TILE::TN][N], uint32_t i0, RSX_LDS char* lds) {
+    staged<TILE, true, N>(w, acc, i0, lds, [&](uint32_t m, uint32_t c, f32x8 g, f32x8 u) {
       if (m < p.m) one<T, 8>(e, m, c, p.n, g, u);
     });
   }
@@ -115,10 +115,10 @@ struct GateGradArgs {
 
 struct GateGrad {
   typedef GateGradArgs Args;
-  template <class T, class TILE>
+  template <class T, class TILE, int N>
   static __device__ __forceinline__ void run(const ProductArgs& p, const Where& w, const GateGradArgs& e,
-                                             const f32x4 (&acc)[TILE::TN][TILE::TM], RSX_LDS char* lds) {
-    staged<TILE, false>(w, acc, lds, [&](uint32_t m, uint32_t c, f32x8 ds) {
+                                             const f32x4 (&acc)[TILE::TN][N], uint32_t i0, RSX_LDS char* lds) {
+    staged<TILE, false, N>(w, acc, i0, lds, [&](uint32_t m, uint32_t c, f32x8 ds) {
       if (m >= p.m || c >= ((p.n + 7) & ~7u)) return;
       const uint64_t row = static_cast<uint64_t>(m) * p.n;
       const f32x8 g = get_as<8>(e.type, e.gate, row, c, p.n), u = get_as<8>(e.type, e.up, row, c, p.n);
@@ -174,12 +174,13 @@ hipError_t few(const FeedForwardArgs& a, void* s, hipStream_t stream) {
   if (a.hidden) RSX_TRY((launch_few<T, 1, true, Gate>(p, e, stream)));
   p = {s, a.w_down.p, nullptr, sizeof(T) == 4 ? a.hidden : copy_ld(a.hidden), a.w_down.ld, 0, static_cast<uint32_t>(a.rows),
        static_cast<uint32_t>(a.dim), static_cast<uint32_t>(a.hidden)};
-  return launch_few<T, 1, false, FewStore>(p, {a.out, a.out_ld, a.type, nullptr, 0, nullptr}, stream);
+  return launch_few<T, 1, false, FewStore>(p, {a.out, a.out_ld, a.type, nullptr, 0}, stream);
 }
 
 struct Forward {
   Prepared x, wg, wu, wd;
   Parts s;
+  Schedule gate;
   void* split;
 };
 Forward plan(const FeedForwardArgs& a, Arena& ws) {
@@ -191,24 +192,16 @@ Forward plan(const FeedForwardArgs& a, Arena& ws) {
   f.wu = take_operand(ws, a.w_up, a.type, n, half, a.copies);
   f.wd = take_operand(ws, a.w_down, a.type, n, half, a.copies);
   f.s = take_parts(ws, a.rows, a.hidden, n);
-  f.split = ws.take(store_ws(a.rows, a.dim, a.hidden, n * (n + 1) / 2));
+  const uint64_t segs = n * (n + 1) / 2, split = store_ws(a.rows, a.dim, a.hidden, segs);
+  f.gate = schedule(a.rows, 2 * a.hidden, 1, steps_of(a.dim, segs), false, false);
+  f.split = ws.take(split > f.gate.bytes ? split : f.gate.bytes);
   return f;
-}
-
-template <class T>
-hipError_t gate(const ProductArgs& p, const GateArgs& e, hipStream_t s) {
-  return large_tiles(p.m, 2ull * p.n, 1, false) ? launch_tiles<T, Large, kRow, kRow, true, false, Gate>(p, e, s)
-                                                : launch_tiles<T, Middle, kRow, kRow, true, false, Gate>(p, e, s);
-}
-template <class T>
-hipError_t gate_grad(const ProductArgs& p, const GateGradArgs& e, hipStream_t s) {
-  return large_tiles(p.m, p.n, 1, false) ? launch_tiles<T, Large, kRow, kCol, false, false, GateGrad>(p, e, s)
-                                         : launch_tiles<T, Middle, kRow, kCol, false, false, GateGrad>(p, e, s);
 }
 
 struct Backward {
   Prepared dout, x, wg, wu, wd;
   Parts s, dg, du;
+  Schedule gate;
   void* split;
 };
 Backward plan(const FeedForwardGradArgs& a, Arena& ws) {
@@ -228,7 +221,12 @@ Backward plan(const FeedForwardGradArgs& a, Arena& ws) {
   b.dg = take_parts(ws, a.rows, a.hidden, n);
   b.du = take_parts(ws, a.rows, a.hidden, n);
   const uint64_t segs = n * (n + 1) / 2;
-  uint64_t split = a.dx ? store_ws(a.rows, a.dim, a.hidden, 2 * segs) : 0;
+  b.gate = schedule(a.rows, a.hidden, 1, steps_of(a.dim, segs), false, false);
+  uint64_t split = b.gate.bytes;
+  if (a.dx) {
+    const uint64_t x = store_ws(a.rows, a.dim, a.hidden, 2 * segs);
+    split = split < x ? x : split;
+  }
   if (a.dw_gate) {
     const uint64_t g = store_ws(a.hidden, a.dim, a.rows, segs), d = store_ws(a.dim, a.hidden, a.rows, segs);
     split = split < g ? g : split;
@@ -261,10 +259,11 @@ hipError_t launch_feed_forward(const FeedForwardArgs& a, hipStream_t s) {
   ProductArgs p = sizes(a.rows, a.hidden, a.dim);
   add_segments(p, f.x.op, f.wg.op, n, &f.wu.op);
   const GateArgs e = {f.s, nullptr, a.gate, a.up, a.act, a.type};
-  RSX_TRY(half ? gate<f16_t>(p, e, s) : gate<bf16_t>(p, e, s));
+  RSX_TRY((half ? launch_product<f16_t, kRow, kRow, true, false, Gate>(p, f.gate, f.split, e, s)
+                : launch_product<bf16_t, kRow, kRow, true, false, Gate>(p, f.gate, f.split, e, s)));
   p = sizes(a.rows, a.dim, a.hidden);
   add_segments(p, operand(f.s), f.wd.op, n);
-  return launch_store(half, kNT, p, {a.out, a.out_ld, a.type, nullptr, 0, nullptr}, f.split, s);
+  return launch_store(half, kNT, p, {a.out, a.out_ld, a.type, nullptr, 0}, f.split, s);
 }
 
 uint64_t feed_forward_grad_ws(const FeedForwardGradArgs& a) {
@@ -288,23 +287,24 @@ hipError_t launch_feed_forward_grad(const FeedForwardGradArgs& a, hipStream_t s)
   ProductArgs p = sizes(a.rows, a.hidden, a.dim);
   add_segments(p, b.dout.op, b.wd.op, n);
   const GateGradArgs e = {a.gate, a.up, b.s, b.dg, b.du, a.act, a.type};
-  if (a.rows && a.hidden) RSX_TRY(half ? gate_grad<f16_t>(p, e, s) : gate_grad<bf16_t>(p, e, s));
+  RSX_TRY((half ? launch_product<f16_t, kRow, kCol, false, false, GateGrad>(p, b.gate, b.split, e, s)
+                : launch_product<bf16_t, kRow, kCol, false, false, GateGrad>(p, b.gate, b.split, e, s)));
   if (a.dx) {
     p = sizes(a.rows, a.dim, a.hidden);
     add_segments(p, operand(b.dg), b.wg.op, n);
     add_segments(p, operand(b.du), b.wu.op, n);
-    RSX_TRY(launch_store(half, kNN, p, {a.dx, a.dx_ld, a.type, nullptr, 0, nullptr}, b.split, s));
+    RSX_TRY(launch_store(half, kNN, p, {a.dx, a.dx_ld, a.type, nullptr, 0}, b.split, s));
   }
   if (!a.dw_gate) return hipSuccess;
   p = sizes(a.hidden, a.dim, a.rows);
   add_segments(p, operand(b.dg), b.x.op, n);
-  RSX_TRY(launch_store(half, kTN, p, {a.dw_gate, a.dw_gate_ld, a.weight_type, nullptr, a.accumulate, nullptr}, b.split, s));
+  RSX_TRY(launch_store(half, kTN, p, {a.dw_gate, a.dw_gate_ld, a.weight_type, nullptr, a.accumulate}, b.split, s));
   p = sizes(a.hidden, a.dim, a.rows);
   add_segments(p, operand(b.du), b.x.op, n);
-  RSX_TRY(launch_store(half, kTN, p, {a.dw_up, a.dw_up_ld, a.weight_type, nullptr, a.accumulate, nullptr}, b.split, s));
+  RSX_TRY(launch_store(half, kTN, p, {a.dw_up, a.dw_up_ld, a.weight_type, nullptr, a.accumulate}, b.split, s));
   p = sizes(a.dim, a.hidden, a.rows);
   add_segments(p, b.dout.op, operand(b.s), n);
-  return launch_store(half, kTN, p, {a.dw_down, a.dw_down_ld, a.weight_type, nullptr, a.accumulate, nullptr}, b.split, s);
+  return launch_store(half, kTN, p, {a.dw_down, a.dw_down_ld, a.weight_type, nullptr, a.accumulate}, b.split, s);
 }
 
 }  // namespace rsx

@@ -59,45 +59,58 @@ struct SoftmaxArgs {
 
 struct Softmax {
   typedef SoftmaxArgs Args;
-  // N groups of four logits of one row, at columns c(j); those from `vocab` on do not count.
-  template <int N, class C>
-  static __device__ __forceinline__ Some take(const SoftmaxArgs& e, const f32x4 (&v)[N], C c, uint32_t vocab, int64_t token,
-                                              uint32_t row) {
+  // N groups of four logits of one row, at columns c(j).  EDGE: those from `vocab` on do not count.
+  template <bool EDGE, int N, class C>
+  static __device__ __forceinline__ Some take(const SoftmaxArgs& e, const f32x4 (&v)[N], C c, uint32_t vocab) {
     float z[4 * N];
     Some s = {-INFINITY, 0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < N; ++j)
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const uint32_t at = c(j) + x;
-        z[4 * j + x] = at < vocab ? v[j][x] * e.scale : -INFINITY;
+        z[4 * j + x] = v[j][x] * e.scale;
+        if (EDGE && c(j) + x >= vocab) z[4 * j + x] = -INFINITY;
         s.most = fmaxf(s.most, z[4 * j + x]);
-        if (at < vocab && at == token) e.picked[row] = z[4 * j + x];
       }
+    const float from = s.most == -INFINITY ? 0.0f : s.most;
 #pragma unroll
     for (int i = 0; i < 4 * N; ++i) {
-      const float d = less(z[i], s.most), x = __builtin_amdgcn_exp2f(d * kLog2e);
+      const float d = z[i] - from, x = __builtin_amdgcn_exp2f(d * kLog2e);
       s.sum += x;
-      s.gap += x == 0.0f ? 0.0f : x * d;
+      s.gap += x * fmaxf(d, -1e30f);  // 0 for a logit of minus infinity; a NaN shows in the sum
     }
     return s;
   }
-  template <class T, class TILE>
+  // The token's logit, where this lane has it.
+  template <int N, class C>
+  static __device__ __forceinline__ void pick(const SoftmaxArgs& e, const f32x4 (&v)[N], C c, int64_t token, uint32_t row) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (c(j) + x == token) e.picked[row] = v[j][x] * e.scale;
+  }
+  template <class T, class TILE, int N>
   static __device__ __forceinline__ void run(const ProductArgs& p, const Where& w, const SoftmaxArgs& e,
-                                             const f32x4 (&acc)[TILE::TN][TILE::TM], RSX_LDS char* lds) {
+                                             const f32x4 (&acc)[TILE::TN][N], uint32_t i0, RSX_LDS char* lds) {
     const Place<TILE> at(w);
     const uint32_t l = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const uint32_t first = w.n0 + uniform(wave) % TILE::WN * (TILE::TN * 16);  // this wave's columns
+    const bool edge = first + TILE::TN * 16 > p.n;
     RSX_LDS float* part = reinterpret_cast<RSX_LDS float*>(lds);  // [wave column][row of the tile][3]
     __builtin_amdgcn_s_waitcnt(0);  // loads of steps past the last one
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < TILE::TM; ++i) {
-      const uint32_t row = at.row(i);
+    for (int i = 0; i < N; ++i) {
+      const uint32_t row = at.row(i0 + i);
       const int64_t token = row < p.m ? token_at(e.tokens, e.wide, row) : -1;
       f32x4 v[TILE::TN];
 #pragma unroll
       for (int j = 0; j < TILE::TN; ++j) v[j] = acc[j][i];
-      Some s = take(e, v, [&](int j) { return at.col(j); }, row < p.m ? p.n : 0, token, row);
+      auto column = [&](int j) { return at.col(j); };
+      const bool mine = token >= first && token < min(first + TILE::TN * 16, p.n);
+      if (__ballot(mine) != 0) pick(e, v, column, mine ? token : -1, row);
+      Some s = edge ? take<true>(e, v, column, p.n) : take<false>(e, v, column, p.n);
       s = across(across(s, 16), 32);
       if (l < 16) {
         RSX_LDS float* to = part + ((wave % TILE::WN) * TILE::BM + (row - w.m0)) * 3;
@@ -108,6 +121,7 @@ struct Softmax {
     }
     __syncthreads();
     for (uint32_t r = threadIdx.x; r < TILE::BM && w.m0 + r < p.m; r += TILE::kThreads) {
+      if (N < TILE::TM && r / 16 % TILE::TM != i0) continue;
       Some s = {part[r * 3], part[r * 3 + 1], part[r * 3 + 2]};
 #pragma unroll
       for (int i = 1; i < TILE::WN; ++i) {
@@ -120,7 +134,9 @@ struct Softmax {
   template <class T, int RG>
   static __device__ __forceinline__ void few(const FewArgs& p, const SoftmaxArgs& e, uint32_t row, uint32_t c, const f32x4 (&v)[RG]) {
     const int64_t token = row < p.n ? token_at(e.tokens, e.wide, row) : -1;
-    Some s = take(e, v, [&](int j) { return c + 16 * j; }, row < p.n ? p.rows : 0, token, row);
+    auto column = [&](int j) { return c + 16 * j; };
+    pick(e, v, column, token >= 0 && token < p.rows ? token : -1, row);
+    Some s = take<true>(e, v, column, p.rows);
     s = across(across(s, 16), 32);
     if (row < p.n && threadIdx.x % 64 < 16)
       e.some[static_cast<uint64_t>(row) * e.tiles + c / (16 * RG)] = float4{s.most, s.sum, s.gap, 0.0f};
@@ -190,10 +206,10 @@ struct DzArgs {
 
 struct Dz {
   typedef DzArgs Args;
-  template <class T, class TILE>
+  template <class T, class TILE, int N>
   static __device__ __forceinline__ void run(const ProductArgs& p, const Where& w, const DzArgs& e,
-                                             const f32x4 (&acc)[TILE::TN][TILE::TM], RSX_LDS char* lds) {
-    staged<TILE, false>(w, acc, lds, [&](uint32_t row, uint32_t c, f32x8 v) {
+                                             const f32x4 (&acc)[TILE::TN][N], uint32_t i0, RSX_LDS char* lds) {
+    staged<TILE, false, N>(w, acc, i0, lds, [&](uint32_t row, uint32_t c, f32x8 v) {
       if (row >= p.m) return;
       const int64_t token = token_at(e.tokens, e.wide, row);
       const bool there = token >= 0 && static_cast<uint64_t>(token) < e.vocab;
@@ -236,19 +252,22 @@ struct Forward {
   float4* some;
   float* picked;
   uint32_t tiles;
-  bool few, large;
+  bool few;
+  Schedule spread;
+  void* pieces;
 };
 Forward plan(const LinearLogprobArgs& a, Arena& ws) {
   Forward f = {};
   const int n = a.type == RSX_FLOAT32 ? 3 : 1;
   const bool half = a.type == RSX_FLOAT16;
   f.few = a.rows <= kFewRows;
-  f.large = large_tiles(a.rows, a.vocab, 1, false);
-  const uint64_t width = f.few ? 16 * kFewGroups : f.large ? Large::BN : Middle::BN;
+  f.spread = schedule(a.rows, a.vocab, 1, steps_of(a.dim, n * (n + 1) / 2), false, false);
+  const uint64_t width = f.few ? 16 * kFewGroups : f.spread.tile == 0 ? Large::BN : Middle::BN;
   f.tiles = static_cast<uint32_t>((a.vocab + width - 1) / width);
   if (!f.few) {
     f.hidden = take_operand(ws, a.hidden, a.type, n, half, a.copies);
     f.weight = take_operand(ws, a.weight, a.type, n, half, a.copies);
+    f.pieces = ws.take(f.spread.bytes);
   }
   f.some = static_cast<float4*>(ws.take(a.rows * f.tiles * sizeof(float4)));
   f.picked = static_cast<float*>(ws.take(a.rows * 4));
@@ -292,22 +311,13 @@ Backward plan(const LinearLogprobGradArgs& a, Arena& ws) {
   for (const uint64_t v : {b.piece, last}) {
     if (v == 0) continue;
     const uint64_t h = a.dhidden ? store_ws(a.rows, a.dim, v, segs) : 0, w = a.dweight ? store_ws(v, a.dim, a.rows, segs) : 0;
+    const uint64_t z = schedule(a.rows, v, 1, steps_of(a.dim, n * (n + 1) / 2), false, false).bytes;
     split = split < h ? h : split;
     split = split < w ? w : split;
+    split = split < z ? z : split;
   }
   b.split = ws.take(split);
   return b;
-}
-
-template <class T>
-hipError_t softmax(const ProductArgs& p, const SoftmaxArgs& e, bool large, hipStream_t s) {
-  return large ? launch_tiles<T, Large, kRow, kRow, false, false, Softmax>(p, e, s)
-               : launch_tiles<T, Middle, kRow, kRow, false, false, Softmax>(p, e, s);
-}
-template <class T>
-hipError_t dlogits(const ProductArgs& p, const DzArgs& e, hipStream_t s) {
-  return large_tiles(p.m, p.n, 1, false) ? launch_tiles<T, Large, kRow, kRow, false, false, Dz>(p, e, s)
-                                         : launch_tiles<T, Middle, kRow, kRow, false, false, Dz>(p, e, s);
 }
 
 }  // namespace
@@ -334,7 +344,8 @@ hipError_t launch_linear_logprobs(const LinearLogprobArgs& a, hipStream_t s) {
     RSX_TRY(fill_operand(f.weight, a.weight, a.type, half, s));
     ProductArgs p = sizes(a.rows, a.vocab, a.dim);
     add_segments(p, f.hidden.op, f.weight.op, a.type == RSX_FLOAT32 ? 3 : 1);
-    RSX_TRY(half ? softmax<f16_t>(p, e, f.large, s) : softmax<bf16_t>(p, e, f.large, s));
+    RSX_TRY((half ? launch_product<f16_t, kRow, kRow, false, false, Softmax>(p, f.spread, f.pieces, e, s)
+                  : launch_product<bf16_t, kRow, kRow, false, false, Softmax>(p, f.spread, f.pieces, e, s)));
   }
   return launch(join_tiles, grid_of(a.rows), 256, 0, s,
                 {f.some, f.picked, a.tokens, a.logprob, a.entropy, a.lse, a.lse_rest, static_cast<uint32_t>(a.rows), f.tiles,
@@ -370,21 +381,23 @@ hipError_t launch_linear_logprobs_grad(const LinearLogprobGradArgs& a, hipStream
       ProductArgs p = sizes(a.rows, v, a.dim);
       add_segments(p, b.hidden.op, rows_from(b.weight.op), n);
       const DzArgs e = {a.tokens, a.lse, a.lse_rest, a.entropy, a.dlogprob, a.dentropy, b.dz, first, a.vocab, a.scale, a.wide};
-      RSX_TRY(half ? dlogits<f16_t>(p, e, s) : dlogits<bf16_t>(p, e, s));
+      const Schedule c = schedule(a.rows, v, 1, steps_of(a.dim, p.nseg), false, false);
+      RSX_TRY((half ? launch_product<f16_t, kRow, kRow, false, false, Dz>(p, c, b.split, e, s)
+                    : launch_product<bf16_t, kRow, kRow, false, false, Dz>(p, c, b.split, e, s)));
     }
     if (a.dweight) {
       ProductArgs p = sizes(v, a.dim, a.rows);
       add_segments(p, operand(b.dz), b.hidden2.op, n2);
       void* to = static_cast<char*>(a.dweight) + first * a.dweight_ld * es;
-      RSX_TRY(launch_store(false, kTN, p, {to, a.dweight_ld, a.weight_type, nullptr, a.accumulate, nullptr}, b.split, s));
+      RSX_TRY(launch_store(false, kTN, p, {to, a.dweight_ld, a.weight_type, nullptr, a.accumulate}, b.split, s));
     }
     if (a.dhidden) {
       ProductArgs p = sizes(a.rows, a.dim, v);
       add_segments(p, operand(b.dz), rows_from(b.weight2.op), n2);
       const bool last = first + v == a.vocab;
       const float* add = first ? b.sum : nullptr;
-      const StoreArgs e = last ? StoreArgs{a.dhidden, a.dhidden_ld, a.type, add, 0, nullptr}
-                               : StoreArgs{b.sum, a.dim, RSX_FLOAT32, add, 0, nullptr};
+      const StoreArgs e = last ? StoreArgs{a.dhidden, a.dhidden_ld, a.type, add, 0}
+                               : StoreArgs{b.sum, a.dim, RSX_FLOAT32, add, 0};
       RSX_TRY(launch_store(false, kNN, p, e, b.split, s));
     }
   }

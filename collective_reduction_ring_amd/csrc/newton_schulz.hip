@@ -143,11 +143,11 @@ struct GramArgs {
 };
 struct Gram {
   typedef GramArgs Args;
-  template <class T, class TILE>
+  template <class T, class TILE, int N>
   static __device__ __forceinline__ void run(const ProductArgs& p, const Where& w, const GramArgs& e,
-                                             const f32x4 (&acc)[TILE::TN][TILE::TM], RSX_LDS char* lds) {
+                                             const f32x4 (&acc)[TILE::TN][N], uint32_t i0, RSX_LDS char* lds) {
     const Parts to = e.to.at(w.batch);
-    staged<TILE, false>(w, acc, lds, [&](uint32_t m, uint32_t n, f32x8 v) { put_both(to, m, n, p.m, v * kUnscale); });
+    staged<TILE, false, N>(w, acc, i0, lds, [&](uint32_t m, uint32_t n, f32x8 v) { put_both(to, m, n, p.m, v * kUnscale); });
   }
 };
 
@@ -157,11 +157,11 @@ struct PolyArgs {
 };
 struct Poly {
   typedef PolyArgs Args;
-  template <class T, class TILE>
+  template <class T, class TILE, int N>
   static __device__ __forceinline__ void run(const ProductArgs& p, const Where& w, const PolyArgs& e,
-                                             const f32x4 (&acc)[TILE::TN][TILE::TM], RSX_LDS char* lds) {
+                                             const f32x4 (&acc)[TILE::TN][N], uint32_t i0, RSX_LDS char* lds) {
     const Parts gram = e.gram.at(w.batch), to = e.to.at(w.batch);
-    staged<TILE, false>(w, acc, lds, [&](uint32_t m, uint32_t n, f32x8 v) {
+    staged<TILE, false, N>(w, acc, i0, lds, [&](uint32_t m, uint32_t n, f32x8 v) {
       if (m >= p.m || n > m) return;
       const f32x8 g = get_parts<f16_t, 8>(gram, m, n);  // rows are filled to 8
       put_both(to, m, n, p.m, g * e.b + v * (e.c * kUnscale));
@@ -178,12 +178,12 @@ struct ApplyArgs {
 };
 struct Apply {
   typedef ApplyArgs Args;
-  template <class T, class TILE>
+  template <class T, class TILE, int N>
   static __device__ __forceinline__ void run(const ProductArgs& p, const Where& w, const ApplyArgs& e,
-                                             const f32x4 (&acc)[TILE::TN][TILE::TM], RSX_LDS char* lds) {
+                                             const f32x4 (&acc)[TILE::TN][N], uint32_t i0, RSX_LDS char* lds) {
     const Parts x = e.x.at(w.batch), to = e.to.at(w.batch);
     const uint64_t first = w.batch * e.each;
-    staged<TILE, false>(w, acc, lds, [&](uint32_t m, uint32_t n, f32x8 sum) {
+    staged<TILE, false, N>(w, acc, i0, lds, [&](uint32_t m, uint32_t n, f32x8 sum) {
       if (m >= p.m || n >= ((p.n + 7) & ~7u)) return;
       const f32x8 v = get_parts<f16_t, 8>(x, m, n) * e.a + sum * kUnscale;
       if (e.out == nullptr) {
@@ -202,6 +202,8 @@ struct Apply {
 struct Space {
   double* sums;
   Stack x, y, gram, poly;
+  Schedule gram_spread, poly_spread, apply_spread;
+  void* pieces;
 };
 Stack take_stack(Arena& ws, uint64_t batch, uint64_t rows, uint64_t cols) {
   Stack s = {};
@@ -216,20 +218,24 @@ Space plan(Arena& ws, uint64_t batch, uint64_t n, uint64_t wide) {
   p.y = take_stack(ws, batch, n, wide);
   p.gram = take_stack(ws, batch, n, n);
   p.poly = take_stack(ws, batch, n, n);
+  p.gram_spread = schedule(n, n, batch, steps_of(wide, 3), true, true);
+  p.poly_spread = schedule(n, n, batch, steps_of(n, 3), true, true);
+  p.apply_spread = schedule(n, wide, batch, steps_of(n, 3), false, true);
+  uint64_t most = p.gram_spread.bytes;
+  most = most < p.poly_spread.bytes ? p.poly_spread.bytes : most;
+  most = most < p.apply_spread.bytes ? p.apply_spread.bytes : most;
+  p.pieces = ws.take(most);
   return p;
 }
 
-// Middle tiles where large ones leave CUs without work, small ones where middle ones do.
 template <int LB, bool TRIANGLE, class EPILOGUE>
-hipError_t multiply(ProductArgs p, const Stack& a, const Stack& b, const typename EPILOGUE::Args& e, hipStream_t s) {
+hipError_t multiply(ProductArgs p, const Stack& a, const Stack& b, const Schedule& c, void* pieces, const typename EPILOGUE::Args& e,
+                    hipStream_t s) {
   add_segments(p, operand(a.p), operand(b.p), 2);
   p.batch_a = a.each;
   p.batch_b = b.each;
-  if (large_tiles(p.m, p.n, p.batch, TRIANGLE)) return launch_tiles<f16_t, Large, kRow, LB, false, TRIANGLE, EPILOGUE>(p, e, s);
-  const uint64_t tm = (p.m + 127) / 128, tn = (p.n + 127) / 128;
-  if ((TRIANGLE ? tm * (tm + 1) / 2 : tm * tn) * p.batch >= kCus)
-    return launch_tiles<f16_t, Middle, kRow, LB, false, TRIANGLE, EPILOGUE>(p, e, s);
-  return launch_tiles<f16_t, Small, kRow, LB, false, TRIANGLE, EPILOGUE>(p, e, s);
+  return c.tile == 2 ? launch_tiles<f16_t, Small, kRow, LB, false, TRIANGLE, EPILOGUE>(p, c, pieces, e, s)
+                     : launch_product<f16_t, kRow, LB, false, TRIANGLE, EPILOGUE>(p, c, pieces, e, s);
 }
 
 template <class S>
@@ -266,11 +272,11 @@ hipError_t launch_newton_schulz(const NewtonSchulzArgs& a, hipStream_t s) {
     p.batch = static_cast<uint32_t>(a.batch);
     p.m = p.n = static_cast<uint32_t>(n);
     p.k = static_cast<uint32_t>(wide);
-    RSX_TRY((multiply<kRow, true, Gram>(p, x, x, {w.gram}, s)));
+    RSX_TRY((multiply<kRow, true, Gram>(p, x, x, w.gram_spread, w.pieces, {w.gram}, s)));
     p.k = static_cast<uint32_t>(n);
-    RSX_TRY((multiply<kRow, true, Poly>(p, w.gram, w.gram, {w.gram, w.poly, a.b, a.c}, s)));
+    RSX_TRY((multiply<kRow, true, Poly>(p, w.gram, w.gram, w.poly_spread, w.pieces, {w.gram, w.poly, a.b, a.c}, s)));
     p.n = static_cast<uint32_t>(wide);
-    RSX_TRY((multiply<kCol, false, Apply>(p, w.poly, x, {x, y, last ? a.out : nullptr, a.out_ld, a.out_batch, a.type, tall, a.a}, s)));
+    RSX_TRY((multiply<kCol, false, Apply>(p, w.poly, x, w.apply_spread, w.pieces, {x, y, last ? a.out : nullptr, a.out_ld, a.out_batch, a.type, tall, a.a}, s)));
     const Stack t = x;
     x = y;
     y = t;

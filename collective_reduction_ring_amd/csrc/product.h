@@ -37,9 +37,10 @@ struct ProductArgs {
   uint32_t m, n, k;
   uint32_t nseg, seg_steps;   // segments; steps of each
   uint32_t tiles_m, tiles_n;
-  uint32_t splits, split_steps;  // the steps cut over workgroups, and a cut's steps
   uint32_t batch;
-  uint32_t tiles;                // of one matrix and cut: all, or those on and below the diagonal
+  uint32_t tiles;             // of one matrix: all, or those on and below the diagonal
+  uint32_t full, cuts;        // tiles that a workgroup has whole; workgroups that share the steps of each other one
+  float* pieces;              // a tile's sums for each of those
 };
 
 template <class T>
@@ -233,32 +234,46 @@ struct Int {
 };
 
 struct Where {
-  uint32_t m0, n0, batch, split;
+  uint32_t m0, n0, batch;
 };
 
+// Tile t of all matrices'.
 template <class TILE, bool DUAL, bool TRIANGLE>
-__device__ __forceinline__ Where where_of(const ProductArgs& p, uint32_t id) {
+__device__ __forceinline__ Where where_of(const ProductArgs& p, uint32_t t) {
   Where w;
-  uint32_t t = xcd_run(id, p.tiles * p.splits * p.batch);
-  w.batch = t / (p.tiles * p.splits);
-  t %= p.tiles * p.splits;
-  w.split = t / p.tiles;
+  w.batch = t / p.tiles;
   t %= p.tiles;
   uint32_t i, j;
-  if (TRIANGLE) {  // row after row; the square root is off by one at most
-    i = static_cast<uint32_t>((sqrtf(8.0f * static_cast<float>(t) + 1.0f) - 1.0f) * 0.5f);
-    while (static_cast<uint64_t>(i) * (i + 1) / 2 > t) --i;
-    while (static_cast<uint64_t>(i + 1) * (i + 2) / 2 <= t) ++i;
-    j = t - static_cast<uint32_t>(static_cast<uint64_t>(i) * (i + 1) / 2);
+  constexpr uint32_t kGroup = 8;
+  if (TRIANGLE) {
+    // Before row i are i (i + 1) / 2 tiles; the root says which row t would be in, row after row, and with it the group.
+    auto before = [](uint32_t row) { return static_cast<uint32_t>(static_cast<uint64_t>(row) * (row + 1) / 2); };
+    auto row_of = [&](uint32_t x) {
+      uint32_t r = static_cast<uint32_t>((sqrtf(8.0f * static_cast<float>(x) + 1.0f) - 1.0f) * 0.5f);  // off by one at most
+      while (before(r) > x) --r;
+      while (before(r + 1) <= x) ++r;
+      return r;
+    };
+    const uint32_t first = row_of(t) / kGroup * kGroup, rows = min(kGroup, p.tiles_m - first);
+    t -= before(first);
+    if (t < rows * first) {  // the group's columns up to the diagonal's block
+      i = first + t % rows;
+      j = t / rows;
+    } else {
+      t -= rows * first;
+      i = row_of(t);
+      j = first + t - before(i);
+      i += first;
+    }
   } else {
-    constexpr uint32_t kGroup = 8;
     const uint32_t group = t / (kGroup * p.tiles_n), first = group * kGroup, rows = min(kGroup, p.tiles_m - first);
     t -= group * kGroup * p.tiles_n;
     i = first + t % rows;
     j = t / rows;
   }
-  w.m0 = i * TILE::BM;
-  w.n0 = j * (DUAL ? TILE::BN / 2 : TILE::BN);
+  w.m0 = uniform(i * TILE::BM);
+  w.n0 = uniform(j * (DUAL ? TILE::BN / 2 : TILE::BN));
+  w.batch = uniform(w.batch);
   return w;
 }
 
@@ -275,8 +290,8 @@ __device__ __forceinline__ Where where_of(const ProductArgs& p, uint32_t id) {
 // where they start, and what waits with them is the matrix instructions behind
 // them (8192^3: 918 us with six of eight loads in one phase).
 template <class T, class TILE, int LA, int LB, bool DUAL>
-__device__ __forceinline__ void tile_product(const ProductArgs& p, const Where& w, const Stage& st0, const Stage& st1,
-                                             f32x4 (&acc)[TILE::TN][TILE::TM]) {
+__device__ __forceinline__ void tile_product(const ProductArgs& p, const Where& w, uint32_t begin, uint32_t end, const Stage& st0,
+                                             const Stage& st1, f32x4 (&acc)[TILE::TN][TILE::TM]) {
   constexpr int TM = TILE::TM, TN = TILE::TN, THREADS = TILE::kThreads, H = TM / 2;
   typedef Loader<LA, TILE::BM, THREADS, 2, H * 16, false> LoadA;
   typedef Loader<LB, TILE::BN, THREADS, 1, 0, DUAL> LoadB;
@@ -292,9 +307,6 @@ __device__ __forceinline__ void tile_product(const ProductArgs& p, const Where& 
 #pragma unroll
     for (int i = 0; i < TM; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  const uint32_t total = p.nseg * p.seg_steps;
-  const uint32_t begin = w.split * p.split_steps, end = min(total, begin + p.split_steps);
-  if (begin >= end) return;
   uint32_t s = begin / p.seg_steps, k = begin % p.seg_steps, ahead = begin;
   auto open = [&]() {
     const Segment& g = p.seg[s];
@@ -413,8 +425,9 @@ struct Place {
 // cache lines for the loads and stores of an epilogue, and its code once.
 // f(row, column, v), or of a double product f(row, column, v, v2).  A wave's
 // patch is its own; 16-byte chunks are moved by the row, against bank conflicts.
-template <class TILE, bool DUAL, class F>
-__device__ __forceinline__ void staged(const Where& w, const f32x4 (&acc)[TILE::TN][TILE::TM], RSX_LDS char* lds, F f) {
+// acc holds N of the wave's TM groups of 16 rows, from group i0 on.
+template <class TILE, bool DUAL, int N, class F>
+__device__ __forceinline__ void staged(const Where& w, const f32x4 (&acc)[TILE::TN][N], uint32_t i0, RSX_LDS char* lds, F f) {
   constexpr int COLS = TILE::TN * 16, CHUNKS = COLS / 4, WIDTH = DUAL ? COLS / 2 : COLS, LANES = WIDTH / 8, ROWS = 64 / LANES;
   static_assert(TILE::WM * TILE::WN * 16 * COLS * 4 <= TILE::kBytesB, "");
   const uint32_t l = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
@@ -423,9 +436,9 @@ __device__ __forceinline__ void staged(const Where& w, const f32x4 (&acc)[TILE::
   __builtin_amdgcn_s_waitcnt(0);  // loads of steps past the last one
   __syncthreads();
 #pragma nounroll
-  for (int i = 0; i < TILE::TM; ++i) {
+  for (int i = 0; i < N; ++i) {
 #pragma unroll
-    for (int q = 0; q < TILE::TM; ++q)
+    for (int q = 0; q < N; ++q)
       if (q == i) {
 #pragma unroll
         for (int j = 0; j < TILE::TN; ++j) *chunk(l % 16, j * 4 + l / 16) = acc[j][q];
@@ -434,7 +447,7 @@ __device__ __forceinline__ void staged(const Where& w, const f32x4 (&acc)[TILE::
     const uint32_t c = l % LANES;
 #pragma nounroll
     for (uint32_t r = l / LANES; r < 16; r += ROWS) {
-      const uint32_t row = w.m0 + wave / TILE::WN * (TILE::TM * 16) + i * 16 + r, col = w.n0 + wave % TILE::WN * WIDTH + c * 8;
+      const uint32_t row = w.m0 + wave / TILE::WN * (TILE::TM * 16) + (i0 + i) * 16 + r, col = w.n0 + wave % TILE::WN * WIDTH + c * 8;
       const f32x8 v = __builtin_shufflevector(*chunk(r, 2 * c), *chunk(r, 2 * c + 1), 0, 1, 2, 3, 4, 5, 6, 7);
       if constexpr (DUAL) {
         f(row, col, v,
@@ -520,16 +533,71 @@ __device__ __forceinline__ typename Vec<float, N>::type get_parts(const Parts& p
   return v;
 }
 
+// A tile's sums as they lie in the lanes.
+template <class TILE>
+__device__ __forceinline__ f32x4* sums_at(const ProductArgs& p, uint32_t slot) {
+  return reinterpret_cast<f32x4*>(p.pieces) + static_cast<uint64_t>(slot) * (TILE::TN * TILE::TM * TILE::kThreads) + threadIdx.x;
+}
 template <class T, class TILE, int LA, int LB, bool DUAL, bool TRIANGLE, class EPILOGUE>
-__global__ __launch_bounds__(TILE::kThreads, 2) void product_kernel(const ProductArgs p, const typename EPILOGUE::Args e) {
+__global__ __launch_bounds__(TILE::kThreads, 2) void full_tiles(const ProductArgs p, const typename EPILOGUE::Args e) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host's compiler takes no part in the body
   const uint64_t id = block_id();
-  if (id >= static_cast<uint64_t>(p.tiles) * p.splits * p.batch) return;
+  if (id >= p.full) return;
   RSX_PRODUCT_LDS(TILE, st0, st1);
-  const Where w = where_of<TILE, DUAL, TRIANGLE>(p, static_cast<uint32_t>(id));
+  const Where w = where_of<TILE, DUAL, TRIANGLE>(p, xcd_run(static_cast<uint32_t>(id), p.full));
   f32x4 acc[TILE::TN][TILE::TM];
-  tile_product<T, TILE, LA, LB, DUAL>(p, w, st0, st1, acc);
-  EPILOGUE::template run<T, TILE>(p, w, e, acc, st0.b);
+  tile_product<T, TILE, LA, LB, DUAL>(p, w, 0, p.nseg * p.seg_steps, st0, st1, acc);
+  EPILOGUE::template run<T, TILE, TILE::TM>(p, w, e, acc, 0, st0.b);
+#endif
+}
+
+// The tiles past the last full round of the CUs, few of them: `cuts` workgroups
+// have a stretch of each one's steps, all of them in step (the first stretches of
+// all tiles, then the second ones), so that what their rows and columns have in
+// common is read once.  Another launch adds a tile's pieces in their order and
+// has its epilogue.  (The tiles' steps laid end to end and shared out evenly, any
+// number of tiles, were slower than an unfilled round: workgroups at different k
+// share nothing in the L2.)
+template <class T, class TILE, int LA, int LB, bool DUAL, bool TRIANGLE>
+__global__ __launch_bounds__(TILE::kThreads, 2) void cut_tiles(const ProductArgs p) {
+#ifdef __HIP_DEVICE_COMPILE__
+  const uint64_t id = block_id();
+  const uint32_t rest = p.tiles * p.batch - p.full, total = p.nseg * p.seg_steps;
+  if (id >= static_cast<uint64_t>(rest) * p.cuts) return;
+  RSX_PRODUCT_LDS(TILE, st0, st1);
+  const uint32_t slot = xcd_run(static_cast<uint32_t>(id), rest * p.cuts), cut = slot / rest;
+  const Where w = where_of<TILE, DUAL, TRIANGLE>(p, p.full + slot % rest);
+  f32x4 acc[TILE::TN][TILE::TM];
+  tile_product<T, TILE, LA, LB, DUAL>(p, w, static_cast<uint32_t>(static_cast<uint64_t>(total) * cut / p.cuts),
+                                      static_cast<uint32_t>(static_cast<uint64_t>(total) * (cut + 1) / p.cuts), st0, st1, acc);
+  f32x4* q = sums_at<TILE>(p, slot);
+#pragma unroll
+  for (int j = 0; j < TILE::TN; ++j)
+#pragma unroll
+    for (int i = 0; i < TILE::TM; ++i) q[(j * TILE::TM + i) * TILE::kThreads] = acc[j][i];
+#endif
+}
+
+// A workgroup for each group of 16 rows of the tile's waves.
+template <class T, class TILE, bool DUAL, bool TRIANGLE, class EPILOGUE>
+__global__ __launch_bounds__(TILE::kThreads, 2) void finish_tiles(const ProductArgs p, const typename EPILOGUE::Args e) {
+#ifdef __HIP_DEVICE_COMPILE__
+  const uint64_t id = block_id();
+  const uint32_t rest = p.tiles * p.batch - p.full;
+  if (id >= static_cast<uint64_t>(rest) * TILE::TM) return;
+  __shared__ __attribute__((aligned(1024))) char lds[TILE::kBytesB];
+  const uint32_t tile = static_cast<uint32_t>(id / TILE::TM), i0 = static_cast<uint32_t>(id % TILE::TM);
+  const Where w = where_of<TILE, DUAL, TRIANGLE>(p, p.full + tile);
+  f32x4 acc[TILE::TN][1];
+#pragma unroll
+  for (int j = 0; j < TILE::TN; ++j) acc[j][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (uint32_t cut = 0; cut < p.cuts; ++cut) {
+    const f32x4* q = sums_at<TILE>(p, cut * rest + tile) + i0 * TILE::kThreads;
+#pragma unroll
+    for (int j = 0; j < TILE::TN; ++j) acc[j][0] += q[j * TILE::TM * TILE::kThreads];
+  }
+  EPILOGUE::template run<T, TILE, 1>(p, w, e, acc, i0, (RSX_LDS char*)lds);
 #endif
 }
 
@@ -555,36 +623,47 @@ inline void add_segments(ProductArgs& p, const Operand& a, const Operand& b, int
       p.seg[p.nseg++] = {a.part[i], b.part[sum - i], b2 ? b2->part[sum - i] : nullptr, a.ld, b.ld, b2 ? b2->ld : 0};
 }
 
+// How a product m x n of `steps` steps is spread over the CUs: the tile, and how
+// many tiles a workgroup has whole; the others' steps are cut.
+struct Schedule {
+  int tile;  // 0 large, 1 middle, 2 small
+  uint32_t full, cuts;
+  uint64_t bytes;  // of the pieces' sums
+};
+Schedule schedule(uint64_t m, uint64_t n, uint64_t batch, uint64_t steps, bool triangle, bool small);
+
+// Sets what a schedule says; n as the schedule's (of a double product, both matrices' columns).
 template <class TILE>
-void set_tiles(ProductArgs& p, bool dual, bool triangle) {
+void set_tiles(ProductArgs& p, const Schedule& c, void* pieces, bool dual, bool triangle) {
+  const uint32_t bn = dual ? TILE::BN / 2 : TILE::BN;
   p.seg_steps = p.k == 0 ? 1 : (p.k + kStep - 1) / kStep;
   p.tiles_m = (p.m + TILE::BM - 1) / TILE::BM;
-  p.tiles_n = (p.n + (dual ? TILE::BN / 2 : TILE::BN) - 1) / (dual ? TILE::BN / 2 : TILE::BN);
-  const uint64_t all = static_cast<uint64_t>(p.tiles_m) * p.tiles_n;
-  p.tiles = static_cast<uint32_t>(triangle ? static_cast<uint64_t>(p.tiles_m) * (p.tiles_m + 1) / 2 : all);
-  if (p.splits == 0) p.splits = 1;
-  const uint32_t total = p.nseg * p.seg_steps;
-  p.split_steps = (total + p.splits - 1) / p.splits;
-}
-
-// Which tile finishes first: a CU has one large tile at a time or two middle
-// ones; rounds of each, a large tile's work being four middle ones' at 0.9 of
-// their time (8192^3: 0.90 ms and 0.98 ms).
-inline bool large_tiles(uint64_t m, uint64_t n, uint64_t batch, bool triangle) {
-  auto count = [&](uint64_t bm, uint64_t bn) {
-    const uint64_t tm = (m + bm - 1) / bm, tn = (n + bn - 1) / bn;
-    return (triangle ? tm * (tm + 1) / 2 : tm * tn) * batch;
-  };
-  const uint64_t large = (count(256, 256) + kCus - 1) / kCus, middle = (count(128, 128) + 2 * kCus - 1) / (2 * kCus);
-  return large * 36 <= middle * 20;
+  p.tiles_n = (p.n + bn - 1) / bn;
+  p.tiles = static_cast<uint32_t>(triangle ? static_cast<uint64_t>(p.tiles_m) * (p.tiles_m + 1) / 2
+                                           : static_cast<uint64_t>(p.tiles_m) * p.tiles_n);
+  p.full = c.full;
+  p.cuts = c.cuts;
+  p.pieces = static_cast<float*>(pieces);
 }
 
 template <class T, class TILE, int LA, int LB, bool DUAL, bool TRIANGLE, class EPILOGUE>
-hipError_t launch_tiles(ProductArgs p, const typename EPILOGUE::Args& e, hipStream_t s) {
-  set_tiles<TILE>(p, DUAL, TRIANGLE);
-  const uint64_t groups = static_cast<uint64_t>(p.tiles) * p.splits * p.batch;
-  if (groups == 0) return hipSuccess;
-  return launch(product_kernel<T, TILE, LA, LB, DUAL, TRIANGLE, EPILOGUE>, grid_of(groups), TILE::kThreads, 0, s, p, e);
+hipError_t launch_tiles(ProductArgs p, const Schedule& c, void* pieces, const typename EPILOGUE::Args& e, hipStream_t s) {
+  set_tiles<TILE>(p, c, pieces, DUAL, TRIANGLE);
+  if (p.full != 0) {
+    const hipError_t st = launch(full_tiles<T, TILE, LA, LB, DUAL, TRIANGLE, EPILOGUE>, grid_of(p.full), TILE::kThreads, 0, s, p, e);
+    if (st != hipSuccess) return st;
+  }
+  const uint32_t rest = p.tiles * p.batch - p.full;
+  if (rest == 0) return hipSuccess;
+  const hipError_t st = launch(cut_tiles<T, TILE, LA, LB, DUAL, TRIANGLE>, grid_of(static_cast<uint64_t>(rest) * p.cuts), TILE::kThreads, 0, s, p);
+  if (st != hipSuccess) return st;
+  return launch(finish_tiles<T, TILE, DUAL, TRIANGLE, EPILOGUE>, grid_of(static_cast<uint64_t>(rest) * TILE::TM), TILE::kThreads, 0, s, p,
+                e);
+}
+template <class T, int LA, int LB, bool DUAL, bool TRIANGLE, class EPILOGUE>
+hipError_t launch_product(const ProductArgs& p, const Schedule& c, void* pieces, const typename EPILOGUE::Args& e, hipStream_t s) {
+  return c.tile == 0 ? launch_tiles<T, Large, LA, LB, DUAL, TRIANGLE, EPILOGUE>(p, c, pieces, e, s)
+                     : launch_tiles<T, Middle, LA, LB, DUAL, TRIANGLE, EPILOGUE>(p, c, pieces, e, s);
 }
 
 }  // namespace rsx

@@ -15,18 +15,16 @@ struct StoreArgs {
   int type;
   const float* add;  // fp32 [m][n] to add, or null
   int accumulate;    // add what `out` holds
-  float* partial;    // fp32 [split][m][n] instead, for reduce_splits
 };
 
-// How many ways the steps of a product of few tiles are cut, and the bytes of
-// the cuts' sums.
-uint32_t store_splits(uint64_t m, uint64_t n, uint64_t steps);
-inline uint64_t store_ws(uint64_t m, uint64_t n, uint64_t k, uint64_t segments) {
-  const uint32_t splits = store_splits(m, n, segments * ((k + kStep - 1) / kStep));
-  return splits > 1 ? splits * m * n * 4 : 0;
+// Steps of a product of `segments` times k.
+inline uint64_t steps_of(uint64_t k, uint64_t segments) { return segments * (k == 0 ? 1 : (k + kStep - 1) / kStep); }
+inline Schedule store_schedule(uint64_t m, uint64_t n, uint64_t k, uint64_t segments) {
+  return schedule(m, n, 1, steps_of(k, segments), false, false);
 }
+inline uint64_t store_ws(uint64_t m, uint64_t n, uint64_t k, uint64_t segments) { return store_schedule(m, n, k, segments).bytes; }
 // half: the parts are fp16, else bf16.  ws: store_ws bytes.
-hipError_t launch_store(bool half, Layouts l, ProductArgs p, StoreArgs e, void* ws, hipStream_t s);
+hipError_t launch_store(bool half, Layouts l, ProductArgs p, const StoreArgs& e, void* ws, hipStream_t s);
 
 // Rows of a copy start on cache lines.
 inline uint64_t copy_ld(uint64_t cols) { return (cols + 63) & ~63ull; }

@@ -6,45 +6,23 @@ namespace {
 
 struct Store {
   typedef StoreArgs Args;
-  template <class T, class TILE>
+  template <class T, class TILE, int N>
   static __device__ __forceinline__ void run(const ProductArgs& p, const Where& w, const StoreArgs& e,
-                                             const f32x4 (&acc)[TILE::TN][TILE::TM], RSX_LDS char* lds) {
-    staged<TILE, false>(w, acc, lds, [&](uint32_t m, uint32_t n, f32x8 v) {
+                                             const f32x4 (&acc)[TILE::TN][N], uint32_t i0, RSX_LDS char* lds) {
+    staged<TILE, false, N>(w, acc, i0, lds, [&](uint32_t m, uint32_t n, f32x8 v) {
       if (m >= p.m || n >= p.n) return;
-      if (e.partial) {
-        put<float, 8>(e.partial + (static_cast<uint64_t>(w.split) * p.m + m) * p.n, n, p.n, v);
-      } else {
-        if (e.add) v += get<float, 8>(e.add + static_cast<uint64_t>(m) * p.n, n, p.n);
-        if (e.accumulate) v += get_as<8>(e.type, e.out, m * e.ld, n, p.n);
-        put_as<8>(e.type, e.out, m * e.ld, n, p.n, v);
-      }
+      if (e.add) v += get<float, 8>(e.add + static_cast<uint64_t>(m) * p.n, n, p.n);
+      if (e.accumulate) v += get_as<8>(e.type, e.out, m * e.ld, n, p.n);
+      put_as<8>(e.type, e.out, m * e.ld, n, p.n, v);
     });
   }
 };
 
-// The cuts' sums, added in their order.
-__global__ __launch_bounds__(256) void reduce_splits(const float* partial, uint32_t splits, uint32_t m, uint32_t n, StoreArgs e) {
-  const uint32_t chunks = (n + 3) / 4;
-  const uint64_t t = block_id() * 256 + threadIdx.x;
-  if (t >= static_cast<uint64_t>(m) * chunks) return;
-  const uint64_t row = t / chunks;
-  const uint32_t c = static_cast<uint32_t>(t % chunks) * 4;
-  f32x4 v = get<float, 4>(partial + row * n, c, n);
-  for (uint32_t s = 1; s < splits; ++s) v += get<float, 4>(partial + (s * static_cast<uint64_t>(m) + row) * n, c, n);
-  if (e.add) v += get<float, 4>(e.add + row * n, c, n);
-  if (e.accumulate) v += get_as<4>(e.type, e.out, row * e.ld, c, n);
-  put_as<4>(e.type, e.out, row * e.ld, c, n, v);
-}
-
-template <class T, int LA, int LB>
-hipError_t store(const ProductArgs& p, const StoreArgs& e, bool large, hipStream_t s) {
-  return large ? launch_tiles<T, Large, LA, LB, false, false, Store>(p, e, s)
-               : launch_tiles<T, Middle, LA, LB, false, false, Store>(p, e, s);
-}
 template <class T>
-hipError_t store(Layouts l, const ProductArgs& p, const StoreArgs& e, bool large, hipStream_t s) {
-  return l == kNT ? store<T, kRow, kRow>(p, e, large, s)
-                  : l == kNN ? store<T, kRow, kCol>(p, e, large, s) : store<T, kCol, kCol>(p, e, large, s);
+hipError_t store(Layouts l, const ProductArgs& p, const Schedule& c, const StoreArgs& e, void* ws, hipStream_t s) {
+  return l == kNT   ? launch_product<T, kRow, kRow, false, false, Store>(p, c, ws, e, s)
+         : l == kNN ? launch_product<T, kRow, kCol, false, false, Store>(p, c, ws, e, s)
+                    : launch_product<T, kCol, kCol, false, false, Store>(p, c, ws, e, s);
 }
 
 // A workgroup moves one stretch of 2048 elements of a row, eight a lane.
@@ -74,26 +52,48 @@ hipError_t copy(const Matrix& m, const Parts& dst, hipStream_t s) {
 
 }  // namespace
 
-uint32_t store_splits(uint64_t m, uint64_t n, uint64_t steps) {
-  if (m == 0 || n == 0 || large_tiles(m, n, 1, false)) return 1;
-  const uint64_t tiles = ((m + 127) / 128) * ((n + 127) / 128);
-  // Two middle tiles a CU; a cut of fewer than 8 steps is mostly its beginning and its end.
-  uint64_t splits = 2 * kCus / tiles;
-  if (splits > steps / 8) splits = steps / 8;
-  if (splits > 16) splits = 16;
-  return splits < 2 ? 1 : static_cast<uint32_t>(splits);
+// The times are in units of a large tile's step with every CU at one, 1.75 us: what
+// the chip's power allows, so that fewer tiles at a time run faster, but not in
+// proportion.  A CU holds one large tile at a time, two middle or four small ones.
+// A tile begins and ends in two to three steps' time.  Cut tiles cost their sums'
+// way through memory (a large tile's are 256 KB) and two more launches.
+Schedule schedule(uint64_t m, uint64_t n, uint64_t batch, uint64_t steps, bool triangle, bool small) {
+  Schedule best = {1, 0, 0, 0};
+  if (m == 0 || n == 0 || batch == 0) return best;
+  constexpr uint64_t kSide[3] = {256, 128, 64}, kHeld[3] = {1, 2, 4};
+  constexpr double kLeast[3] = {0.5, 0.28, 0.14}, kMost[3] = {1.0, 0.56, 0.45}, kEnds[3] = {2.5, 2.0, 1.5}, kPiece[3] = {0.4, 0.25, 0.15};
+  double least = 1e300;
+  for (int i = 0; i < (small ? 3 : 2); ++i) {
+    const uint64_t tm = (m + kSide[i] - 1) / kSide[i], tn = (n + kSide[i] - 1) / kSide[i], slots = kHeld[i] * kCus;
+    const uint64_t tiles = (triangle ? tm * (tm + 1) / 2 : tm * tn) * batch, rest = tiles % slots, rounds = tiles / slots;
+    // of `count` tiles at a time
+    auto rate = [&](uint64_t count) {
+      return kLeast[i] + (kMost[i] - kLeast[i]) * static_cast<double>(count) / static_cast<double>(slots);
+    };
+    const double s = static_cast<double>(steps), whole = static_cast<double>(rounds) * (kMost[i] * s + kEnds[i]);
+    const double apart = whole + (rest ? rate(rest) * s + kEnds[i] : 0.0);
+    if (apart < least) {
+      least = apart;
+      best = {i, static_cast<uint32_t>(tiles), 0, 0};
+    }
+    uint64_t cuts = rest ? slots / rest : 0;
+    cuts = cuts > steps / 4 ? steps / 4 : cuts;  // a piece of fewer steps is mostly its ends
+    cuts = cuts > 16 ? 16 : cuts;
+    if (cuts < 2) continue;
+    const double cut = whole + rate(rest * cuts) * (s / static_cast<double>(cuts)) + kEnds[i] + 5.0 + kPiece[i] * static_cast<double>(cuts);
+    if (cut < least) {
+      least = cut;
+      best = {i, static_cast<uint32_t>(tiles - rest), static_cast<uint32_t>(cuts), rest * cuts * kSide[i] * kSide[i] * 4};
+    }
+  }
+  return best;
 }
 
-hipError_t launch_store(bool half, Layouts l, ProductArgs p, StoreArgs e, void* ws, hipStream_t s) {
+hipError_t launch_store(bool half, Layouts l, ProductArgs p, const StoreArgs& e, void* ws, hipStream_t s) {
   if (p.m == 0 || p.n == 0) return hipSuccess;
   p.batch = 1;
-  const bool large = large_tiles(p.m, p.n, 1, false);
-  p.splits = store_splits(p.m, p.n, p.nseg * ((p.k + static_cast<uint64_t>(kStep) - 1) / kStep));
-  e.partial = p.splits > 1 ? static_cast<float*>(ws) : nullptr;
-  const hipError_t st = half ? store<f16_t>(l, p, e, large, s) : store<bf16_t>(l, p, e, large, s);
-  if (st != hipSuccess || p.splits == 1) return st;
-  const uint64_t groups = (static_cast<uint64_t>(p.m) * ((p.n + 3) / 4) + 255) / 256;
-  return launch(reduce_splits, grid_of(groups), 256, 0, s, static_cast<const float*>(ws), p.splits, p.m, p.n, e);
+  const Schedule c = store_schedule(p.m, p.n, p.k, p.nseg);
+  return half ? store<f16_t>(l, p, c, e, ws, s) : store<bf16_t>(l, p, c, e, ws, s);
 }
 
 hipError_t launch_copy(const Matrix& m, int type, const Parts& dst, bool half, hipStream_t s) {
