@@ -634,7 +634,8 @@ rsx_status_t rsx_linear_logprobs_grad(const void* hidden, size_t hidden_stride, 
  * X = x / (|x| + eps) with the Frobenius norm |x|, then `steps` (at least 1) times
  * A = X X^T, X = a X + (b A + c A A) X; for rows > cols the same of the transpose.
  * out = X, of `type`; out == x with the same strides is allowed.
- * X, A and b A + c A A are held to 22 bits and products summed in fp32; their
+ * X, A and b A + c A A are held to 22 bits and products summed in fp32 (of a
+ * bf16 update's last step, the products are of 11 bits); their
  * values may not pass 16 (the singular values of X begin at 1 or less, and stay
  * below 1.3 with the usual coefficients 3.4445, -4.775, 2.0315).
  * A matrix of zeros gives zeros if eps > 0.  batch is below 2^16.

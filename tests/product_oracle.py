@@ -154,30 +154,32 @@ def linear_logprobs_grad(hidden, weight, tokens, lse, ent, g, d, scale):
 USUAL = (3.4445, -4.7750, 2.0315)
 
 
-def newton_schulz(x, steps, coefficients, eps, noise=None):
+def newton_schulz(x, steps, coefficients, eps, noise=None, dtype=torch.float32):
     """x (rows, cols) orthogonalised in 64 bits.  With a generator as `noise`, every rounding of the kernel is put in
-    as a random error of the size of its bound: 2^-22 of what two fp16 parts keep, and of a product's sum 2 U of the
-    root of the number of its terms (three for each k) times the root of the sum of their squares."""
+    as a random error of the size of its bound: 2^-22 of what two fp16 parts keep (2^-11 of the operands of a bf16
+    update's last products, which are the first parts alone), and of a product's sum 2 U of the root of the number
+    of its terms (three for each k) times the root of the sum of their squares."""
     a, b, c = (float(torch.tensor(v, dtype=torch.float32)) for v in coefficients)
     x = x.double()
     tall = x.shape[0] > x.shape[1]
     x = x.t() if tall else x
 
-    def keep(v):
-        if noise is None:
-            return v
-        r = torch.randint(0, 2, v.shape, generator=noise, dtype=torch.float64).to(v.device) * 2 - 1
-        return v + r * (2.0 ** -22 * v.abs() + 2.0 ** -37)
+    def signs(v):
+        return torch.randint(0, 2, v.shape, generator=noise, dtype=torch.float64).to(v.device) * 2 - 1
 
-    def product(p, q):
+    def keep(v, bits=2.0 ** -22):
+        return v if noise is None else v + signs(v) * (bits * v.abs() + 2.0 ** -37)
+
+    def product(p, q, single):
+        if noise is not None and single:
+            # one rounding of a matrix, and of what is multiplied with it
+            p, q = keep(p, 2.0 ** -11), keep(q, 2.0 ** -11)
         v = p @ q
-        if noise is None:
-            return v
-        r = torch.randint(0, 2, v.shape, generator=noise, dtype=torch.float64).to(v.device) * 2 - 1
-        return v + r * 2 * U * math.sqrt(3 * p.shape[1]) * ((p * p) @ (q * q)).sqrt()
+        return v if noise is None else v + signs(v) * 2 * U * math.sqrt(3 * p.shape[1]) * ((p * p) @ (q * q)).sqrt()
     x = keep(x / (x.norm() + float(torch.tensor(eps, dtype=torch.float32))))
-    for _ in range(steps):
-        gram = keep(product(x, x.t()))
-        poly = keep(b * gram + c * product(gram, gram))
-        x = keep(a * x + product(poly, x))
+    for step in range(steps):
+        single = dtype == torch.bfloat16 and step and step + 1 == steps
+        gram = keep(product(x, x.t(), single))
+        poly = keep(b * gram + c * product(gram, gram, single))
+        x = keep(a * x + product(poly, x, single))
     return x.t() if tall else x

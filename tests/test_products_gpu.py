@@ -332,10 +332,10 @@ def stacked(host, pad):
     return view
 
 
-def ortho_bound(x, steps, coefficients):
+def ortho_bound(x, steps, coefficients, t):
     """(result, bound of any element): four times the furthest of three runs with random errors in every rounding."""
     ref = po.newton_schulz(x, steps, coefficients, 1e-7)
-    far = max((po.newton_schulz(x, steps, coefficients, 1e-7, torch.Generator().manual_seed(s)) - ref).abs().max().item() for s in range(3))
+    far = max((po.newton_schulz(x, steps, coefficients, 1e-7, torch.Generator().manual_seed(s), t) - ref).abs().max().item() for s in range(3))
     return ref, 4 * far + 2.0 ** -36
 
 
@@ -351,7 +351,7 @@ def test_newton_schulz(shape, t, steps, coefficients, pad):
     plan()
     assert plan.out.is_contiguous() and same_bits(d.cpu().contiguous(), x)
     for one, got in zip(x.reshape(-1, *shape[-2:]), plan.out.reshape(-1, *shape[-2:])):
-        ref, tol = ortho_bound(one, steps, coefficients)
+        ref, tol = ortho_bound(one, steps, coefficients, t)
         fits(got, ref, torch.tensor(tol), t, "out")
     once = plan.out.clone()
     rsx.newton_schulz(d, d, steps=steps, coefficients=coefficients)  # in place
