@@ -11,8 +11,10 @@
 // transposed in memory.
 //
 // What is rounded: s (and dg, du) to the matrices' type, as the next product's
-// operand, and g and u to the type of x where they are kept for the gradient.
-// In fp32 all three are kept whole, as three bf16 parts.
+// operand; in fp32 they are kept whole, as three bf16 parts.  g and u stay fp32 for
+// the gradient: rounded to bf16 as well, they leave the weights' gradients off by
+// 3.5e-3 (rms) where one rounding of an operand and one of the result leave 2.4e-3;
+// their way through memory costs 3% more time (8192 x 4096 x 11008).
 #include "few_rows.h"
 #include "product_store.h"
 
@@ -71,9 +73,9 @@ __device__ __forceinline__ Slope<N> activation(int act, typename Vec<float, N>::
 struct GateArgs {
   Parts s;
   float* s32;  // the few-row form in fp32 keeps s as it is, rows of p.rows
-  void* gate;  // null: not kept
-  void* up;
-  int act, type;
+  float* gate;  // null: not kept
+  float* up;
+  int act;
 };
 
 struct Gate {
@@ -82,8 +84,8 @@ struct Gate {
   static __device__ __forceinline__ void one(const GateArgs& e, uint64_t m, uint32_t c, uint32_t n, typename Vec<float, N>::type g,
                                              typename Vec<float, N>::type u) {
     if (e.gate) {
-      put_as<N>(e.type, e.gate, m * n, c, n, g);
-      put_as<N>(e.type, e.up, m * n, c, n, u);
+      put<float, N>(e.gate + m * n, c, n, g);
+      put<float, N>(e.up + m * n, c, n, u);
     }
     auto s = activation<false, N>(e.act, g).value;
 #pragma unroll
@@ -107,10 +109,10 @@ struct Gate {
 };
 
 struct GateGradArgs {
-  const void* gate;
-  const void* up;
+  const float* gate;
+  const float* up;
   Parts s, dg, du;  // count 0: not wanted
-  int act, type;
+  int act;
 };
 
 struct GateGrad {
@@ -121,7 +123,7 @@ struct GateGrad {
     staged<TILE, false, N>(w, acc, i0, lds, [&](uint32_t m, uint32_t c, f32x8 ds) {
       if (m >= p.m || c >= ((p.n + 7) & ~7u)) return;
       const uint64_t row = static_cast<uint64_t>(m) * p.n;
-      const f32x8 g = get_as<8>(e.type, e.gate, row, c, p.n), u = get_as<8>(e.type, e.up, row, c, p.n);
+      const f32x8 g = get<float, 8>(e.gate + row, c, p.n), u = get<float, 8>(e.up + row, c, p.n);
       const Slope<8> a = activation<true, 8>(e.act, g);
       f32x8 s, dg, du;
 #pragma unroll
@@ -168,7 +170,7 @@ ProductArgs sizes(uint64_t m, uint64_t n, uint64_t k) {
 
 template <class T>
 hipError_t few(const FeedForwardArgs& a, void* s, hipStream_t stream) {
-  GateArgs e = {{{s, nullptr, nullptr}, copy_ld(a.hidden), 1}, static_cast<float*>(s), a.gate, a.up, a.act, a.type};
+  GateArgs e = {{{s, nullptr, nullptr}, copy_ld(a.hidden), 1}, static_cast<float*>(s), a.gate, a.up, a.act};
   FewArgs p = {a.x.p, a.w_gate.p, a.w_up.p, a.x.ld, a.w_gate.ld, a.w_up.ld, static_cast<uint32_t>(a.rows),
                static_cast<uint32_t>(a.hidden), static_cast<uint32_t>(a.dim)};
   if (a.hidden) RSX_TRY((launch_few<T, 1, true, Gate>(p, e, stream)));
@@ -192,7 +194,7 @@ Forward plan(const FeedForwardArgs& a, Arena& ws) {
   f.wu = take_operand(ws, a.w_up, a.type, n, half, a.copies);
   f.wd = take_operand(ws, a.w_down, a.type, n, half, a.copies);
   f.s = take_parts(ws, a.rows, a.hidden, n);
-  const uint64_t segs = n * (n + 1) / 2, split = store_ws(a.rows, a.dim, a.hidden, segs);
+  const uint64_t segs = segments_of(n, n), split = store_ws(a.rows, a.dim, a.hidden, segs);
   f.gate = schedule(a.rows, 2 * a.hidden, 1, steps_of(a.dim, segs), false, false);
   f.split = ws.take(split > f.gate.bytes ? split : f.gate.bytes);
   return f;
@@ -220,7 +222,7 @@ Backward plan(const FeedForwardGradArgs& a, Arena& ws) {
   }
   b.dg = take_parts(ws, a.rows, a.hidden, n);
   b.du = take_parts(ws, a.rows, a.hidden, n);
-  const uint64_t segs = n * (n + 1) / 2;
+  const uint64_t segs = segments_of(n, n);
   b.gate = schedule(a.rows, a.hidden, 1, steps_of(a.dim, segs), false, false);
   uint64_t split = b.gate.bytes;
   if (a.dx) {
@@ -257,12 +259,12 @@ hipError_t launch_feed_forward(const FeedForwardArgs& a, hipStream_t s) {
   RSX_TRY(fill_operand(f.wu, a.w_up, a.type, half, s));
   RSX_TRY(fill_operand(f.wd, a.w_down, a.type, half, s));
   ProductArgs p = sizes(a.rows, a.hidden, a.dim);
-  add_segments(p, f.x.op, f.wg.op, n, &f.wu.op);
-  const GateArgs e = {f.s, nullptr, a.gate, a.up, a.act, a.type};
+  add_segments(p, f.x.op, n, f.wg.op, n, &f.wu.op);
+  const GateArgs e = {f.s, nullptr, a.gate, a.up, a.act};
   RSX_TRY((half ? launch_product<f16_t, kRow, kRow, true, false, Gate>(p, f.gate, f.split, e, s)
                 : launch_product<bf16_t, kRow, kRow, true, false, Gate>(p, f.gate, f.split, e, s)));
   p = sizes(a.rows, a.dim, a.hidden);
-  add_segments(p, operand(f.s), f.wd.op, n);
+  add_segments(p, operand(f.s), n, f.wd.op, n);
   return launch_store(half, kNT, p, {a.out, a.out_ld, a.type, nullptr, 0}, f.split, s);
 }
 
@@ -285,25 +287,25 @@ hipError_t launch_feed_forward_grad(const FeedForwardGradArgs& a, hipStream_t s)
     RSX_TRY(fill_operand(b.wu, a.w_up, a.type, half, s));
   }
   ProductArgs p = sizes(a.rows, a.hidden, a.dim);
-  add_segments(p, b.dout.op, b.wd.op, n);
-  const GateGradArgs e = {a.gate, a.up, b.s, b.dg, b.du, a.act, a.type};
+  add_segments(p, b.dout.op, n, b.wd.op, n);
+  const GateGradArgs e = {a.gate, a.up, b.s, b.dg, b.du, a.act};
   RSX_TRY((half ? launch_product<f16_t, kRow, kCol, false, false, GateGrad>(p, b.gate, b.split, e, s)
                 : launch_product<bf16_t, kRow, kCol, false, false, GateGrad>(p, b.gate, b.split, e, s)));
   if (a.dx) {
     p = sizes(a.rows, a.dim, a.hidden);
-    add_segments(p, operand(b.dg), b.wg.op, n);
-    add_segments(p, operand(b.du), b.wu.op, n);
+    add_segments(p, operand(b.dg), n, b.wg.op, n);
+    add_segments(p, operand(b.du), n, b.wu.op, n);
     RSX_TRY(launch_store(half, kNN, p, {a.dx, a.dx_ld, a.type, nullptr, 0}, b.split, s));
   }
   if (!a.dw_gate) return hipSuccess;
   p = sizes(a.hidden, a.dim, a.rows);
-  add_segments(p, operand(b.dg), b.x.op, n);
+  add_segments(p, operand(b.dg), n, b.x.op, n);
   RSX_TRY(launch_store(half, kTN, p, {a.dw_gate, a.dw_gate_ld, a.weight_type, nullptr, a.accumulate}, b.split, s));
   p = sizes(a.hidden, a.dim, a.rows);
-  add_segments(p, operand(b.du), b.x.op, n);
+  add_segments(p, operand(b.du), n, b.x.op, n);
   RSX_TRY(launch_store(half, kTN, p, {a.dw_up, a.dw_up_ld, a.weight_type, nullptr, a.accumulate}, b.split, s));
   p = sizes(a.dim, a.hidden, a.rows);
-  add_segments(p, b.dout.op, operand(b.s), n);
+  add_segments(p, b.dout.op, n, operand(b.s), n);
   return launch_store(half, kTN, p, {a.dw_down, a.dw_down_ld, a.weight_type, nullptr, a.accumulate}, b.split, s);
 }
 

@@ -12,10 +12,13 @@
 // and dh += dz W.  That is 4/3 of the operations of keeping all logits, and
 // memory for one piece.
 //
-// What is rounded: dz, as an operand, to bf16 (half a step of 2^-9 of each, with
-// errors that add up as those of the hidden states do).  With fp16 matrices dz
-// is two bf16 parts, and so are the matrices: probabilities of large
-// vocabularies lie below fp16's range.  With fp32 all is three.
+// What is rounded: dz, as an operand, to bf16, which leaves the gradients off by
+// 2.4e-3 (rms) where their own rounding leaves 1.7e-3.  Most of a row's dz is its
+// token's, so that in a few rows a few roundings say how far the gradients are off
+// as a whole: up to 256 rows, where the products wait for the matrix's way through
+// memory, dz is two bf16 parts.  With fp16 matrices it is always, and so are the
+// matrices: probabilities of large vocabularies lie below fp16's range.  With
+// fp32 all is three.
 #include "few_rows.h"
 #include "product_store.h"
 
@@ -261,7 +264,7 @@ Forward plan(const LinearLogprobArgs& a, Arena& ws) {
   const int n = a.type == RSX_FLOAT32 ? 3 : 1;
   const bool half = a.type == RSX_FLOAT16;
   f.few = a.rows <= kFewRows;
-  f.spread = schedule(a.rows, a.vocab, 1, steps_of(a.dim, n * (n + 1) / 2), false, false);
+  f.spread = schedule(a.rows, a.vocab, 1, steps_of(a.dim, segments_of(n, n)), false, false);
   const uint64_t width = f.few ? 16 * kFewGroups : f.spread.tile == 0 ? Large::BN : Middle::BN;
   f.tiles = static_cast<uint32_t>((a.vocab + width - 1) / width);
   if (!f.few) {
@@ -286,6 +289,7 @@ struct Backward {
   Prepared hidden, weight;    // of the logits' product
   Prepared hidden2, weight2;  // of the gradients' products
   Parts dz;
+  int parts, parts_dz;  // of the matrices in the gradients' products, and of dz
   float* sum;  // dhidden so far
   void* split;
   uint64_t piece;
@@ -294,6 +298,8 @@ Backward plan(const LinearLogprobGradArgs& a, Arena& ws) {
   Backward b = {};
   const bool half = a.type == RSX_FLOAT16;
   const int n = a.type == RSX_FLOAT32 ? 3 : 1, n2 = half ? 2 : n;
+  b.parts = n2;
+  b.parts_dz = a.type == RSX_FLOAT32 ? 3 : half || a.rows <= 256 ? 2 : 1;
   b.hidden = take_operand(ws, a.hidden, a.type, n, half, a.copies);
   b.weight = take_operand(ws, a.weight, a.type, n, half, a.copies);
   b.hidden2 = b.hidden;
@@ -303,15 +309,15 @@ Backward plan(const LinearLogprobGradArgs& a, Arena& ws) {
     if (a.dhidden) b.weight2 = take_operand(ws, a.weight, a.type, n2, false, a.copies);
   }
   b.piece = piece(a.rows, a.vocab);
-  b.dz = take_parts(ws, a.rows, b.piece, n2);
+  b.dz = take_parts(ws, a.rows, b.piece, b.parts_dz);
   if (a.dhidden && b.piece < a.vocab) b.sum = static_cast<float*>(ws.take(a.rows * a.dim * 4));
-  const uint64_t segs = n2 * (n2 + 1) / 2;
+  const uint64_t segs = segments_of(b.parts_dz, n2);
   uint64_t split = 0;
   const uint64_t last = b.piece ? a.vocab % b.piece : 0;  // the last piece is cut in its own way
   for (const uint64_t v : {b.piece, last}) {
     if (v == 0) continue;
     const uint64_t h = a.dhidden ? store_ws(a.rows, a.dim, v, segs) : 0, w = a.dweight ? store_ws(v, a.dim, a.rows, segs) : 0;
-    const uint64_t z = schedule(a.rows, v, 1, steps_of(a.dim, n * (n + 1) / 2), false, false).bytes;
+    const uint64_t z = schedule(a.rows, v, 1, steps_of(a.dim, segments_of(n, n)), false, false).bytes;
     split = split < h ? h : split;
     split = split < w ? w : split;
     split = split < z ? z : split;
@@ -343,7 +349,8 @@ hipError_t launch_linear_logprobs(const LinearLogprobArgs& a, hipStream_t s) {
     RSX_TRY(fill_operand(f.hidden, a.hidden, a.type, half, s));
     RSX_TRY(fill_operand(f.weight, a.weight, a.type, half, s));
     ProductArgs p = sizes(a.rows, a.vocab, a.dim);
-    add_segments(p, f.hidden.op, f.weight.op, a.type == RSX_FLOAT32 ? 3 : 1);
+    const int n = a.type == RSX_FLOAT32 ? 3 : 1;
+    add_segments(p, f.hidden.op, n, f.weight.op, n);
     RSX_TRY((half ? launch_product<f16_t, kRow, kRow, false, false, Softmax>(p, f.spread, f.pieces, e, s)
                   : launch_product<bf16_t, kRow, kRow, false, false, Softmax>(p, f.spread, f.pieces, e, s)));
   }
@@ -360,7 +367,7 @@ uint64_t linear_logprobs_grad_ws(const LinearLogprobGradArgs& a) {
 
 hipError_t launch_linear_logprobs_grad(const LinearLogprobGradArgs& a, hipStream_t s) {
   const bool half = a.type == RSX_FLOAT16;
-  const int n = a.type == RSX_FLOAT32 ? 3 : 1, n2 = half ? 2 : n;
+  const int n = a.type == RSX_FLOAT32 ? 3 : 1;
   Arena ws(a.ws);
   const Backward b = plan(a, ws);
   RSX_TRY(fill_operand(b.hidden, a.hidden, a.type, half, s));
@@ -379,7 +386,7 @@ hipError_t launch_linear_logprobs_grad(const LinearLogprobGradArgs& a, hipStream
     };
     if (a.rows) {
       ProductArgs p = sizes(a.rows, v, a.dim);
-      add_segments(p, b.hidden.op, rows_from(b.weight.op), n);
+      add_segments(p, b.hidden.op, n, rows_from(b.weight.op), n);
       const DzArgs e = {a.tokens, a.lse, a.lse_rest, a.entropy, a.dlogprob, a.dentropy, b.dz, first, a.vocab, a.scale, a.wide};
       const Schedule c = schedule(a.rows, v, 1, steps_of(a.dim, p.nseg), false, false);
       RSX_TRY((half ? launch_product<f16_t, kRow, kRow, false, false, Dz>(p, c, b.split, e, s)
@@ -387,13 +394,13 @@ hipError_t launch_linear_logprobs_grad(const LinearLogprobGradArgs& a, hipStream
     }
     if (a.dweight) {
       ProductArgs p = sizes(v, a.dim, a.rows);
-      add_segments(p, operand(b.dz), b.hidden2.op, n2);
+      add_segments(p, operand(b.dz), b.parts_dz, b.hidden2.op, b.parts);
       void* to = static_cast<char*>(a.dweight) + first * a.dweight_ld * es;
       RSX_TRY(launch_store(false, kTN, p, {to, a.dweight_ld, a.weight_type, nullptr, a.accumulate}, b.split, s));
     }
     if (a.dhidden) {
       ProductArgs p = sizes(a.rows, a.dim, v);
-      add_segments(p, operand(b.dz), rows_from(b.weight2.op), n2);
+      add_segments(p, operand(b.dz), b.parts_dz, rows_from(b.weight2.op), b.parts);
       const bool last = first + v == a.vocab;
       const float* add = first ? b.sum : nullptr;
       const StoreArgs e = last ? StoreArgs{a.dhidden, a.dhidden_ld, a.type, add, 0}

@@ -217,7 +217,7 @@ struct Spread {
   }
 };
 Spread spread(uint64_t batch, uint64_t n, uint64_t wide, int parts) {
-  const uint64_t segs = static_cast<uint64_t>(parts) * (parts + 1) / 2;
+  const uint64_t segs = segments_of(parts, parts);
   return {schedule(n, n, batch, steps_of(wide, segs), true, true), schedule(n, n, batch, steps_of(n, segs), true, true),
           schedule(n, wide, batch, steps_of(n, segs), false, true)};
 }
@@ -242,7 +242,7 @@ Space plan(Arena& ws, uint64_t batch, uint64_t n, uint64_t wide) {
 template <int LB, bool TRIANGLE, class EPILOGUE>
 hipError_t multiply(ProductArgs p, const Stack& a, const Stack& b, int parts, const Schedule& c, void* pieces,
                     const typename EPILOGUE::Args& e, hipStream_t s) {
-  add_segments(p, operand(a.p), operand(b.p), parts);
+  add_segments(p, operand(a.p), parts, operand(b.p), parts);
   p.batch_a = a.each;
   p.batch_b = b.each;
   return c.tile == 2 ? launch_tiles<f16_t, Small, kRow, LB, false, TRIANGLE, EPILOGUE>(p, c, pieces, e, s)

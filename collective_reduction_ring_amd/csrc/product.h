@@ -615,12 +615,19 @@ struct Operand {
   uint64_t ld;
 };
 
-// Products of the parts i of A and j of B with i + j < count, the smallest
-// first: what is left out is below the last part's own rounding.
-inline void add_segments(ProductArgs& p, const Operand& a, const Operand& b, int count, const Operand* b2 = nullptr) {
-  for (int sum = count - 1; sum >= 0; --sum)
+// Products of the parts i of A and j of B, the smallest first.  What is left out,
+// i + j from the larger count on, is below the last part's own rounding.
+inline void add_segments(ProductArgs& p, const Operand& a, int parts_a, const Operand& b, int parts_b, const Operand* b2 = nullptr) {
+  for (int sum = (parts_a > parts_b ? parts_a : parts_b) - 1; sum >= 0; --sum)
     for (int i = sum; i >= 0; --i)
-      p.seg[p.nseg++] = {a.part[i], b.part[sum - i], b2 ? b2->part[sum - i] : nullptr, a.ld, b.ld, b2 ? b2->ld : 0};
+      if (i < parts_a && sum - i < parts_b)
+        p.seg[p.nseg++] = {a.part[i], b.part[sum - i], b2 ? b2->part[sum - i] : nullptr, a.ld, b.ld, b2 ? b2->ld : 0};
+}
+// How many.
+inline uint64_t segments_of(int parts_a, int parts_b) {
+  ProductArgs p = {};
+  add_segments(p, {}, parts_a, {}, parts_b);
+  return p.nseg;
 }
 
 // How a product m x n of `steps` steps is spread over the CUs: the tile, and how

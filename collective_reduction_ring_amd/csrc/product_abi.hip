@@ -36,7 +36,7 @@ size_t rsx_feed_forward_workspace_size(size_t rows, size_t dim, size_t hidden, r
 
 rsx_status_t rsx_feed_forward(const void* x, size_t x_stride, const void* w_gate, size_t gate_stride,
                               const void* w_up, size_t up_stride, const void* w_down,
-                              size_t down_stride, void* out, size_t out_stride, void* gate, void* up,
+                              size_t down_stride, void* out, size_t out_stride, float* gate, float* up,
                               size_t rows, size_t dim, size_t hidden, rsx_activation_t activation,
                               rsx_dtype_t type, void* workspace, size_t workspace_bytes,
                               hipStream_t stream) {
@@ -53,8 +53,8 @@ rsx_status_t rsx_feed_forward(const void* x, size_t x_stride, const void* w_gate
   m.read(w_up, hidden, dim, up_stride, es);
   m.read(w_down, dim, hidden, down_stride, es);
   if (gate != nullptr) {
-    m.write(gate, rows, hidden, hidden, es);
-    m.write(up, rows, hidden, hidden, es);
+    m.write(gate, rows, hidden, hidden, 4);
+    m.write(up, rows, hidden, hidden, 4);
   }
   const Matrix mx = {x, rows, dim, x_stride}, mg = {w_gate, hidden, dim, gate_stride}, mu = {w_up, hidden, dim, up_stride},
                md = {w_down, dim, hidden, down_stride};
@@ -77,7 +77,7 @@ size_t rsx_feed_forward_grad_workspace_size(size_t rows, size_t dim, size_t hidd
 rsx_status_t rsx_feed_forward_grad(const void* dout, size_t dout_stride, const void* x, size_t x_stride,
                                    const void* w_gate, size_t gate_stride, const void* w_up,
                                    size_t up_stride, const void* w_down, size_t down_stride,
-                                   const void* gate, const void* up, void* dx, size_t dx_stride,
+                                   const float* gate, const float* up, void* dx, size_t dx_stride,
                                    void* dw_gate, size_t dw_gate_stride, void* dw_up,
                                    size_t dw_up_stride, void* dw_down, size_t dw_down_stride,
                                    size_t rows, size_t dim, size_t hidden,
@@ -97,8 +97,8 @@ rsx_status_t rsx_feed_forward_grad(const void* dout, size_t dout_stride, const v
   m.read(w_gate, hidden, dim, gate_stride, es);
   m.read(w_up, hidden, dim, up_stride, es);
   m.read(w_down, dim, hidden, down_stride, es);
-  m.read(gate, rows, hidden, hidden, es);
-  m.read(up, rows, hidden, hidden, es);
+  m.read(gate, rows, hidden, hidden, 4);
+  m.read(up, rows, hidden, hidden, 4);
   if (dx != nullptr) m.write(dx, rows, dim, dx_stride, es);
   if (dw_gate != nullptr) {
     m.write(dw_gate, hidden, dim, dw_gate_stride, gs);

@@ -42,8 +42,8 @@ struct FeedForwardArgs {
   Matrix x, w_gate, w_up, w_down;
   void* out;
   uint64_t out_ld;
-  void* gate;  // kept for the gradient; null: not kept
-  void* up;
+  float* gate;  // kept for the gradient; null: not kept
+  float* up;
   uint64_t rows, dim, hidden;
   int act, type;
   bool copies;  // some matrix cannot be read in place
@@ -54,8 +54,8 @@ hipError_t launch_feed_forward(const FeedForwardArgs& a, hipStream_t s);
 
 struct FeedForwardGradArgs {
   Matrix dout, x, w_gate, w_up, w_down;
-  const void* gate;
-  const void* up;
+  const float* gate;
+  const float* up;
   void* dx;  // null: no gradient of x
   void* dw_gate;  // null: none of the weights
   void* dw_up;

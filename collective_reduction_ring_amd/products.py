@@ -70,8 +70,8 @@ class FeedForward(_Plan):
     """Prepared gated feed-forward block: ``out = (act(x @ w_gate.T) * (x @ w_up.T))
     @ w_down.T``, with ``w_gate`` and ``w_up`` of (hidden, dim), ``w_down`` of (dim,
     hidden), all of x's type, and ``activation`` "silu", "gelu", "gelu_tanh" or
-    "relu".  With ``keep`` the two projections stay in ``gate`` and ``up`` for the
-    gradient."""
+    "relu".  With ``keep`` the two projections stay in ``gate`` and ``up`` (float32)
+    for the gradient."""
 
     def __init__(self, x, w_gate, w_up, w_down, out=None, activation: str = "silu", keep: bool = False):
         rows, dim, hidden, xt, (xs, gs, us, ds) = _block(x, w_gate, w_up, w_down)
@@ -81,7 +81,7 @@ class FeedForward(_Plan):
         os_ = _rows(out, "out", device=x.device, shape=x.shape, dtype=x.dtype, output=True)[2]
         self.out, self.gate, self.up = out, None, None
         if keep:
-            self.gate, self.up = (torch.empty((*x.shape[:-1], hidden), dtype=x.dtype, device=x.device) for _ in range(2))
+            self.gate, self.up = (torch.empty((*x.shape[:-1], hidden), dtype=torch.float32, device=x.device) for _ in range(2))
         copies = _copies((x, rows, dim, xs), (w_gate, hidden, dim, gs), (w_up, hidden, dim, us), (w_down, dim, hidden, ds))
         ws, wb, self._ws = self._workspace(L.lib().rsx_feed_forward_workspace_size(rows, dim, hidden, xt, copies), x.device)
         # Tensors without elements have no address, and the library takes no half of a pair.
@@ -103,8 +103,8 @@ class FeedForwardGrad(_Plan):
         rows, dim, hidden, xt, (xs, gs, us, ds) = _block(x, w_gate, w_up, w_down)
         dev, act = x.device, _activation(activation)
         ys = _rows(dout, "dout", device=dev, shape=x.shape, dtype=x.dtype)[2]
-        _vector(gate, "gate", rows * hidden, x.dtype, dev)
-        _vector(up, "up", rows * hidden, x.dtype, dev)
+        _vector(gate, "gate", rows * hidden, torch.float32, dev)
+        _vector(up, "up", rows * hidden, torch.float32, dev)
         given = [t is not None for t in (dw_gate, dw_up, dw_down)]
         if accumulate and weights and not all(given):
             raise ValueError("accumulate needs dw_gate, dw_up and dw_down")

@@ -558,8 +558,7 @@ typedef enum {
  * Gated feed-forward block: with g = x w_gate^T and u = x w_up^T,
  * out = (act(g) * u) w_down^T.
  * x, out: [rows][dim]; w_gate, w_up: [hidden][dim]; w_down: [dim][hidden].
- * gate, up: [rows][hidden] of `type`, dense: g and u for the gradient; or both
- * null.  act(g) * u is rounded to `type` (fp32: kept whole) between the products.
+ * gate, up: [rows][hidden] fp32, dense: g and u for the gradient; or both null.  act(g) * u is rounded to `type` (fp32: kept whole) between the products.
  * out overlaps nothing that is read.
  */
 size_t rsx_feed_forward_workspace_size(size_t rows, size_t dim, size_t hidden, rsx_dtype_t type,
@@ -567,7 +566,7 @@ size_t rsx_feed_forward_workspace_size(size_t rows, size_t dim, size_t hidden, r
 rsx_status_t rsx_feed_forward(const void* x, size_t x_stride, const void* w_gate,
                               size_t gate_stride, const void* w_up, size_t up_stride,
                               const void* w_down, size_t down_stride, void* out, size_t out_stride,
-                              void* gate, void* up, size_t rows, size_t dim, size_t hidden,
+                              float* gate, float* up, size_t rows, size_t dim, size_t hidden,
                               rsx_activation_t activation, rsx_dtype_t type, void* workspace,
                               size_t workspace_bytes, hipStream_t stream);
 
@@ -585,7 +584,7 @@ size_t rsx_feed_forward_grad_workspace_size(size_t rows, size_t dim, size_t hidd
 rsx_status_t rsx_feed_forward_grad(const void* dout, size_t dout_stride, const void* x,
                                    size_t x_stride, const void* w_gate, size_t gate_stride,
                                    const void* w_up, size_t up_stride, const void* w_down,
-                                   size_t down_stride, const void* gate, const void* up, void* dx,
+                                   size_t down_stride, const float* gate, const float* up, void* dx,
                                    size_t dx_stride, void* dw_gate, size_t dw_gate_stride,
                                    void* dw_up, size_t dw_up_stride, void* dw_down,
                                    size_t dw_down_stride, size_t rows, size_t dim, size_t hidden,
@@ -613,8 +612,8 @@ rsx_status_t rsx_linear_logprobs(const void* hidden, size_t hidden_stride, const
  * dweight = dz^T hidden (with `accumulate` added to what is there).  Either may
  * be null.  dweight is of dweight_type: `type` or RSX_FLOAT32.
  * The vocabulary is taken in pieces, of which the logits are multiplied again.
- * dz is rounded to bf16 (fp16 matrices: to 16 bits, with the range of fp32;
- * fp32: kept whole).
+ * dz is rounded to bf16 (fp16 matrices and up to 256 rows: to 16 bits, with the
+ * range of fp32; fp32: kept whole).
  */
 size_t rsx_linear_logprobs_grad_workspace_size(size_t rows, size_t vocab, size_t dim,
                                                rsx_dtype_t type, int copies);

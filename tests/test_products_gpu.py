@@ -63,8 +63,8 @@ def test_feed_forward(rows, dim, hidden, t, act, pad, keep):
     assert same_bits(once, out)
     if not keep:
         return
-    fits(plan.gate, ref[1], tol[1], t, "gate")
-    fits(plan.up, ref[2], tol[2], t, "up")
+    fits(plan.gate, ref[1], tol[1], F32, "gate")
+    fits(plan.up, ref[2], tol[2], F32, "up")
     dy = rand(g, rows, dim, dtype=t)
     wtype = F32 if rows % 2 else t
     dx_big, dx = wide_rows(torch.zeros(rows, dim, dtype=t), pad)
