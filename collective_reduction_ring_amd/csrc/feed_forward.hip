@@ -176,7 +176,7 @@ hipError_t few(const FeedForwardArgs& a, void* s, hipStream_t stream) {
   if (a.hidden) RSX_TRY((launch_few<T, 1, true, Gate>(p, e, stream)));
   p = {s, a.w_down.p, nullptr, sizeof(T) == 4 ? a.hidden : copy_ld(a.hidden), a.w_down.ld, 0, static_cast<uint32_t>(a.rows),
        static_cast<uint32_t>(a.dim), static_cast<uint32_t>(a.hidden)};
-  return launch_few<T, 1, false, FewStore>(p, {a.out, a.out_ld, a.type, nullptr, 0}, stream);
+  return launch_few<T, 1, false, FewStore>(p, {a.out, a.out_ld, a.type, nullptr, nullptr, 0}, stream);
 }
 
 struct Forward {
@@ -265,7 +265,7 @@ hipError_t launch_feed_forward(const FeedForwardArgs& a, hipStream_t s) {
                 : launch_product<bf16_t, kRow, kRow, true, false, Gate>(p, f.gate, f.split, e, s)));
   p = sizes(a.rows, a.dim, a.hidden);
   add_segments(p, operand(f.s), n, f.wd.op, n);
-  return launch_store(half, kNT, p, {a.out, a.out_ld, a.type, nullptr, 0}, f.split, s);
+  return launch_store(half, kNT, p, {a.out, a.out_ld, a.type, nullptr, nullptr, 0}, f.split, s);
 }
 
 uint64_t feed_forward_grad_ws(const FeedForwardGradArgs& a) {
@@ -295,18 +295,18 @@ hipError_t launch_feed_forward_grad(const FeedForwardGradArgs& a, hipStream_t s)
     p = sizes(a.rows, a.dim, a.hidden);
     add_segments(p, operand(b.dg), n, b.wg.op, n);
     add_segments(p, operand(b.du), n, b.wu.op, n);
-    RSX_TRY(launch_store(half, kNN, p, {a.dx, a.dx_ld, a.type, nullptr, 0}, b.split, s));
+    RSX_TRY(launch_store(half, kNN, p, {a.dx, a.dx_ld, a.type, nullptr, nullptr, 0}, b.split, s));
   }
   if (!a.dw_gate) return hipSuccess;
   p = sizes(a.hidden, a.dim, a.rows);
   add_segments(p, operand(b.dg), n, b.x.op, n);
-  RSX_TRY(launch_store(half, kTN, p, {a.dw_gate, a.dw_gate_ld, a.weight_type, nullptr, a.accumulate}, b.split, s));
+  RSX_TRY(launch_store(half, kTN, p, {a.dw_gate, a.dw_gate_ld, a.weight_type, nullptr, nullptr, a.accumulate}, b.split, s));
   p = sizes(a.hidden, a.dim, a.rows);
   add_segments(p, operand(b.du), n, b.x.op, n);
-  RSX_TRY(launch_store(half, kTN, p, {a.dw_up, a.dw_up_ld, a.weight_type, nullptr, a.accumulate}, b.split, s));
+  RSX_TRY(launch_store(half, kTN, p, {a.dw_up, a.dw_up_ld, a.weight_type, nullptr, nullptr, a.accumulate}, b.split, s));
   p = sizes(a.dim, a.hidden, a.rows);
   add_segments(p, b.dout.op, n, operand(b.s), n);
-  return launch_store(half, kTN, p, {a.dw_down, a.dw_down_ld, a.weight_type, nullptr, a.accumulate}, b.split, s);
+  return launch_store(half, kTN, p, {a.dw_down, a.dw_down_ld, a.weight_type, nullptr, nullptr, a.accumulate}, b.split, s);
 }
 
 }  // namespace rsx

@@ -12,13 +12,14 @@
 // and dh += dz W.  That is 4/3 of the operations of keeping all logits, and
 // memory for one piece.
 //
-// What is rounded: dz, as an operand, to bf16, which leaves the gradients off by
-// 2.4e-3 (rms) where their own rounding leaves 1.7e-3.  Most of a row's dz is its
-// token's, so that in a few rows a few roundings say how far the gradients are off
-// as a whole: up to 256 rows, where the products wait for the matrix's way through
-// memory, dz is two bf16 parts.  With fp16 matrices it is always, and so are the
-// matrices: probabilities of large vocabularies lie below fp16's range.  With
-// fp32 all is three.
+// What is rounded: dz, as an operand, to bf16; with fp16 matrices it is two bf16
+// parts, and so are the matrices, since probabilities of large vocabularies lie
+// below fp16's range; with fp32 all is three.  Most of a row's dz is its token's.
+// Each row is divided by about that before it is rounded, dz = c dz', so that the
+// token's is 1 and keeps all its digits: dhidden = c (dz' W) is as good as
+// its own rounding, and dW = dz'^T (c h) has the rounding of c h, one by one.
+// Rounded as it is, a row's dz would be off by one error in all its elements, and
+// where all rows have one weight, all rows by the same.
 #include "few_rows.h"
 #include "product_store.h"
 
@@ -194,17 +195,80 @@ __global__ __launch_bounds__(256) void join_tiles(const JoinArgs a) {
   if (a.entropy) a.entropy[row] = none ? 0.0f : ln - s.gap / s.sum;
 }
 
-struct DzArgs {
+// What a row of dz is made of, but for its logits.
+struct RowArgs {
   const void* tokens;
   const float* lse;
   const float* lse_rest;
   const float* entropy;
   const float* dlogprob;
   const float* dentropy;
-  Parts dz;
-  uint64_t first, vocab;  // the piece's first row of the matrix; all rows
+  uint64_t vocab;
   float scale;
   int wide;
+};
+struct Row {
+  int64_t token;  // -1: none in the vocabulary
+  float lse, rest, g, d, h;
+  __device__ __forceinline__ Row(const RowArgs& e, uint32_t i) {
+    token = token_at(e.tokens, e.wide, i);
+    if (token < 0 || static_cast<uint64_t>(token) >= e.vocab) token = -1;
+    lse = e.lse[i];
+    rest = e.lse_rest ? e.lse_rest[i] : 0.0f;
+    g = token >= 0 ? e.dlogprob[i] : 0.0f;
+    d = e.dentropy ? e.dentropy[i] : 0.0f;
+    h = e.dentropy ? e.entropy[i] : 0.0f;
+  }
+  // The gradient in logit z.
+  __device__ __forceinline__ float dz(float z, bool hit) const {
+    const float lp = (z - lse) - rest, p = __builtin_amdgcn_exp2f(lp * kLog2e), own = hit ? g : 0.0f;
+    if (lse == -INFINITY) return 0.0f;
+    return p == 0.0f ? own : own - p * (g + d * (lp + h));
+  }
+};
+
+// Each row's factor c, and c h in parts: a workgroup a row.  c is scale times the
+// token's dz, or what bounds dz where that is small beside it or not there.
+template <class S>
+__global__ __launch_bounds__(256) void scale_rows(const S* hidden, uint64_t ld, const S* weight, uint64_t wld, uint32_t rows, uint32_t dim,
+                                                  RowArgs e, float* factor, Parts to) {
+  const uint64_t i = block_id();
+  if (i >= rows) return;
+  __shared__ float part[4];
+  const Row row(e, static_cast<uint32_t>(i));
+  const S* h = hidden + i * ld;
+  float sum = 0.0f;
+  if (row.token >= 0) {
+    const S* w = weight + row.token * wld;
+    for (uint64_t c = threadIdx.x * 8; c < dim; c += 2048) {
+      const auto a = load_row<S, 8, false>(h, static_cast<uint32_t>(c), dim), b = load_row<S, 8, false>(w, static_cast<uint32_t>(c), dim);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) sum = fmaf(static_cast<float>(a[x]), static_cast<float>(b[x]), sum);
+    }
+  }
+  sum = wave_sum(sum);
+  if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = sum;
+  __syncthreads();
+  const float most = fabsf(row.g) + fabsf(row.d);
+  float c = row.token >= 0 ? row.dz(((part[0] + part[1]) + (part[2] + part[3])) * e.scale, true) : most;
+  // (not of a NaN, which is to show)
+  if (fabsf(c) < most * (row.d == 0.0f ? 0x1p-20f : 0x1p-3f)) c = most;
+  c = row.lse == -INFINITY ? 0.0f : c * e.scale;
+  if (c != 0.0f && fabsf(c) < 1e-30f) c = 1e-30f;  // so that 1 / c and the parts of c h are in range
+  if (threadIdx.x == 0) factor[i] = c;
+  if (to.count == 0) return;
+  for (uint64_t x = threadIdx.x * 8; x < dim; x += 2048) {
+    f32x8 v = __builtin_convertvector((load_row<S, 8, false>(h, static_cast<uint32_t>(x), dim)), f32x8) * c;
+    if (c == 0.0f) v = f32x8{};  // whatever h is
+    put_parts<bf16_t, 8>(to, i, static_cast<uint32_t>(x), dim, v);
+  }
+}
+
+struct DzArgs {
+  RowArgs row;
+  const float* factor;
+  Parts dz;
+  uint64_t first;  // the piece's first row of the matrix
 };
 
 struct Dz {
@@ -212,23 +276,14 @@ struct Dz {
   template <class T, class TILE, int N>
   static __device__ __forceinline__ void run(const ProductArgs& p, const Where& w, const DzArgs& e,
                                              const f32x4 (&acc)[TILE::TN][N], uint32_t i0, RSX_LDS char* lds) {
-    staged<TILE, false, N>(w, acc, i0, lds, [&](uint32_t row, uint32_t c, f32x8 v) {
-      if (row >= p.m) return;
-      const int64_t token = token_at(e.tokens, e.wide, row);
-      const bool there = token >= 0 && static_cast<uint64_t>(token) < e.vocab;
-      const uint64_t hit = there ? static_cast<uint64_t>(token) - e.first : ~0ull;
-      const float lse = e.lse[row], rest = e.lse_rest ? e.lse_rest[row] : 0.0f;
-      const float g = there ? e.dlogprob[row] : 0.0f;
-      const float d = e.dentropy ? e.dentropy[row] : 0.0f, h = e.dentropy ? e.entropy[row] : 0.0f;
-      const bool none = lse == -INFINITY;
+    staged<TILE, false, N>(w, acc, i0, lds, [&](uint32_t i, uint32_t c, f32x8 v) {
+      if (i >= p.m) return;
+      const Row row(e.row, i);
+      const float f = e.factor[i], by = f == 0.0f ? 0.0f : e.row.scale / f;
+      const uint64_t hit = row.token >= 0 ? static_cast<uint64_t>(row.token) - e.first : ~0ull;
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const float lp = (v[x] * e.scale - lse) - rest, q = __builtin_amdgcn_exp2f(lp * kLog2e);
-        const float own = c + x == hit ? g : 0.0f;
-        const float dz = q == 0.0f ? own : own - q * (g + d * (lp + h));
-        v[x] = none ? 0.0f : e.scale * dz;
-      }
-      put_parts<bf16_t, 8>(e.dz, row, c, p.n, v);
+      for (int x = 0; x < 8; ++x) v[x] = row.dz(v[x] * e.row.scale, c + x == hit) * by;
+      put_parts<bf16_t, 8>(e.dz, i, c, p.n, v);
     });
   }
 };
@@ -286,10 +341,12 @@ uint64_t piece(uint64_t rows, uint64_t vocab) {
 }
 
 struct Backward {
-  Prepared hidden, weight;    // of the logits' product
-  Prepared hidden2, weight2;  // of the gradients' products
+  Prepared hidden, weight;  // of the logits' product
+  Prepared weight2;         // of dhidden's
+  Parts scaled;             // rows of hidden times their factors
   Parts dz;
-  int parts, parts_dz;  // of the matrices in the gradients' products, and of dz
+  float* factor;
+  int parts;  // of the operands in the gradients' products
   float* sum;  // dhidden so far
   void* split;
   uint64_t piece;
@@ -299,19 +356,16 @@ Backward plan(const LinearLogprobGradArgs& a, Arena& ws) {
   const bool half = a.type == RSX_FLOAT16;
   const int n = a.type == RSX_FLOAT32 ? 3 : 1, n2 = half ? 2 : n;
   b.parts = n2;
-  b.parts_dz = a.type == RSX_FLOAT32 ? 3 : half || a.rows <= 256 ? 2 : 1;
   b.hidden = take_operand(ws, a.hidden, a.type, n, half, a.copies);
   b.weight = take_operand(ws, a.weight, a.type, n, half, a.copies);
-  b.hidden2 = b.hidden;
   b.weight2 = b.weight;
-  if (half) {
-    if (a.dweight) b.hidden2 = take_operand(ws, a.hidden, a.type, n2, false, a.copies);
-    if (a.dhidden) b.weight2 = take_operand(ws, a.weight, a.type, n2, false, a.copies);
-  }
+  if (half && a.dhidden) b.weight2 = take_operand(ws, a.weight, a.type, n2, false, a.copies);
+  if (a.dweight) b.scaled = take_parts(ws, a.rows, a.dim, n2);
+  b.factor = static_cast<float*>(ws.take(a.rows * 4));
   b.piece = piece(a.rows, a.vocab);
-  b.dz = take_parts(ws, a.rows, b.piece, b.parts_dz);
+  b.dz = take_parts(ws, a.rows, b.piece, n2);
   if (a.dhidden && b.piece < a.vocab) b.sum = static_cast<float*>(ws.take(a.rows * a.dim * 4));
-  const uint64_t segs = segments_of(b.parts_dz, n2);
+  const uint64_t segs = segments_of(n2, n2);
   uint64_t split = 0;
   const uint64_t last = b.piece ? a.vocab % b.piece : 0;  // the last piece is cut in its own way
   for (const uint64_t v : {b.piece, last}) {
@@ -324,6 +378,12 @@ Backward plan(const LinearLogprobGradArgs& a, Arena& ws) {
   }
   b.split = ws.take(split);
   return b;
+}
+
+template <class S>
+hipError_t factors(const LinearLogprobGradArgs& a, const Backward& b, const RowArgs& row, hipStream_t s) {
+  return launch(scale_rows<S>, grid_of(a.rows), 256, 0, s, static_cast<const S*>(a.hidden.p), a.hidden.ld, static_cast<const S*>(a.weight.p),
+                a.weight.ld, static_cast<uint32_t>(a.rows), static_cast<uint32_t>(a.dim), row, b.factor, b.scaled);
 }
 
 }  // namespace
@@ -372,10 +432,11 @@ hipError_t launch_linear_logprobs_grad(const LinearLogprobGradArgs& a, hipStream
   const Backward b = plan(a, ws);
   RSX_TRY(fill_operand(b.hidden, a.hidden, a.type, half, s));
   RSX_TRY(fill_operand(b.weight, a.weight, a.type, half, s));
-  if (half) {
-    if (a.dweight) RSX_TRY(fill_operand(b.hidden2, a.hidden, a.type, false, s));
-    if (a.dhidden) RSX_TRY(fill_operand(b.weight2, a.weight, a.type, false, s));
-  }
+  if (half && a.dhidden) RSX_TRY(fill_operand(b.weight2, a.weight, a.type, false, s));
+  const RowArgs row = {a.tokens, a.lse, a.lse_rest, a.entropy, a.dlogprob, a.dentropy, a.vocab, a.scale, a.wide};
+  if (a.rows)
+    RSX_TRY(a.type == RSX_FLOAT32    ? factors<float>(a, b, row, s)
+            : a.type == RSX_BFLOAT16 ? factors<bf16_t>(a, b, row, s) : factors<f16_t>(a, b, row, s));
   const uint64_t es = a.weight_type == RSX_FLOAT32 ? 4 : 2;
   for (uint64_t first = 0; first < a.vocab; first += b.piece) {
     const uint64_t v = a.vocab - first < b.piece ? a.vocab - first : b.piece;
@@ -387,24 +448,24 @@ hipError_t launch_linear_logprobs_grad(const LinearLogprobGradArgs& a, hipStream
     if (a.rows) {
       ProductArgs p = sizes(a.rows, v, a.dim);
       add_segments(p, b.hidden.op, n, rows_from(b.weight.op), n);
-      const DzArgs e = {a.tokens, a.lse, a.lse_rest, a.entropy, a.dlogprob, a.dentropy, b.dz, first, a.vocab, a.scale, a.wide};
+      const DzArgs e = {row, b.factor, b.dz, first};
       const Schedule c = schedule(a.rows, v, 1, steps_of(a.dim, p.nseg), false, false);
       RSX_TRY((half ? launch_product<f16_t, kRow, kRow, false, false, Dz>(p, c, b.split, e, s)
                     : launch_product<bf16_t, kRow, kRow, false, false, Dz>(p, c, b.split, e, s)));
     }
     if (a.dweight) {
       ProductArgs p = sizes(v, a.dim, a.rows);
-      add_segments(p, operand(b.dz), b.parts_dz, b.hidden2.op, b.parts);
+      add_segments(p, operand(b.dz), b.parts, operand(b.scaled), b.parts);
       void* to = static_cast<char*>(a.dweight) + first * a.dweight_ld * es;
-      RSX_TRY(launch_store(false, kTN, p, {to, a.dweight_ld, a.weight_type, nullptr, a.accumulate}, b.split, s));
+      RSX_TRY(launch_store(false, kTN, p, {to, a.dweight_ld, a.weight_type, nullptr, nullptr, a.accumulate}, b.split, s));
     }
     if (a.dhidden) {
       ProductArgs p = sizes(a.rows, a.dim, v);
-      add_segments(p, operand(b.dz), b.parts_dz, rows_from(b.weight2.op), b.parts);
+      add_segments(p, operand(b.dz), b.parts, rows_from(b.weight2.op), b.parts);
       const bool last = first + v == a.vocab;
       const float* add = first ? b.sum : nullptr;
-      const StoreArgs e = last ? StoreArgs{a.dhidden, a.dhidden_ld, a.type, add, 0}
-                               : StoreArgs{b.sum, a.dim, RSX_FLOAT32, add, 0};
+      const StoreArgs e = last ? StoreArgs{a.dhidden, a.dhidden_ld, a.type, add, b.factor, 0}
+                               : StoreArgs{b.sum, a.dim, RSX_FLOAT32, add, nullptr, 0};
       RSX_TRY(launch_store(false, kNN, p, e, b.split, s));
     }
   }

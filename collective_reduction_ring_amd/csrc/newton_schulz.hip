@@ -11,9 +11,12 @@
 // at the rate of 16-bit matrix instructions.  All three are bounded, and are kept
 // times 2^12, the parts' exponents far from either end: values up to 16 fit.
 //
-// Of a bf16 update the last step multiplies the first parts alone: its roundings are
-// not drawn out any more, and with them the matrix above is off by 1.75e-3 (rms)
-// where bf16's own rounding leaves 1.66e-3.  One step earlier it would be 2.5e-3.
+// Of a bf16 update the last step multiplies the first parts alone, from a square
+// of kSingle on: its roundings are not drawn out any more, and with them the matrix
+// above is off by 1.75e-3 (rms) where bf16's own rounding leaves 1.66e-3.  One step
+// earlier it would be 2.5e-3.  In a small square few roundings decide, as with any
+// common factor: a single vector came out 4.9e-3 off.  For the same reason a small
+// square in fp32 has three parts; there the time is the launches'.
 //
 // A and B are symmetric: only tiles on and below the diagonal are multiplied,
 // and stored to both sides.
@@ -23,6 +26,7 @@ namespace rsx {
 namespace {
 
 constexpr float kScale = 4096.0f, kUnscale = 1.0f / 4096.0f;
+constexpr uint64_t kSingle = 256, kTriple = 128;
 constexpr uint32_t kNormGroups = 512;  // workgroups that sum a matrix's squares, at most
 
 #define RSX_TRY(x)                        \
@@ -37,8 +41,8 @@ struct Stack {
   uint64_t each;  // elements from one to the next
   __device__ __forceinline__ Parts at(uint32_t i) const {
     Parts r = p;
-    r.part[0] = static_cast<f16_t*>(p.part[0]) + i * each;
-    r.part[1] = static_cast<f16_t*>(p.part[1]) + i * each;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) r.part[k] = static_cast<f16_t*>(p.part[k]) + i * each;
     return r;
   }
 };
@@ -101,7 +105,8 @@ __global__ __launch_bounds__(256) void first_parts(const S* x, uint64_t ld, uint
     const Parts ga = gram.at(m), po = poly.at(m);
     for (uint32_t c = n; c < ((n + 7) & ~7u); ++c)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 3; ++i) {
+        if (i >= ga.count) break;
         static_cast<f16_t*>(ga.part[i])[(r0 + t) * ga.ld + c] = 0.0f;
         static_cast<f16_t*>(po.part[i])[(r0 + t) * po.ld + c] = 0.0f;
       }
@@ -114,31 +119,23 @@ __global__ __launch_bounds__(256) void first_parts(const S* x, uint64_t ld, uint
 __device__ __forceinline__ void put_both(const Parts& p, uint32_t m, uint32_t n, uint32_t size, f32x8 v) {
   typedef Vec<f16_t, 8>::type V;
   if (n > m || m >= size) return;
-  const V hi = __builtin_convertvector(v, V);
-  const f32x8 back = __builtin_convertvector(hi, f32x8);
-  f32x8 rest;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) rest[e] = fabsf(back[e]) < INFINITY ? v[e] - back[e] : 0.0f;
-  const V lo = __builtin_convertvector(rest, V);
-  f16_t* a = static_cast<f16_t*>(p.part[0]);
-  f16_t* b = static_cast<f16_t*>(p.part[1]);
   const uint64_t at = m * p.ld + n;
   const bool whole = n + 7 <= m;
-  if (whole) {
-    *reinterpret_cast<V*>(a + at) = hi;
-    *reinterpret_cast<V*>(b + at) = lo;
-  }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    if (n + e > m) break;
-    if (!whole) {
-      a[at + e] = hi[e];
-      b[at + e] = lo[e];
+  for (int i = 0; i < 3; ++i) {
+    if (i >= p.count) break;
+    const V h = __builtin_convertvector(v, V);
+    f16_t* a = static_cast<f16_t*>(p.part[i]);
+    if (whole) *reinterpret_cast<V*>(a + at) = h;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (n + e > m) break;
+      if (!whole) a[at + e] = h[e];
+      if (n + e < m) a[(n + e) * p.ld + m] = h[e];
     }
-    if (n + e < m) {
-      a[(n + e) * p.ld + m] = hi[e];
-      b[(n + e) * p.ld + m] = lo[e];
-    }
+    const f32x8 back = __builtin_convertvector(h, f32x8);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = fabsf(back[e]) < INFINITY ? v[e] - back[e] : 0.0f;
   }
 }
 
@@ -221,21 +218,22 @@ Spread spread(uint64_t batch, uint64_t n, uint64_t wide, int parts) {
   return {schedule(n, n, batch, steps_of(wide, segs), true, true), schedule(n, n, batch, steps_of(n, segs), true, true),
           schedule(n, wide, batch, steps_of(n, segs), false, true)};
 }
-Stack take_stack(Arena& ws, uint64_t batch, uint64_t rows, uint64_t cols) {
+Stack take_stack(Arena& ws, uint64_t batch, uint64_t rows, uint64_t cols, int parts) {
   Stack s = {};
-  s.p = take_parts(ws, batch * rows, cols, 2);
+  s.p = take_parts(ws, batch * rows, cols, parts);
   s.each = rows * s.p.ld;
   return s;
 }
-Space plan(Arena& ws, uint64_t batch, uint64_t n, uint64_t wide) {
+int parts_of(uint64_t n, int type) { return type == RSX_FLOAT32 && n < kTriple ? 3 : 2; }
+Space plan(Arena& ws, uint64_t batch, uint64_t n, uint64_t wide, int parts) {
   Space p;
   p.sums = static_cast<double*>(ws.take(batch * kNormGroups * sizeof(double)));
-  p.x = take_stack(ws, batch, n, wide);
-  p.y = take_stack(ws, batch, n, wide);
-  p.gram = take_stack(ws, batch, n, n);
-  p.poly = take_stack(ws, batch, n, n);
-  const uint64_t one = spread(batch, n, wide, 1).bytes(), two = spread(batch, n, wide, 2).bytes();
-  p.pieces = ws.take(one < two ? two : one);
+  p.x = take_stack(ws, batch, n, wide, parts);
+  p.y = take_stack(ws, batch, n, wide, parts);
+  p.gram = take_stack(ws, batch, n, n, parts);
+  p.poly = take_stack(ws, batch, n, n, parts);
+  const uint64_t one = spread(batch, n, wide, 1).bytes(), all = spread(batch, n, wide, parts).bytes();
+  p.pieces = ws.take(one < all ? all : one);
   return p;
 }
 
@@ -265,7 +263,8 @@ hipError_t start(const NewtonSchulzArgs& a, const Space& w, uint64_t n, uint64_t
 
 uint64_t newton_schulz_ws(uint64_t batch, uint64_t rows, uint64_t cols) {
   Arena ws(nullptr);
-  plan(ws, batch, rows < cols ? rows : cols, rows < cols ? cols : rows);
+  const uint64_t n = rows < cols ? rows : cols, wide = rows < cols ? cols : rows;
+  plan(ws, batch, n, wide, n < kTriple ? 3 : 2);  // of any type
   return ws.at;
 }
 
@@ -273,13 +272,14 @@ hipError_t launch_newton_schulz(const NewtonSchulzArgs& a, hipStream_t s) {
   const bool tall = a.rows > a.cols;
   const uint64_t n = tall ? a.cols : a.rows, wide = tall ? a.rows : a.cols;
   Arena ws(a.ws);
-  const Space w = plan(ws, a.batch, n, wide);
+  const int all = parts_of(n, a.type);
+  const Space w = plan(ws, a.batch, n, wide, all);
   RSX_TRY(a.type == RSX_FLOAT32    ? start<float>(a, w, n, wide, tall, s)
           : a.type == RSX_BFLOAT16 ? start<bf16_t>(a, w, n, wide, tall, s) : start<f16_t>(a, w, n, wide, tall, s));
   Stack x = w.x, y = w.y;
   for (int step = 0; step < a.steps; ++step) {
     const bool last = step + 1 == a.steps;
-    const int parts = last && step != 0 && a.type == RSX_BFLOAT16 ? 1 : 2;  // a single step is the first one too
+    const int parts = last && step != 0 && n >= kSingle && a.type == RSX_BFLOAT16 ? 1 : all;  // a single step is the first one too
     const Spread c = spread(a.batch, n, wide, parts);
     ProductArgs p = {};
     p.batch = static_cast<uint32_t>(a.batch);

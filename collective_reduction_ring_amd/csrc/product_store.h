@@ -14,6 +14,7 @@ struct StoreArgs {
   uint64_t ld;
   int type;
   const float* add;  // fp32 [m][n] to add, or null
+  const float* row;  // then a factor for each row, or null
   int accumulate;    // add what `out` holds
 };
 

@@ -12,6 +12,7 @@ struct Store {
     staged<TILE, false, N>(w, acc, i0, lds, [&](uint32_t m, uint32_t n, f32x8 v) {
       if (m >= p.m || n >= p.n) return;
       if (e.add) v += get<float, 8>(e.add + static_cast<uint64_t>(m) * p.n, n, p.n);
+      if (e.row) v *= e.row[m];
       if (e.accumulate) v += get_as<8>(e.type, e.out, m * e.ld, n, p.n);
       put_as<8>(e.type, e.out, m * e.ld, n, p.n, v);
     });

@@ -612,7 +612,8 @@ rsx_status_t rsx_linear_logprobs(const void* hidden, size_t hidden_stride, const
  * dweight = dz^T hidden (with `accumulate` added to what is there).  Either may
  * be null.  dweight is of dweight_type: `type` or RSX_FLOAT32.
  * The vocabulary is taken in pieces, of which the logits are multiplied again.
- * dz is rounded to bf16 (fp16 matrices and up to 256 rows: to 16 bits, with the
+ * dz is rounded to bf16, each row by itself divided by its token's dz, and the
+ * rows of hidden times that to bf16 too (fp16 matrices: either to 16 bits, with the
  * range of fp32; fp32: kept whole).
  */
 size_t rsx_linear_logprobs_grad_workspace_size(size_t rows, size_t vocab, size_t dim,

@@ -140,14 +140,17 @@ def linear_logprobs_grad(hidden, weight, tokens, lse, ent, g, d, scale):
     e = e + p * ez.exp() * ez * (gg + dd * (flat + hh + 1))
     sc = abs(float(torch.tensor(scale, dtype=torch.float32)))
     dz, e = dz * float(torch.tensor(scale, dtype=torch.float32)), e * sc
-    # as an operand: bf16, two bf16 values, or three
-    e = e + {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -16, torch.float32: 2.0 ** -24}[t] * (dz.abs() + e) + U * dz.abs()
+    # as operands, dz and the hidden states are bf16, two bf16 values, or three; either has a factor of the row taken out
+    # or put in, an fp32 rounding or two each
+    r = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -16, torch.float32: 2.0 ** -24}[t]
+    e = e + (r + 4 * U) * (dz.abs() + e)
     parts = {torch.bfloat16: 1, torch.float16: 2, torch.float32: 3}[t]
     h, w = hidden.double(), weight.double()
+    eh = h.abs() * (r + 2 * U)
     dh, dw = dz @ w, dz.t() @ h
-    eh = e @ w.abs() + terms(t, dz.shape[1], parts) * ((dz.abs() + e) @ w.abs())
-    ew = e.t() @ h.abs() + terms(t, dz.shape[0], parts) * ((dz.abs() + e).t() @ h.abs())
-    return (dh, dw), (eh, ew)
+    e_dh = e @ w.abs() + terms(t, dz.shape[1], parts) * ((dz.abs() + e) @ w.abs()) + 4 * U * dh.abs()
+    e_dw = e.t() @ (h.abs() + eh) + dz.abs().t() @ eh + terms(t, dz.shape[0], parts) * ((dz.abs() + e).t() @ (h.abs() + eh))
+    return (dh, dw), (e_dh, e_dw)
 
 
 # ------------------------------------------------- orthogonalised updates
@@ -178,7 +181,7 @@ def newton_schulz(x, steps, coefficients, eps, noise=None, dtype=torch.float32):
         return v if noise is None else v + signs(v) * 2 * U * math.sqrt(3 * p.shape[1]) * ((p * p) @ (q * q)).sqrt()
     x = keep(x / (x.norm() + float(torch.tensor(eps, dtype=torch.float32))))
     for step in range(steps):
-        single = dtype == torch.bfloat16 and step and step + 1 == steps
+        single = dtype == torch.bfloat16 and step and step + 1 == steps and min(x.shape) >= 256
         gram = keep(product(x, x.t(), single))
         poly = keep(b * gram + c * product(gram, gram, single))
         x = keep(a * x + product(poly, x, single))
