@@ -150,6 +150,31 @@ struct FewStore {
   }
 };
 
+struct FewSumsArgs {
+  float* to;  // [cut][row][column]
+};
+struct FewSums {
+  typedef FewSumsArgs Args;
+  template <class T, int RG>
+  static __device__ __forceinline__ void few(const FewArgs& p, const FewSumsArgs& e, uint32_t row, uint32_t c, const f32x4 (&v)[RG]) {
+    if (row >= p.n) return;
+    float* to = e.to + (static_cast<uint64_t>(few_cut(p)) * p.n + row) * p.rows;
+#pragma unroll
+    for (int r = 0; r < RG; ++r)
+      if (c + 16 * r < p.rows) put<float, 4>(to, c + 16 * r, p.rows, v[r]);
+  }
+};
+__global__ __launch_bounds__(256) void few_add(const float* sums, uint32_t cuts, uint32_t rows, uint32_t dim, void* out, uint64_t ld, int type) {
+  const uint64_t t = block_id() * 256 + threadIdx.x, all = static_cast<uint64_t>(rows) * dim;
+  if (t >= all) return;
+  float v = sums[t];
+  for (uint32_t c = 1; c < cuts; ++c) v += sums[c * all + t];
+  const uint32_t c = static_cast<uint32_t>(t % dim);
+  put_as<1>(type, out, t / dim * ld, c, c + 1, typename Vec<float, 1>::type{v});
+}
+// Bytes of act(g) * u in the few-row form.
+uint64_t few_product_bytes(const FeedForwardArgs& a) { return (a.rows * copy_ld(a.hidden) * 4 + 255) & ~255ull; }
+
 // Parts of a matrix of `type` as an operand: fp32 is three bf16 values exactly.
 int parts_of(int type) { return type == RSX_FLOAT32 ? 3 : 1; }
 
@@ -168,6 +193,14 @@ ProductArgs sizes(uint64_t m, uint64_t n, uint64_t k) {
     if (st_ != hipSuccess) return st_;    \
   } while (0)
 
+// Into how many stretches of k the second product's workgroups are cut where its
+// rows are too few for the CUs: 256 at least, and 1024 k a stretch.  (192 rows of
+// 26577 bf16: 72 us uncut.)
+uint32_t few_cuts(uint64_t dim, uint64_t hidden) {
+  const uint64_t groups = (dim + 15) / 16, most = hidden / 1024, cuts = groups ? kCus / groups : 0;
+  return static_cast<uint32_t>(cuts < 2 || most < 2 ? 1 : cuts < most ? cuts : most);
+}
+
 template <class T>
 hipError_t few(const FeedForwardArgs& a, void* s, hipStream_t stream) {
   GateArgs e = {{{s, nullptr, nullptr}, copy_ld(a.hidden), 1}, static_cast<float*>(s), a.gate, a.up, a.act};
@@ -176,7 +209,13 @@ hipError_t few(const FeedForwardArgs& a, void* s, hipStream_t stream) {
   if (a.hidden) RSX_TRY((launch_few<T, 1, true, Gate>(p, e, stream)));
   p = {s, a.w_down.p, nullptr, sizeof(T) == 4 ? a.hidden : copy_ld(a.hidden), a.w_down.ld, 0, static_cast<uint32_t>(a.rows),
        static_cast<uint32_t>(a.dim), static_cast<uint32_t>(a.hidden)};
-  return launch_few<T, 1, false, FewStore>(p, {a.out, a.out_ld, a.type, nullptr, nullptr, 0}, stream);
+  const uint32_t cuts = few_cuts(a.dim, a.hidden);
+  if (cuts == 1) return launch_few<T, 1, false, FewStore>(p, {a.out, a.out_ld, a.type, nullptr, nullptr, 0}, stream);
+  float* sums = reinterpret_cast<float*>(static_cast<char*>(s) + few_product_bytes(a));
+  p.cuts = cuts;
+  RSX_TRY((launch_few<T, 1, false, FewSums>(p, {sums}, stream)));
+  return launch(few_add, grid_of((a.rows * a.dim + 255) / 256), 256, 0, stream, sums, cuts, static_cast<uint32_t>(a.rows),
+                static_cast<uint32_t>(a.dim), a.out, a.out_ld, a.type);
 }
 
 struct Forward {
@@ -241,7 +280,10 @@ Backward plan(const FeedForwardGradArgs& a, Arena& ws) {
 }  // namespace
 
 uint64_t feed_forward_ws(const FeedForwardArgs& a) {
-  if (a.rows <= kFewRows) return a.rows * copy_ld(a.hidden) * 4;
+  if (a.rows <= kFewRows) {
+    const uint32_t cuts = few_cuts(a.dim, a.hidden);
+    return few_product_bytes(a) + (cuts > 1 ? cuts * a.rows * a.dim * 4 : 0);
+  }
   Arena ws(nullptr);
   plan(a, ws);
   return ws.at;
@@ -254,10 +296,12 @@ hipError_t launch_feed_forward(const FeedForwardArgs& a, hipStream_t s) {
   const int n = parts_of(a.type);
   Arena ws(a.ws);
   const Forward f = plan(a, ws);
-  RSX_TRY(fill_operand(f.x, a.x, a.type, half, s));
-  RSX_TRY(fill_operand(f.wg, a.w_gate, a.type, half, s));
-  RSX_TRY(fill_operand(f.wu, a.w_up, a.type, half, s));
-  RSX_TRY(fill_operand(f.wd, a.w_down, a.type, half, s));
+  Copies c = {};
+  fill_operand(c, f.x, a.x);
+  fill_operand(c, f.wg, a.w_gate);
+  fill_operand(c, f.wu, a.w_up);
+  fill_operand(c, f.wd, a.w_down);
+  RSX_TRY(launch_copies(c, a.type, half, s));
   ProductArgs p = sizes(a.rows, a.hidden, a.dim);
   add_segments(p, f.x.op, n, f.wg.op, n, &f.wu.op);
   const GateArgs e = {f.s, nullptr, a.gate, a.up, a.act};
@@ -279,13 +323,15 @@ hipError_t launch_feed_forward_grad(const FeedForwardGradArgs& a, hipStream_t s)
   const int n = parts_of(a.type);
   Arena ws(a.ws);
   const Backward b = plan(a, ws);
-  RSX_TRY(fill_operand(b.dout, a.dout, a.type, half, s));
-  RSX_TRY(fill_operand(b.wd, a.w_down, a.type, half, s));
-  if (a.dw_gate) RSX_TRY(fill_operand(b.x, a.x, a.type, half, s));
+  Copies c = {};
+  fill_operand(c, b.dout, a.dout);
+  fill_operand(c, b.wd, a.w_down);
+  if (a.dw_gate) fill_operand(c, b.x, a.x);
   if (a.dx) {
-    RSX_TRY(fill_operand(b.wg, a.w_gate, a.type, half, s));
-    RSX_TRY(fill_operand(b.wu, a.w_up, a.type, half, s));
+    fill_operand(c, b.wg, a.w_gate);
+    fill_operand(c, b.wu, a.w_up);
   }
+  RSX_TRY(launch_copies(c, a.type, half, s));
   ProductArgs p = sizes(a.rows, a.hidden, a.dim);
   add_segments(p, b.dout.op, n, b.wd.op, n);
   const GateGradArgs e = {a.gate, a.up, b.s, b.dg, b.du, a.act};

@@ -20,7 +20,10 @@ struct FewArgs {
   const void* w2;  // second matrix of a double product
   uint64_t ldx, ldw, ldw2;
   uint32_t n, rows, k;  // rows of x, of the matrix; length of either
+  uint32_t cuts;        // workgroups that share a group of rows' k; 0 is 1
 };
+// Which of them this one is.
+__device__ __forceinline__ uint32_t few_cut(const FewArgs& p) { return p.cuts ? static_cast<uint32_t>(block_id() % p.cuts) : 0; }
 
 constexpr int kFewWaves = 8;
 constexpr uint32_t kFewRows = 64;  // rows of x that this form takes
@@ -47,8 +50,10 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void few_rows_kernel(const FewAr
   typedef typename FewFrag<T>::type V;
   __shared__ f32x4 sums[kFewWaves][NM][NT][64];
   const uint32_t l = threadIdx.x % 64, wave = uniform(threadIdx.x / 64), r = l % 16, g = l / 16;
-  const uint32_t first = static_cast<uint32_t>(block_id()) * (16 * RG);
-  if (first >= p.rows) return;
+  const uint32_t cuts = p.cuts ? p.cuts : 1, cut = few_cut(p);
+  const uint64_t group = block_id() / cuts;
+  if (group * (16 * RG) >= p.rows) return;
+  const uint32_t first = static_cast<uint32_t>(group) * (16 * RG);
   const T* wr[NM];
   const T* xr[NT];
 #pragma unroll
@@ -63,12 +68,14 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void few_rows_kernel(const FewAr
   for (int m = 0; m < NM; ++m)
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const uint32_t turns = p.k / (U * S), mine = turns > wave ? (turns - wave + kFewWaves - 1) / kFewWaves : 0;
+  // the waves of all cuts take turns
+  const uint32_t turns = p.k / (U * S), all = kFewWaves * cuts, me = cut * kFewWaves + wave;
+  const uint32_t mine = turns > me ? (turns - me + all - 1) / all : 0;
   // Workgroups begin in different places of the rows: row strides are often powers of two, and in step all would
   // ask the same memory channels.
-  uint32_t at = mine ? static_cast<uint32_t>(block_id()) % mine : 0;
+  uint32_t at = mine ? static_cast<uint32_t>(group % mine) : 0;
   for (uint32_t i = 0; i < mine; ++i) {
-    const uint32_t turn = wave + at * kFewWaves;
+    const uint32_t turn = me + at * all;
     at = at + 1 < mine ? at + 1 : 0;
     V w[U][NM], x[U][NT];
 #pragma unroll
@@ -86,7 +93,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void few_rows_kernel(const FewAr
 #pragma unroll
         for (int t = 0; t < NT; ++t) acc[m][t] = few_mma(w[u][m], x[u][t], acc[m][t]);
   }
-  for (uint32_t step = turns * U + wave; step * S < p.k; step += kFewWaves) {
+  for (uint32_t step = turns * U + me; step * S < p.k; step += all) {
     // what is left of a row, element by element where it ends in a lane's 16 bytes
     const uint32_t k = step * S + g * N;
     V x[NT];
@@ -118,7 +125,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void few_rows_kernel(const FewAr
 
 template <class T, int RG, bool DUAL, class EPILOGUE>
 hipError_t launch_few(const FewArgs& p, const typename EPILOGUE::Args& e, hipStream_t s) {
-  const dim3 grid = grid_of((static_cast<uint64_t>(p.rows) + 16 * RG - 1) / (16 * RG));
+  const dim3 grid = grid_of((static_cast<uint64_t>(p.rows) + 16 * RG - 1) / (16 * RG) * (p.cuts ? p.cuts : 1));
   if (p.n <= 16) return launch(few_rows_kernel<T, 1, RG, DUAL, EPILOGUE>, grid, 64 * kFewWaves, 0, s, p, e);
   if (p.n <= 32) return launch(few_rows_kernel<T, 2, RG, DUAL, EPILOGUE>, grid, 64 * kFewWaves, 0, s, p, e);
   return launch(few_rows_kernel<T, 4, RG, DUAL, EPILOGUE>, grid, 64 * kFewWaves, 0, s, p, e);

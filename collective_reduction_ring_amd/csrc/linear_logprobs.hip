@@ -406,8 +406,10 @@ hipError_t launch_linear_logprobs(const LinearLogprobArgs& a, hipStream_t s) {
              : half                ? launch_few<f16_t, kFewGroups, false, Softmax>(p, e, s)
                                    : launch_few<bf16_t, kFewGroups, false, Softmax>(p, e, s)));
   } else {
-    RSX_TRY(fill_operand(f.hidden, a.hidden, a.type, half, s));
-    RSX_TRY(fill_operand(f.weight, a.weight, a.type, half, s));
+    Copies c = {};
+    fill_operand(c, f.hidden, a.hidden);
+    fill_operand(c, f.weight, a.weight);
+    RSX_TRY(launch_copies(c, a.type, half, s));
     ProductArgs p = sizes(a.rows, a.vocab, a.dim);
     const int n = a.type == RSX_FLOAT32 ? 3 : 1;
     add_segments(p, f.hidden.op, n, f.weight.op, n);
@@ -430,9 +432,15 @@ hipError_t launch_linear_logprobs_grad(const LinearLogprobGradArgs& a, hipStream
   const int n = a.type == RSX_FLOAT32 ? 3 : 1;
   Arena ws(a.ws);
   const Backward b = plan(a, ws);
-  RSX_TRY(fill_operand(b.hidden, a.hidden, a.type, half, s));
-  RSX_TRY(fill_operand(b.weight, a.weight, a.type, half, s));
-  if (half && a.dhidden) RSX_TRY(fill_operand(b.weight2, a.weight, a.type, false, s));
+  Copies copies = {};
+  fill_operand(copies, b.hidden, a.hidden);
+  fill_operand(copies, b.weight, a.weight);
+  RSX_TRY(launch_copies(copies, a.type, half, s));
+  if (half && a.dhidden) {
+    Copies c = {};
+    fill_operand(c, b.weight2, a.weight);
+    RSX_TRY(launch_copies(c, a.type, false, s));
+  }
   const RowArgs row = {a.tokens, a.lse, a.lse_rest, a.entropy, a.dlogprob, a.dentropy, a.vocab, a.scale, a.wide};
   if (a.rows)
     RSX_TRY(a.type == RSX_FLOAT32    ? factors<float>(a, b, row, s)

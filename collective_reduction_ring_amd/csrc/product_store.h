@@ -40,8 +40,15 @@ inline Parts take_parts(Arena& ws, uint64_t rows, uint64_t cols, int count) {
 inline Operand operand(const Parts& p) { return {{p.part[0], p.part[1], p.part[2]}, p.ld}; }
 inline Operand operand(const Matrix& m) { return {{m.p, nullptr, nullptr}, m.ld}; }
 
-// dst = the parts of a matrix of `type`, zeros behind its columns.
-hipError_t launch_copy(const Matrix& m, int type, const Parts& dst, bool half, hipStream_t s);
+// Matrices of one type to be kept as parts, zeros behind their columns: one launch.
+struct Copies {
+  static constexpr int kMost = 6;
+  Matrix from[kMost];
+  Parts to[kMost];
+  uint64_t begin[kMost + 1];  // workgroups before each
+  int n;
+};
+hipError_t launch_copies(Copies& c, int type, bool half, hipStream_t s);
 
 // A matrix as an operand of `count` parts of bf16 (or fp16 with half): itself
 // where that is possible, else a copy.
@@ -59,8 +66,10 @@ inline Prepared take_operand(Arena& ws, const Matrix& m, int type, int count, bo
   r.op = r.copied ? operand(r.copy) : operand(m);
   return r;
 }
-inline hipError_t fill_operand(const Prepared& r, const Matrix& m, int type, bool half, hipStream_t s) {
-  return r.copied ? launch_copy(m, type, r.copy, half, s) : hipSuccess;
+inline void fill_operand(Copies& c, const Prepared& r, const Matrix& m) {
+  if (!r.copied || m.rows == 0 || m.cols == 0) return;
+  c.from[c.n] = m;
+  c.to[c.n++] = r.copy;
 }
 
 }  // namespace rsx

@@ -27,28 +27,29 @@ hipError_t store(Layouts l, const ProductArgs& p, const Schedule& c, const Store
 }
 
 // A workgroup moves one stretch of 2048 elements of a row, eight a lane.
+constexpr uint64_t kStretch = 2048;
 template <class S, class T>
-__global__ __launch_bounds__(256) void copy_parts(const S* src, uint64_t ld, uint32_t rows, uint32_t cols, uint32_t groups, Parts dst) {
-  const uint64_t id = block_id();
-  const uint64_t row = id / groups;
-  const uint32_t c = static_cast<uint32_t>(id % groups) * 2048 + threadIdx.x * 8;
-  if (row >= rows || c >= dst.ld) return;
-  typename Vec<float, 8>::type v = __builtin_convertvector((load_row<S, 8, false>(src + row * ld, c, cols)), typename Vec<float, 8>::type);
+__global__ __launch_bounds__(256) void copy_parts(const Copies c) {
+  uint64_t id = block_id();
+  int i = 0;
+  while (i < c.n && id >= c.begin[i + 1]) ++i;
+  if (i == c.n) return;
+  id -= c.begin[i];
+  const Matrix from = c.from[i];
+  const Parts to = c.to[i];
+  const uint64_t groups = (to.ld + kStretch - 1) / kStretch, row = id / groups;
+  const uint32_t col = static_cast<uint32_t>(id % groups * kStretch) + threadIdx.x * 8;
+  if (col >= to.ld) return;
+  f32x8 v = __builtin_convertvector((load_row<S, 8, false>(static_cast<const S*>(from.p) + row * from.ld, col, static_cast<uint32_t>(from.cols))), f32x8);
 #pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    if (i >= dst.count) break;
+  for (int k = 0; k < 3; ++k) {
+    if (k >= to.count) break;
     const auto h = __builtin_convertvector(v, typename Vec<T, 8>::type);
-    *reinterpret_cast<typename Vec<T, 8>::type*>(static_cast<T*>(dst.part[i]) + row * dst.ld + c) = h;
-    const auto back = __builtin_convertvector(h, typename Vec<float, 8>::type);
+    *reinterpret_cast<typename Vec<T, 8>::type*>(static_cast<T*>(to.part[k]) + row * to.ld + col) = h;
+    const f32x8 back = __builtin_convertvector(h, f32x8);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = fabsf(back[e]) < INFINITY ? v[e] - back[e] : 0.0f;
   }
-}
-template <class S, class T>
-hipError_t copy(const Matrix& m, const Parts& dst, hipStream_t s) {
-  const uint32_t groups = static_cast<uint32_t>((dst.ld + 2047) / 2048);
-  return launch(copy_parts<S, T>, grid_of(m.rows * groups), 256, 0, s, static_cast<const S*>(m.p), m.ld,
-                static_cast<uint32_t>(m.rows), static_cast<uint32_t>(m.cols), groups, dst);
 }
 
 }  // namespace
@@ -81,7 +82,7 @@ Schedule schedule(uint64_t m, uint64_t n, uint64_t batch, uint64_t steps, bool t
     cuts = cuts > steps / 4 ? steps / 4 : cuts;  // a piece of fewer steps is mostly its ends
     cuts = cuts > 16 ? 16 : cuts;
     if (cuts < 2) continue;
-    const double cut = whole + rate(rest * cuts) * (s / static_cast<double>(cuts)) + kEnds[i] + 5.0 + kPiece[i] * static_cast<double>(cuts);
+    const double cut = whole + rate(rest * cuts) * (s / static_cast<double>(cuts)) + kEnds[i] + 3.0 + kPiece[i] * static_cast<double>(cuts);
     if (cut < least) {
       least = cut;
       best = {i, static_cast<uint32_t>(tiles - rest), static_cast<uint32_t>(cuts), rest * cuts * kSide[i] * kSide[i] * 4};
@@ -97,11 +98,15 @@ hipError_t launch_store(bool half, Layouts l, ProductArgs p, const StoreArgs& e,
   return half ? store<f16_t>(l, p, c, e, ws, s) : store<bf16_t>(l, p, c, e, ws, s);
 }
 
-hipError_t launch_copy(const Matrix& m, int type, const Parts& dst, bool half, hipStream_t s) {
-  if (m.rows == 0 || m.cols == 0) return hipSuccess;
-  if (half) return copy<f16_t, f16_t>(m, dst, s);  // no fp32 matrix is cut into fp16 parts here
-  return type == RSX_FLOAT32 ? copy<float, bf16_t>(m, dst, s)
-                             : type == RSX_BFLOAT16 ? copy<bf16_t, bf16_t>(m, dst, s) : copy<f16_t, bf16_t>(m, dst, s);
+hipError_t launch_copies(Copies& c, int type, bool half, hipStream_t s) {
+  c.begin[0] = 0;
+  for (int i = 0; i < c.n; ++i) c.begin[i + 1] = c.begin[i] + c.from[i].rows * ((c.to[i].ld + kStretch - 1) / kStretch);
+  if (c.n == 0) return hipSuccess;
+  // no fp32 matrix is cut into fp16 parts here
+  return launch(half                    ? copy_parts<f16_t, f16_t>
+                : type == RSX_FLOAT32  ? copy_parts<float, bf16_t>
+                : type == RSX_BFLOAT16 ? copy_parts<bf16_t, bf16_t> : copy_parts<f16_t, bf16_t>,
+                grid_of(c.begin[c.n]), 256, 0, s, c);
 }
 
 }  // namespace rsx

@@ -37,6 +37,7 @@ FFN = [  # rows, dim, hidden, type, activation, pad, kept
     (100, 33, 47, F32, "silu", 0, True), (128, 128, 128, BF16, "relu", 0, True), (129, 264, 200, BF16, "gelu_tanh", 1, True),
     (200, 1, 300, BF16, "silu", 0, True), (300, 300, 1, F32, "gelu", 0, True), (257, 71, 129, F16, "silu", 3, True),
     (130, 1025, 513, F32, "gelu_tanh", 1, True), (1000, 136, 520, BF16, "silu", 0, True), (70, 8, 2000, BF16, "gelu", 0, True),
+    (4, 200, 9001, BF16, "silu", 0, True), (33, 24, 5000, F32, "gelu", 0, True), (64, 5, 2048, F16, "relu", 1, True),
 ]
 
 
@@ -95,7 +96,7 @@ def whole(g, rows, cols, each, values=(-1, 1)):
 
 
 EXACT = [  # rows, dim, hidden: of large tiles, middle ones, cut sums, few rows
-    (2100, 520, 4200), (2048, 256, 8192), (700, 2056, 1000), (130, 4096, 264), (37, 3000, 1500), (5, 11008, 4099),
+    (2100, 520, 4200), (2048, 256, 8192), (700, 2056, 1000), (130, 4096, 264), (37, 3000, 1500), (5, 11008, 4099), (7, 136, 20000),
 ]
 
 
@@ -105,7 +106,7 @@ def test_feed_forward_whole_numbers(rows, dim, hidden, t):
     say("feed_forward whole", rows, dim, hidden, t)
     g = gen(rows)
     x, wg, wu, dy = whole(g, rows, dim, 3), whole(g, hidden, dim, dim // 4), whole(g, hidden, dim, dim // 4), whole(g, rows, dim, 3)
-    wd = whole(g, dim, hidden, 4)
+    wd = whole(g, dim, hidden, 4)  # of 7 x 136 x 20000 and the like the second product's k is cut
     dev = [m.to(DEV, t) for m in (x, wg, wu, wd, dy)]
     p = rsx.feed_forward(*dev[:4], activation="relu", keep=True)
     x, wg, wu, wd, dy = (m.double() for m in dev)
