@@ -4,8 +4,9 @@
 //
 // A workgroup takes 16 * RG of the matrix's rows and its waves share k out
 // in turns of U steps; their sums meet in LDS.  (131072 x 4096 bf16: eight waves and
-// turns of four steps 185 us; four and eight 191, with streamed loads, which fetch
-// a cache line again for its other half, 221.)  A step is one matrix
+// turns of four steps 185 us, 5.8 TB/s; four and eight 191, with streamed loads,
+// which fetch a cache line again for its other half, 221; sixteen and two 176, but
+// 264 with the softmax's registers.) A step is one matrix
 // instruction of 32 k (16 bits) or four of 4 k (fp32, whose products stay fp32
 // here): a lane's 16 bytes of a row are its k, in the matrix and in x alike.
 #pragma once
@@ -26,7 +27,7 @@ struct FewArgs {
 __device__ __forceinline__ uint32_t few_cut(const FewArgs& p) { return p.cuts ? static_cast<uint32_t>(block_id() % p.cuts) : 0; }
 
 constexpr int kFewWaves = 8;
-constexpr uint32_t kFewRows = 64;  // rows of x that this form takes
+constexpr uint32_t kFewRows = 64;  // rows of x that this form takes at most
 
 template <class T>
 struct FewFrag {

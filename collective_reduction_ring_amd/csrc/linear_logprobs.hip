@@ -303,6 +303,11 @@ ProductArgs sizes(uint64_t m, uint64_t n, uint64_t k) {
   return p;
 }
 
+// Whether a call takes the few-row form: 16-bit matrices that the tiles read in
+// place are faster there from 17 rows on (65536 x 4096 bf16: 99 us for 16 rows and
+// 113 to 120 for 17 to 128 in tiles, 129 for 32 here); others would be copied first.
+bool few_form(const LinearLogprobArgs& a) { return a.rows <= (a.type == RSX_FLOAT32 || a.copies ? kFewRows : 16); }
+
 constexpr int kFewGroups = 2;  // of 16 matrix rows: with one, x is read from L2 as often as the matrix from memory
 
 struct Forward {
@@ -318,7 +323,7 @@ Forward plan(const LinearLogprobArgs& a, Arena& ws) {
   Forward f = {};
   const int n = a.type == RSX_FLOAT32 ? 3 : 1;
   const bool half = a.type == RSX_FLOAT16;
-  f.few = a.rows <= kFewRows;
+  f.few = few_form(a);
   f.spread = schedule(a.rows, a.vocab, 1, steps_of(a.dim, segments_of(n, n)), false, false);
   const uint64_t width = f.few ? 16 * kFewGroups : f.spread.tile == 0 ? Large::BN : Middle::BN;
   f.tiles = static_cast<uint32_t>((a.vocab + width - 1) / width);
@@ -391,7 +396,13 @@ hipError_t factors(const LinearLogprobGradArgs& a, const Backward& b, const RowA
 uint64_t linear_logprobs_ws(const LinearLogprobArgs& a) {
   Arena ws(nullptr);
   plan(a, ws);
-  return ws.at;
+  if (!a.copies) return ws.at;
+  // what is right for matrices that are copied is right for others too
+  LinearLogprobArgs b = a;
+  b.copies = false;
+  Arena other(nullptr);
+  plan(b, other);
+  return ws.at > other.at ? ws.at : other.at;
 }
 
 hipError_t launch_linear_logprobs(const LinearLogprobArgs& a, hipStream_t s) {

@@ -202,3 +202,15 @@ def test_oracle_newton_schulz():
     assert (got - want).abs().max() < 1e-10
     assert (po.newton_schulz(x.t(), 5, po.USUAL, 0.0) - want.t()).abs().max() < 1e-10
     assert (s > 0.6).all() and (s < 1.3).all()
+
+
+@pytest.mark.parametrize("t", [BF16, F16, F32])
+def test_a_workspace_for_copies_is_right_without(t):
+    lib = L.lib()
+    for rows in (1, 16, 17, 32, 33, 64, 65, 300):
+        for dim, hidden in ((64, 96), (4096, 11008), (128, 40000), (7, 5)):
+            for size, args in ((lib.rsx_feed_forward_workspace_size, (rows, dim, hidden)),
+                               (lib.rsx_feed_forward_grad_workspace_size, (rows, dim, hidden)),
+                               (lib.rsx_linear_logprobs_workspace_size, (rows, hidden, dim)),
+                               (lib.rsx_linear_logprobs_grad_workspace_size, (rows, hidden, dim))):
+                assert size(*args, t, 0) <= size(*args, t, 1), (size.__name__, args)
