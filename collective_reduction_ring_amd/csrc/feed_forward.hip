@@ -278,8 +278,11 @@ Backward plan(const FeedForwardGradArgs& a, Arena& ws) {
     b.wg = take_operand(ws, a.w_gate, a.type, n, half, a.copies);
     b.wu = take_operand(ws, a.w_up, a.type, n, half, a.copies);
   }
-  b.dg = take_parts(ws, a.rows, a.hidden, n);
-  b.du = take_parts(ws, a.rows, a.hidden, n);
+  // one above the other, so that the two products with x are one launch
+  b.dg = take_parts(ws, 2 * a.rows, a.hidden, n);
+  b.du = b.dg;
+  if (ws.base != nullptr)
+    for (int i = 0; i < n; ++i) b.du.part[i] = static_cast<char*>(b.dg.part[i]) + a.rows * b.dg.ld * 2;
   const uint64_t segs = segments_of(n, n);
   b.gate = schedule(a.rows, a.hidden, 1, steps_of(a.dim, segs), false, false);
   uint64_t split = b.gate.bytes;
@@ -288,7 +291,7 @@ Backward plan(const FeedForwardGradArgs& a, Arena& ws) {
     split = split < x ? x : split;
   }
   if (a.dw_gate) {
-    const uint64_t g = store_ws(a.hidden, a.dim, a.rows, segs), d = store_ws(a.dim, a.hidden, a.rows, segs);
+    const uint64_t g = store_ws(a.hidden, a.dim, a.rows, segs, 2), d = store_ws(a.dim, a.hidden, a.rows, segs);
     split = split < g ? g : split;
     split = split < d ? d : split;
   }
@@ -371,10 +374,9 @@ hipError_t launch_feed_forward_grad(const FeedForwardGradArgs& a, hipStream_t s)
   if (!a.dw_gate) return hipSuccess;
   p = sizes(a.hidden, a.dim, a.rows);
   add_segments(p, operand(b.dg), n, b.x.op, n);
-  RSX_TRY(launch_store(half, kTN, p, {a.dw_gate, a.dw_gate_ld, a.weight_type, nullptr, nullptr, a.accumulate}, b.split, s));
-  p = sizes(a.hidden, a.dim, a.rows);
-  add_segments(p, operand(b.du), n, b.x.op, n);
-  RSX_TRY(launch_store(half, kTN, p, {a.dw_up, a.dw_up_ld, a.weight_type, nullptr, nullptr, a.accumulate}, b.split, s));
+  p.batch = 2;
+  p.batch_a = a.rows * b.dg.ld;
+  RSX_TRY(launch_store(half, kTN, p, {a.dw_gate, a.dw_gate_ld, a.weight_type, nullptr, nullptr, a.accumulate, a.dw_up, a.dw_up_ld}, b.split, s));
   p = sizes(a.dim, a.hidden, a.rows);
   add_segments(p, b.dout.op, n, operand(b.s), n);
   return launch_store(half, kTN, p, {a.dw_down, a.dw_down_ld, a.weight_type, nullptr, nullptr, a.accumulate}, b.split, s);

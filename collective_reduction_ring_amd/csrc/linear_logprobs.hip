@@ -102,7 +102,6 @@ struct Softmax {
     const uint32_t first = w.n0 + uniform(wave) % TILE::WN * (TILE::TN * 16);  // this wave's columns
     const bool edge = first + TILE::TN * 16 > p.n;
     RSX_LDS float* part = reinterpret_cast<RSX_LDS float*>(lds);  // [wave column][row of the tile][3]
-    __builtin_amdgcn_s_waitcnt(0);  // loads of steps past the last one
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) {

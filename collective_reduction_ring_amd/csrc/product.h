@@ -402,6 +402,8 @@ __device__ __forceinline__ void tile_product(const ProductArgs& p, const Where& 
     step(st0, st1);
     step(st1, st0);
   }
+  // Loads of steps past the last one still land in LDS: before anything else is there, and before it is another workgroup's.
+  __builtin_amdgcn_s_waitcnt(0);
 }
 
 // ------------------------------------------------------------ epilogues
@@ -433,7 +435,6 @@ __device__ __forceinline__ void staged(const Where& w, const f32x4 (&acc)[TILE::
   const uint32_t l = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
   RSX_LDS char* patch = lds + wave * (16 * COLS * 4);
   auto chunk = [&](uint32_t row, uint32_t c) { return reinterpret_cast<RSX_LDS f32x4*>(patch + row * (COLS * 4) + ((c ^ (row % CHUNKS)) * 16)); };
-  __builtin_amdgcn_s_waitcnt(0);  // loads of steps past the last one
   __syncthreads();
 #pragma nounroll
   for (int i = 0; i < N; ++i) {
@@ -605,9 +606,6 @@ __global__ __launch_bounds__(TILE::kThreads, 2) void finish_tiles(const ProductA
 typedef Tile<256, 256, 2, 4> Large;
 typedef Tile<128, 128, 2, 2> Middle;
 typedef Tile<64, 64, 2, 2> Small;
-
-// Workgroups of one launch; the largest grid anything here asks for is below 2^31.
-constexpr uint64_t kMaxTiles = 1ull << 31;
 
 // One operand: parts of a matrix with a common row stride.
 struct Operand {

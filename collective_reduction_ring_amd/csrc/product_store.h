@@ -16,14 +16,18 @@ struct StoreArgs {
   const float* add;  // fp32 [m][n] to add, or null
   const float* row;  // then a factor for each row, or null
   int accumulate;    // add what `out` holds
+  void* out2;        // the second product's of a stack of two
+  uint64_t ld2;
 };
 
 // Steps of a product of `segments` times k.
 inline uint64_t steps_of(uint64_t k, uint64_t segments) { return segments * (k == 0 ? 1 : (k + kStep - 1) / kStep); }
-inline Schedule store_schedule(uint64_t m, uint64_t n, uint64_t k, uint64_t segments) {
-  return schedule(m, n, 1, steps_of(k, segments), false, false);
+inline Schedule store_schedule(uint64_t m, uint64_t n, uint64_t k, uint64_t segments, uint64_t batch = 1) {
+  return schedule(m, n, batch, steps_of(k, segments), false, false);
 }
-inline uint64_t store_ws(uint64_t m, uint64_t n, uint64_t k, uint64_t segments) { return store_schedule(m, n, k, segments).bytes; }
+inline uint64_t store_ws(uint64_t m, uint64_t n, uint64_t k, uint64_t segments, uint64_t batch = 1) {
+  return store_schedule(m, n, k, segments, batch).bytes;
+}
 // half: the parts are fp16, else bf16.  ws: store_ws bytes.
 hipError_t launch_store(bool half, Layouts l, ProductArgs p, const StoreArgs& e, void* ws, hipStream_t s);
 
@@ -38,7 +42,8 @@ inline Parts take_parts(Arena& ws, uint64_t rows, uint64_t cols, int count) {
   return p;
 }
 inline Operand operand(const Parts& p) { return {{p.part[0], p.part[1], p.part[2]}, p.ld}; }
-inline Operand operand(const Matrix& m) { return {{m.p, nullptr, nullptr}, m.ld}; }
+// (of a single row, the stride says nothing and may be anything)
+inline Operand operand(const Matrix& m) { return {{m.p, nullptr, nullptr}, m.rows <= 1 ? m.cols : m.ld}; }
 
 // Matrices of one type to be kept as parts, zeros behind their columns: one launch.
 struct Copies {

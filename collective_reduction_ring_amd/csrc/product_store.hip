@@ -9,12 +9,14 @@ struct Store {
   template <class T, class TILE, int N>
   static __device__ __forceinline__ void run(const ProductArgs& p, const Where& w, const StoreArgs& e,
                                              const f32x4 (&acc)[TILE::TN][N], uint32_t i0, RSX_LDS char* lds) {
+    void* out = w.batch ? e.out2 : e.out;
+    const uint64_t ld = w.batch ? e.ld2 : e.ld;
     staged<TILE, false, N>(w, acc, i0, lds, [&](uint32_t m, uint32_t n, f32x8 v) {
       if (m >= p.m || n >= p.n) return;
       if (e.add) v += get<float, 8>(e.add + static_cast<uint64_t>(m) * p.n, n, p.n);
       if (e.row) v *= e.row[m];
-      if (e.accumulate) v += get_as<8>(e.type, e.out, m * e.ld, n, p.n);
-      put_as<8>(e.type, e.out, m * e.ld, n, p.n, v);
+      if (e.accumulate) v += get_as<8>(e.type, out, m * ld, n, p.n);
+      put_as<8>(e.type, out, m * ld, n, p.n, v);
     });
   }
 };
@@ -93,8 +95,7 @@ Schedule schedule(uint64_t m, uint64_t n, uint64_t batch, uint64_t steps, bool t
 
 hipError_t launch_store(bool half, Layouts l, ProductArgs p, const StoreArgs& e, void* ws, hipStream_t s) {
   if (p.m == 0 || p.n == 0) return hipSuccess;
-  p.batch = 1;
-  const Schedule c = store_schedule(p.m, p.n, p.k, p.nseg);
+  const Schedule c = store_schedule(p.m, p.n, p.k, p.nseg, p.batch);
   return half ? store<f16_t>(l, p, c, e, ws, s) : store<bf16_t>(l, p, c, e, ws, s);
 }
 
