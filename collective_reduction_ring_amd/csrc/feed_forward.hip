@@ -15,6 +15,10 @@
 // the gradient: rounded to bf16 as well, they leave the weights' gradients off by
 // 3.5e-3 (rms) where one rounding of an operand and one of the result leave 2.4e-3;
 // their way through memory costs 3% more time (8192 x 4096 x 11008).
+//
+// The time is the tile products'.  8192 x 4096 x 11008 bf16: both projections 1240 us
+// (200 of them the writes of g, u and s), down 530 (1410 TFLOP/s), ds 860 (1.26 GB
+// through its epilogue), dx 1050, a weight gradient 594 (1244 TFLOP/s).
 #include "few_rows.h"
 #include "product_store.h"
 

@@ -6,7 +6,7 @@
 // in turns of U steps; their sums meet in LDS.  (131072 x 4096 bf16: eight waves and
 // turns of four steps 185 us, 5.8 TB/s; four and eight 191, with streamed loads,
 // which fetch a cache line again for its other half, 221; sixteen and two 176, but
-// 264 with the softmax's registers.) A step is one matrix
+// 264 with the softmax's registers.)  A step is one matrix
 // instruction of 32 k (16 bits) or four of 4 k (fp32, whose products stay fp32
 // here): a lane's 16 bytes of a row are its k, in the matrix and in x alike.
 #pragma once

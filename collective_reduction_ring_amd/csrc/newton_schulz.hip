@@ -20,6 +20,10 @@
 //
 // A and B are symmetric: only tiles on and below the diagonal are multiplied,
 // and stored to both sides.
+//
+// 11008 x 4096 bf16, a step: A 560 us, B 220, X 912 (1210 TFLOP/s as multiplied); X0
+// 125 once.  Of small matrices the time is that of 17 launches, each waiting for
+// the one before: 4 of 256 x 1024 fp32 170 us.
 #include "product_store.h"
 
 namespace rsx {
@@ -262,10 +266,14 @@ hipError_t start(const NewtonSchulzArgs& a, const Space& w, uint64_t n, uint64_t
 }  // namespace
 
 uint64_t newton_schulz_ws(uint64_t batch, uint64_t rows, uint64_t cols) {
-  Arena ws(nullptr);
   const uint64_t n = rows < cols ? rows : cols, wide = rows < cols ? cols : rows;
-  plan(ws, batch, n, wide, n < kTriple ? 3 : 2);  // of any type
-  return ws.at;
+  uint64_t most = 0;  // of any type
+  for (const int parts : {2, n < kTriple ? 3 : 2}) {
+    Arena ws(nullptr);
+    plan(ws, batch, n, wide, parts);
+    most = most < ws.at ? ws.at : most;
+  }
+  return most;
 }
 
 hipError_t launch_newton_schulz(const NewtonSchulzArgs& a, hipStream_t s) {

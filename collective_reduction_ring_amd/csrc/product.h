@@ -7,9 +7,10 @@
 // the parts of values that 16 bits do not hold.  An fp32 value is the sum of
 // three bf16 values exactly, or of two fp16 values within 2^-22 of itself as
 // long as its size is known, and the product of two such sums is a few
-// products of parts at the 16-bit rate: sixteen times the rate of fp32 matrix
-// instructions on this chip, so six products of parts (bf16) still run 2.6
-// times as fast as one in fp32, and three (fp16) 5.3 times.
+// products of parts at the 16-bit rate, sixteen times the rate of fp32 matrix
+// instructions: six products of parts (bf16) by the rates 2.6 times as fast as
+// one in fp32, three (fp16) 5.3 times; as measured (1230 TFLOP/s here, 153 of the
+// library's fp32 product, 8192^3) 1.3 and 2.7 times.
 //
 // An operand is either "row" (k side by side) or "col" (m or n side by side,
 // one k row after another); a col tile is turned by the LDS's transposing
@@ -288,7 +289,14 @@ __device__ __forceinline__ Where where_of(const ProductArgs& p, uint32_t t) {
 // piece, after the second A's second piece; both are loaded again for the step
 // after the next, a quarter of the loads in each phase: loads wait for each other
 // where they start, and what waits with them is the matrix instructions behind
-// them (8192^3: 918 us with six of eight loads in one phase).
+// them (8192^3: 918 us with six of eight loads in one phase, 894 so).
+//
+// What bounds it is the chip's power: the matrix instructions are busy 71% of the
+// time at about 1.75 GHz, and what makes them busier lowers the clock.  8192^3 bf16
+// 1220 to 1250 TFLOP/s, whichever side k is on; with long k in the operators 1390 to
+// 1457.  (The library's product: 1517 with k side by side in both, 1383 in one,
+// 1194 in neither.)  Four waves of 128 x 128 each: 1091 TFLOP/s, fewer waves to
+// change over to; instructions of 32 x 32 x 16: busier, at 1.62 GHz, 5% slower.
 template <class T, class TILE, int LA, int LB, bool DUAL>
 __device__ __forceinline__ void tile_product(const ProductArgs& p, const Where& w, uint32_t begin, uint32_t end, const Stage& st0,
                                              const Stage& st1, f32x4 (&acc)[TILE::TN][TILE::TM]) {

@@ -541,3 +541,58 @@ def test_expanded_inputs_and_refusals():
         rsx.NewtonSchulz(wg.t())
     with pytest.raises(ValueError, match="overlap"):
         rsx.NewtonSchulz(wg, wg[:1].expand(56, 40))
+
+
+def block_example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "train_block.py")
+    spec = importlib.util.spec_from_file_location("train_block", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    return example
+
+
+def test_example_gradients():
+    vocab, dim, hidden, tokens = 203, 72, 136, 301
+    r = block_example().Rank(vocab, dim, hidden, tokens, seed=3, dtype=F32)
+    r.next_batch()
+    loss = r.gradients()
+    table, weight, bias, proj, wg, wu, wd = params = [p.double().requires_grad_(True) for p in r.params]
+    fn = torch.nn.functional
+    x = fn.embedding(r.tokens, table) * dim ** 0.5
+    y = fn.layer_norm(x, (dim,), weight, bias, 1e-5)
+    z = fn.linear(x + fn.linear(fn.silu(fn.linear(y, wg)) * fn.linear(y, wu), wd), proj) * dim ** -0.5
+    want = -torch.log_softmax(z, 1).gather(1, r.targets[:, None]).mean()
+    # ten operators in a row, sums of at most `tokens` values with a rounding of fp32 each
+    tol = 10 * tokens * 2.0 ** -24
+    assert abs(loss.item() - want.item()) < tol * want.item()
+    for what, a, b in zip(r.NAMES, r.grads, torch.autograd.grad(want, params)):
+        assert (a.double() - b).norm() < tol * b.norm(), what
+
+
+def test_example_runs_and_its_ranks_agree():
+    losses, world = block_example().train(ranks=3, steps=4, vocab=200, dim=64, hidden=96, tokens=500)
+    assert all(math.isfinite(v) for v in losses)
+    for r in world[1:]:
+        assert all(same_bits(p, q) for p, q in zip(r.params, world[0].params))
+        assert all(torch.isfinite(p).all() for p in r.params)
+
+
+def test_both_projections_gradients_have_strides_of_their_own():
+    """dw_gate and dw_up come from one launch: unlike strides and addresses, alone and added to."""
+    g = gen(9)
+    x, wg, wu, wd = (m.to(DEV) for m in block(g, 90, 40, 56, BF16))
+    dout = rand(g, 90, 40).to(BF16).to(DEV)
+    p = rsx.feed_forward(x, wg, wu, wd, keep=True)
+    want = rsx.feed_forward_grad(dout, x, wg, wu, wd, p.gate, p.up)
+    for accumulate in (False, True):
+        bufs = [torch.full((56, 40 + pad), math.nan, dtype=BF16, device=DEV) for pad in (3, 11)]
+        views = [bufs[0][:, 1:41], bufs[1][:, 8:48]]
+        for v in views:
+            v.zero_()
+        down = torch.zeros(40, 56, dtype=BF16, device=DEV)
+        rsx.feed_forward_grad(dout, x, wg, wu, wd, p.gate, p.up, dw_gate=views[0], dw_up=views[1], dw_down=down, accumulate=accumulate)
+        # 0 + v is v, of either sign (an exact 0 may differ in its sign)
+        assert all(torch.equal(a, b) for a, b in zip((*views, down), want[1:]))
+        assert all(torch.isnan(b).sum() == 56 * (b.shape[1] - 40) for b in bufs)
