@@ -21,7 +21,7 @@
 // A and B are symmetric: only tiles on and below the diagonal are multiplied,
 // and stored to both sides.
 //
-// 11008 x 4096 bf16, a step: A 560 us, B 220, X 912 (1210 TFLOP/s as multiplied); X0
+// 11008 x 4096 bf16, a step: A 558 us, B 211, X 911 (1210 TFLOP/s as multiplied); X0
 // 125 once.  Of small matrices the time is that of 17 launches, each waiting for
 // the one before: 4 of 256 x 1024 fp32 170 us.
 #include "product_store.h"
@@ -117,25 +117,27 @@ __global__ __launch_bounds__(256) void first_parts(const S* x, uint64_t ld, uint
   }
 }
 
-// v to (m, n ..) and to (n .., m) of a symmetric matrix.  Of a tile on the
-// diagonal the sums above it are left: their parts' products add up in another
+// A symmetric matrix of `size` rows gets v at (m, n ..), what is on and below the
+// diagonal, and then the same values at (n, m ..), what is above.  The sums above
+// the diagonal in its own tiles are left: their parts' products add up in another
 // order, and a value is written once.
-__device__ __forceinline__ void put_both(const Parts& p, uint32_t m, uint32_t n, uint32_t size, f32x8 v) {
+template <bool ABOVE>
+__device__ __forceinline__ void put_half(const Parts& p, uint32_t row, uint32_t col, uint32_t size, f32x8 v) {
   typedef Vec<f16_t, 8>::type V;
-  if (n > m || m >= size) return;
-  const uint64_t at = m * p.ld + n;
-  const bool whole = n + 7 <= m;
+  if (row >= size || (ABOVE ? col + 7 <= row || col >= size : col > row)) return;
+  const uint64_t at = row * p.ld + col;
+  const bool whole = ABOVE ? col > row && col + 7 < size : col + 7 <= row;
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
     if (i >= p.count) break;
     const V h = __builtin_convertvector(v, V);
-    f16_t* a = static_cast<f16_t*>(p.part[i]);
-    if (whole) *reinterpret_cast<V*>(a + at) = h;
+    f16_t* a = static_cast<f16_t*>(p.part[i]) + at;
+    if (whole) {
+      *reinterpret_cast<V*>(a) = h;
+    } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (n + e > m) break;
-      if (!whole) a[at + e] = h[e];
-      if (n + e < m) a[(n + e) * p.ld + m] = h[e];
+      for (int e = 0; e < 8; ++e)
+        if (ABOVE ? col + e > row && col + e < size : col + e <= row) a[e] = h[e];
     }
     const f32x8 back = __builtin_convertvector(h, f32x8);
 #pragma unroll
@@ -152,7 +154,14 @@ struct Gram {
   static __device__ __forceinline__ void run(const ProductArgs& p, const Where& w, const GramArgs& e,
                                              const f32x4 (&acc)[TILE::TN][N], uint32_t i0, RSX_LDS char* lds) {
     const Parts to = e.to.at(w.batch);
-    staged<TILE, false, N>(w, acc, i0, lds, [&](uint32_t m, uint32_t n, f32x8 v) { put_both(to, m, n, p.m, v * kUnscale); });
+    staged<TILE, false, N>(
+        w, acc, i0, lds,
+        [&](uint32_t m, uint32_t n, f32x8 v) {
+          v *= kUnscale;
+          put_half<false>(to, m, n, p.m, v);
+          return v;
+        },
+        [&](uint32_t m, uint32_t n, f32x8 v) { put_half<true>(to, n, m, p.m, v); });
   }
 };
 
@@ -166,11 +175,16 @@ struct Poly {
   static __device__ __forceinline__ void run(const ProductArgs& p, const Where& w, const PolyArgs& e,
                                              const f32x4 (&acc)[TILE::TN][N], uint32_t i0, RSX_LDS char* lds) {
     const Parts gram = e.gram.at(w.batch), to = e.to.at(w.batch);
-    staged<TILE, false, N>(w, acc, i0, lds, [&](uint32_t m, uint32_t n, f32x8 v) {
-      if (m >= p.m || n > m) return;
-      const f32x8 g = get_parts<f16_t, 8>(gram, m, n);  // rows are filled to 8
-      put_both(to, m, n, p.m, g * e.b + v * (e.c * kUnscale));
-    });
+    staged<TILE, false, N>(
+        w, acc, i0, lds,
+        [&](uint32_t m, uint32_t n, f32x8 v) {
+          if (m >= p.m || n > m) return v;
+          const f32x8 g = get_parts<f16_t, 8>(gram, m, n);  // rows are filled to 8
+          v = g * e.b + v * (e.c * kUnscale);
+          put_half<false>(to, m, n, p.m, v);
+          return v;
+        },
+        [&](uint32_t m, uint32_t n, f32x8 v) { put_half<true>(to, n, m, p.m, v); });
   }
 };
 
@@ -188,19 +202,23 @@ struct Apply {
                                              const f32x4 (&acc)[TILE::TN][N], uint32_t i0, RSX_LDS char* lds) {
     const Parts x = e.x.at(w.batch), to = e.to.at(w.batch);
     const uint64_t first = w.batch * e.each;
-    staged<TILE, false, N>(w, acc, i0, lds, [&](uint32_t m, uint32_t n, f32x8 sum) {
-      if (m >= p.m || n >= ((p.n + 7) & ~7u)) return;
-      const f32x8 v = get_parts<f16_t, 8>(x, m, n) * e.a + sum * kUnscale;
-      if (e.out == nullptr) {
-        put_parts<f16_t, 8>(to, m, n, p.n, v);
-      } else if (!e.tall) {
-        if (n < p.n) put_as<8>(e.type, e.out, first + m * e.ld, n, p.n, v * kUnscale);
-      } else {
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (n + q < p.n) put_as<1>(e.type, e.out, first + (n + q) * e.ld, m, m + 1, typename Vec<float, 1>::type{v[q] * kUnscale});
-      }
-    });
+    staged<TILE, false, N>(
+        w, acc, i0, lds,
+        [&](uint32_t m, uint32_t n, f32x8 v) {
+          if (m >= p.m || n >= ((p.n + 7) & ~7u)) return v;
+          v = get_parts<f16_t, 8>(x, m, n) * e.a + v * kUnscale;
+          if (e.out == nullptr) {
+            put_parts<f16_t, 8>(to, m, n, p.n, v);
+          } else {
+            v *= kUnscale;
+            if (!e.tall && n < p.n) put_as<8>(e.type, e.out, first + m * e.ld, n, p.n, v);
+          }
+          return v;
+        },
+        [&](uint32_t m, uint32_t n, f32x8 v) {
+          if (m < p.m && n < p.n) put_as<8>(e.type, e.out, first + n * e.ld, m, p.m, v);
+        },
+        e.out != nullptr && e.tall);
   }
 };
 
