@@ -11,7 +11,8 @@
 // transposed in memory.
 //
 // What is rounded: s (and dg, du) to the matrices' type, as the next product's
-// operand; in fp32 they are kept whole, as three bf16 parts.  g and u stay fp32 for
+// operand (in two parts of it, where the result has few values); in fp32 they are
+// kept whole, as three bf16 parts.  g and u stay fp32 for
 // the gradient: rounded to bf16 as well, they leave the weights' gradients off by
 // 3.5e-3 (rms) where one rounding of an operand and one of the result leave 2.4e-3;
 // their way through memory costs 3% more time (8192 x 4096 x 11008).
@@ -195,9 +196,15 @@ __global__ __launch_bounds__(256) void few_add(const float* sums, uint32_t cuts,
 // place are faster there from 33 rows on (4096 x 11008 bf16: 83 us for 32 rows and
 // 94 for 33 to 128 in tiles, 122 for 64 here); others would be copied first.
 bool few_form(const FeedForwardArgs& a) { return a.rows <= (a.type == RSX_FLOAT32 || a.copies ? kFewRows : 32); }
-// Bytes of act(g) * u in the few-row form.
+// Bytes of s in the few-row form: fp32, or two parts.
 uint64_t few_product_bytes(const FeedForwardArgs& a) { return (a.rows * copy_ld(a.hidden) * 4 + 255) & ~255ull; }
 
+// Parts of s.  A result of few values has no crowd of roundings to even out what one
+// of s adds to them: below kWhole values s has two parts (rms 1.6e-3 for 2.4e-3 of 5 x
+// 270 bf16, as far off as the rounded result must be).  Everywhere, they would cost 8
+// rows of 4096 64 us for 55.5, whose first operand's reads double, and tiles a third.
+constexpr uint64_t kWhole = 1 << 14;
+int product_parts(const FeedForwardArgs& a) { return a.type == RSX_FLOAT32 ? 3 : a.rows * a.dim < kWhole ? 2 : 1; }
 // Parts of a matrix of `type` as an operand: fp32 is three bf16 values exactly.
 int parts_of(int type) { return type == RSX_FLOAT32 ? 3 : 1; }
 
@@ -226,17 +233,23 @@ uint32_t few_cuts(uint64_t dim, uint64_t hidden) {
 
 template <class T>
 hipError_t few(const FeedForwardArgs& a, void* s, hipStream_t stream) {
-  GateArgs e = {{{s, nullptr, nullptr}, copy_ld(a.hidden), 1}, static_cast<float*>(s), a.gate, a.up, a.act};
+  const uint64_t rest = a.rows * copy_ld(a.hidden);
+  GateArgs e = {{{s, static_cast<char*>(s) + rest * 2, nullptr}, copy_ld(a.hidden), product_parts(a)}, static_cast<float*>(s), a.gate, a.up, a.act};
   FewArgs p = {a.x.p, a.w_gate.p, a.w_up.p, a.x.ld, a.w_gate.ld, a.w_up.ld, static_cast<uint32_t>(a.rows),
                static_cast<uint32_t>(a.hidden), static_cast<uint32_t>(a.dim)};
   if (a.hidden) RSX_TRY((launch_few<T, 1, true, Gate>(p, e, stream)));
   p = {s, a.w_down.p, nullptr, sizeof(T) == 4 ? a.hidden : copy_ld(a.hidden), a.w_down.ld, 0, static_cast<uint32_t>(a.rows),
-       static_cast<uint32_t>(a.dim), static_cast<uint32_t>(a.hidden)};
+       static_cast<uint32_t>(a.dim), static_cast<uint32_t>(a.hidden), 0, rest};
   const uint32_t cuts = few_cuts(a.dim, a.hidden);
-  if (cuts == 1) return launch_few<T, 1, false, FewStore>(p, {a.out, a.out_ld, a.type, nullptr, nullptr, 0}, stream);
+  constexpr bool CAN = sizeof(T) == 2;
+  const bool two = CAN && product_parts(a) == 2;
+  if (cuts == 1) {
+    const StoreArgs to = {a.out, a.out_ld, a.type, nullptr, nullptr, 0};
+    return two ? launch_few<T, 1, false, FewStore, CAN>(p, to, stream) : launch_few<T, 1, false, FewStore>(p, to, stream);
+  }
   float* sums = reinterpret_cast<float*>(static_cast<char*>(s) + few_product_bytes(a));
   p.cuts = cuts;
-  RSX_TRY((launch_few<T, 1, false, FewSums>(p, {sums}, stream)));
+  RSX_TRY((two ? launch_few<T, 1, false, FewSums, CAN>(p, {sums}, stream) : launch_few<T, 1, false, FewSums>(p, {sums}, stream)));
   return launch(few_add, grid_of((a.rows * a.dim + 255) / 256), 256, 0, stream, sums, cuts, static_cast<uint32_t>(a.rows),
                 static_cast<uint32_t>(a.dim), a.out, a.out_ld, a.type);
 }
@@ -255,8 +268,9 @@ Forward plan(const FeedForwardArgs& a, Arena& ws) {
   f.wg = take_operand(ws, a.w_gate, a.type, n, half, a.copies);
   f.wu = take_operand(ws, a.w_up, a.type, n, half, a.copies);
   f.wd = take_operand(ws, a.w_down, a.type, n, half, a.copies);
-  f.s = take_parts(ws, a.rows, a.hidden, n);
-  const uint64_t segs = segments_of(n, n), split = store_ws(a.rows, a.dim, a.hidden, segs);
+  const int ns = product_parts(a);
+  f.s = take_parts(ws, a.rows, a.hidden, ns);
+  const uint64_t segs = segments_of(n, n), split = store_ws(a.rows, a.dim, a.hidden, segments_of(ns, n));
   f.gate = schedule(a.rows, 2 * a.hidden, 1, steps_of(a.dim, segs), false, false);
   f.split = ws.take(split > f.gate.bytes ? split : f.gate.bytes);
   return f;
@@ -340,7 +354,7 @@ hipError_t launch_feed_forward(const FeedForwardArgs& a, hipStream_t s) {
   RSX_TRY((half ? launch_product<f16_t, kRow, kRow, true, false, Gate>(p, f.gate, f.split, e, s)
                 : launch_product<bf16_t, kRow, kRow, true, false, Gate>(p, f.gate, f.split, e, s)));
   p = sizes(a.rows, a.dim, a.hidden);
-  add_segments(p, operand(f.s), n, f.wd.op, n);
+  add_segments(p, operand(f.s), product_parts(a), f.wd.op, n);
   return launch_store(half, kNT, p, {a.out, a.out_ld, a.type, nullptr, nullptr, 0}, f.split, s);
 }
 

@@ -22,6 +22,7 @@ struct FewArgs {
   uint64_t ldx, ldw, ldw2;
   uint32_t n, rows, k;  // rows of x, of the matrix; length of either
   uint32_t cuts;        // workgroups that share a group of rows' k; 0 is 1
+  uint64_t rest;        // SPLIT: elements from x to its second part, which is multiplied as well
 };
 // Which of them this one is.
 __device__ __forceinline__ uint32_t few_cut(const FewArgs& p) { return p.cuts ? static_cast<uint32_t>(block_id() % p.cuts) : 0; }
@@ -44,10 +45,10 @@ __device__ __forceinline__ f32x4 few_mma(FewFrag<f16_t>::type w, FewFrag<f16_t>:
 
 // v[g][t] for the waves t mod kFewWaves: lane l has x row 16 t + l % 16 and matrix
 // rows first + 16 g + 4 (l / 16) .. + 3 (g from RG on: the second matrix's).
-template <class T, int NT, int RG, bool DUAL, class EPILOGUE>
+template <class T, int NT, int RG, bool DUAL, bool SPLIT, class EPILOGUE>
 __global__ __launch_bounds__(64 * kFewWaves, 4) void few_rows_kernel(const FewArgs p, const typename EPILOGUE::Args e) {
-  constexpr int NM = DUAL ? 2 * RG : RG, N = FewFrag<T>::N, S = 4 * N;
-  constexpr int U = NM + NT <= 5 ? 4 : 2;  // a turn's loads in registers: 80 at most, beside the sums
+  constexpr int NM = DUAL ? 2 * RG : RG, N = FewFrag<T>::N, S = 4 * N, NX = SPLIT ? 2 * NT : NT;
+  constexpr int U = NM + NX <= 5 ? 4 : NM + NX <= 8 ? 2 : 1;  // a turn's loads in registers: 80 at most, beside the sums
   typedef typename FewFrag<T>::type V;
   __shared__ f32x4 sums[kFewWaves][NM][NT][64];
   const uint32_t l = threadIdx.x % 64, wave = uniform(threadIdx.x / 64), r = l % 16, g = l / 16;
@@ -56,14 +57,15 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void few_rows_kernel(const FewAr
   if (group * (16 * RG) >= p.rows) return;
   const uint32_t first = static_cast<uint32_t>(group) * (16 * RG);
   const T* wr[NM];
-  const T* xr[NT];
+  const T* xr[NX];
 #pragma unroll
   for (int m = 0; m < NM; ++m) {
     const uint64_t row = min(first + m % RG * 16 + r, p.rows - 1);
     wr[m] = (m < RG ? static_cast<const T*>(p.w) + row * p.ldw : static_cast<const T*>(p.w2) + row * p.ldw2) + g * N;
   }
 #pragma unroll
-  for (int t = 0; t < NT; ++t) xr[t] = static_cast<const T*>(p.x) + static_cast<uint64_t>(min(t * 16 + r, p.n - 1)) * p.ldx + g * N;
+  for (int t = 0; t < NX; ++t)
+    xr[t] = static_cast<const T*>(p.x) + (t < NT ? 0 : p.rest) + static_cast<uint64_t>(min(t % NT * 16 + r, p.n - 1)) * p.ldx + g * N;
   f32x4 acc[NM][NT];
 #pragma unroll
   for (int m = 0; m < NM; ++m)
@@ -78,13 +80,13 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void few_rows_kernel(const FewAr
   for (uint32_t i = 0; i < mine; ++i) {
     const uint32_t turn = me + at * all;
     at = at + 1 < mine ? at + 1 : 0;
-    V w[U][NM], x[U][NT];
+    V w[U][NM], x[U][NX];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
 #pragma unroll
       for (int m = 0; m < NM; ++m) w[u][m] = load_kept<T, N>(wr[m] + (turn * U + u) * S);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) x[u][t] = load_kept<T, N>(xr[t] + (turn * U + u) * S);
+      for (int t = 0; t < NX; ++t) x[u][t] = load_kept<T, N>(xr[t] + (turn * U + u) * S);
     }
     __builtin_amdgcn_sched_barrier(0);  // a turn's loads are all on their way before the first is waited for
 #pragma unroll
@@ -92,19 +94,19 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void few_rows_kernel(const FewAr
 #pragma unroll
       for (int m = 0; m < NM; ++m)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) acc[m][t] = few_mma(w[u][m], x[u][t], acc[m][t]);
+        for (int t = 0; t < NX; ++t) acc[m][t % NT] = few_mma(w[u][m], x[u][t], acc[m][t % NT]);
   }
   for (uint32_t step = turns * U + me; step * S < p.k; step += all) {
     // what is left of a row, element by element where it ends in a lane's 16 bytes
     const uint32_t k = step * S + g * N;
-    V x[NT];
+    V x[NX];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) x[t] = load_row<T, N, false>(xr[t] - g * N, k, p.k);
+    for (int t = 0; t < NX; ++t) x[t] = load_row<T, N, false>(xr[t] - g * N, k, p.k);
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
       const V w = load_row<T, N, false>(wr[m] - g * N, k, p.k);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) acc[m][t] = few_mma(w, x[t], acc[m][t]);
+      for (int t = 0; t < NX; ++t) acc[m][t % NT] = few_mma(w, x[t], acc[m][t % NT]);
     }
   }
 #pragma unroll
@@ -124,12 +126,12 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void few_rows_kernel(const FewAr
   }
 }
 
-template <class T, int RG, bool DUAL, class EPILOGUE>
+template <class T, int RG, bool DUAL, class EPILOGUE, bool SPLIT = false>
 hipError_t launch_few(const FewArgs& p, const typename EPILOGUE::Args& e, hipStream_t s) {
   const dim3 grid = grid_of((static_cast<uint64_t>(p.rows) + 16 * RG - 1) / (16 * RG) * (p.cuts ? p.cuts : 1));
-  if (p.n <= 16) return launch(few_rows_kernel<T, 1, RG, DUAL, EPILOGUE>, grid, 64 * kFewWaves, 0, s, p, e);
-  if (p.n <= 32) return launch(few_rows_kernel<T, 2, RG, DUAL, EPILOGUE>, grid, 64 * kFewWaves, 0, s, p, e);
-  return launch(few_rows_kernel<T, 4, RG, DUAL, EPILOGUE>, grid, 64 * kFewWaves, 0, s, p, e);
+  if (p.n <= 16) return launch(few_rows_kernel<T, 1, RG, DUAL, SPLIT, EPILOGUE>, grid, 64 * kFewWaves, 0, s, p, e);
+  if (p.n <= 32) return launch(few_rows_kernel<T, 2, RG, DUAL, SPLIT, EPILOGUE>, grid, 64 * kFewWaves, 0, s, p, e);
+  return launch(few_rows_kernel<T, 4, RG, DUAL, SPLIT, EPILOGUE>, grid, 64 * kFewWaves, 0, s, p, e);
 }
 
 }  // namespace rsx
