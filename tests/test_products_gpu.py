@@ -596,3 +596,25 @@ def test_both_projections_gradients_have_strides_of_their_own():
         # 0 + v is v, of either sign (an exact 0 may differ in its sign)
         assert all(torch.equal(a, b) for a, b in zip((*views, down), want[1:]))
         assert all(torch.isnan(b).sum() == 56 * (b.shape[1] - 40) for b in bufs)
+
+
+@pytest.mark.parametrize("rows,dim,hidden,t,act,pad,keep", [
+    # 2^14 values and more of few rows, in one part: k uncut, cut, with ends off the vectors, and just on either side
+    (8, 2056, 200, BF16, "silu", 0, True), (16, 1024, 4100, F16, "gelu", 0, False), (31, 1001, 2050, BF16, "relu", 1, False),
+    (32, 513, 2100, F16, "silu", 8, True), (16, 1023, 130, BF16, "gelu_tanh", 0, False), (33, 496, 72, BF16, "silu", 0, False),
+    (33, 497, 72, F16, "silu", 3, False), (64, 300, 2100, BF16, "gelu", 1, True)])
+def test_feed_forward_few_rows_of_many(rows, dim, hidden, t, act, pad, keep):
+    test_feed_forward(rows, dim, hidden, t, act, pad, keep)
+
+
+@pytest.mark.parametrize("rows,dim,hidden", [(5, 270, 192), (29, 24, 7101), (2, 40, 5000), (40, 300, 200), (100, 24, 1000)])
+def test_small_results_are_as_good_as_their_rounding(rows, dim, hidden):
+    say("small results", rows, dim, hidden)
+    host = block(gen(rows + dim), rows, dim, hidden, BF16)
+    out = rsx.feed_forward(*(h.to(DEV) for h in host)).out
+    # the bounds of matrices kept whole, and what two bf16 parts of s leave out: a half step of the second, 2^-9 of 2^-9
+    ref, tol = po.feed_forward(*(h.float() for h in host), "silu")
+    x, wg, wu, wd = (h.double() for h in host)
+    g = x @ wg.t()
+    s = g * torch.sigmoid(g) * (x @ wu.t())
+    fits(out, ref[0], tol[0] + 2.0 ** -17 * (s.abs() @ wd.abs().t()), BF16, "out")
