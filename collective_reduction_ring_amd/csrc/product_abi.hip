@@ -212,6 +212,8 @@ rsx_status_t rsx_newton_schulz(const void* x, size_t x_stride, size_t x_matrix, 
   if (batch > 65535 || rows >= kMaxWidth || cols >= kMaxWidth || x_matrix > kMaxSpan / es || out_matrix > kMaxSpan / es ||
       rows * cols > kMaxSpan / 4 / (batch ? batch : 1) || x_stride > kMaxSpan / es || out_stride > kMaxSpan / es)
     return RSX_ERR_UNSUPPORTED;
+  // a matrix's span is in range before it is made of rows and stride: the product may wrap
+  if (rows > 1 && (x_stride > kMaxSpan / es / rows || out_stride > kMaxSpan / es / rows)) return RSX_ERR_UNSUPPORTED;
   if (steps < 1 || !(eps >= 0.0f)) return RSX_ERR_INVALID_ARGUMENT;
   // a stack's matrices do not overlap in what is written
   const bool some = rows != 0 && cols != 0;

@@ -1,0 +1,23 @@
+"""The step's matrix products at the ends of their ranges, without a GPU.
+
+Calls with made-up addresses have to be refused before any HIP call.
+"""
+import pytest
+
+from test_abi import fake_ptrs
+from test_products import ortho
+from test_steps import A, BF16, F32, UNSUPPORTED
+
+TALL = (1 << 21) + 1
+
+
+@fake_ptrs
+@pytest.mark.parametrize("kw", [
+    # (rows - 1) * stride is 0 in 64 bits: the span of a matrix looked like that of one row
+    dict(xs=1 << 43), dict(os=1 << 43), dict(xs=1 << 43, os=1 << 43), dict(xs=1 << 44, os=1 << 44, t=BF16),
+    dict(xs=1 << 43, rows=(1 << 21) + 3), dict(os=1 << 43, batch=2, xm=TALL * 64, om=64), dict(xs=1 << 43, batch=2, xm=64, om=TALL * 64),
+    # and where nothing wraps, spans past 2^45 bytes
+    dict(xs=1 << 25), dict(os=1 << 25)], ids=str)
+def test_update_strides_whose_span_leaves_the_range(kw):
+    args = dict(rows=TALL, cols=64, xs=64, os=64, xm=0, om=0, batch=1, t=F32, out=A(100), ws=A(200), wb=1 << 40)
+    assert ortho(**{**args, **kw}) == UNSUPPORTED
