@@ -256,7 +256,7 @@ __global__ __launch_bounds__(256) void scale_rows(const S* hidden, uint64_t ld, 
   float c = row.token >= 0 ? row.dz(((part[0] + part[1]) + (part[2] + part[3])) * e.scale, true) : most;
   // (not of a NaN, which is to show)
   if (fabsf(c) < most * (row.d == 0.0f ? 0x1p-20f : 0x1p-3f)) c = most;
-  c = row.lse == -INFINITY ? 0.0f : c * e.scale;
+  c = row.lse == -INFINITY || most == 0.0f ? 0.0f : c * e.scale;  // without a gradient, a row adds nothing whatever it holds
   if (c != 0.0f && fabsf(c) < 1e-30f) c = 1e-30f;  // so that 1 / c and the parts of c h are in range
   if (threadIdx.x == 0) factor[i] = c;
   if (to.count == 0) return;
@@ -285,7 +285,7 @@ struct Dz {
       const float f = e.factor[i], by = f == 0.0f ? 0.0f : e.row.scale / f;
       const uint64_t hit = row.token >= 0 ? static_cast<uint64_t>(row.token) - e.first : ~0ull;
 #pragma unroll
-      for (int x = 0; x < 8; ++x) v[x] = row.dz(v[x] * e.row.scale, c + x == hit) * by;
+      for (int x = 0; x < 8; ++x) v[x] = f == 0.0f ? 0.0f : row.dz(v[x] * e.row.scale, c + x == hit) * by;
       put_parts<bf16_t, 8>(e.dz, i, c, p.n, v);
     });
   }

@@ -611,6 +611,9 @@ rsx_status_t rsx_linear_logprobs(const void* hidden, size_t hidden_stride, const
  * gives it (lse_rest may be null), times scale, dhidden = dz weight and
  * dweight = dz^T hidden (with `accumulate` added to what is there).  Either may
  * be null.  dweight is of dweight_type: `type` or RSX_FLOAT32.
+ * A row whose token is outside [0, vocab) or whose dlogprob is 0, and whose
+ * dentropy is 0 or null, has a gradient of 0 and adds nothing to dweight, whatever
+ * its values are: NaN and infinities of a batch's padding stay there.
  * The vocabulary is taken in pieces, of which the logits are multiplied again.
  * dz is rounded to bf16, each row by itself divided by its token's dz, and the
  * rows of hidden times that to bf16 too (fp16 matrices: either to 16 bits, with the

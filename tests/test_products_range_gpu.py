@@ -48,3 +48,34 @@ def test_nan_shows_in_every_gradient(rows, dim, hidden, t, act):
     assert torch.isnan(out[1]).all() and torch.isnan(dx[1]).all()
     assert same_bits(out[rest], clean[0][rest]) and same_bits(dx[rest], clean[1][rest])
     assert all(torch.isnan(d).all() for d in (dg, du, dd))
+
+
+@pytest.mark.parametrize("t", [BF16, F16, F32])
+@pytest.mark.parametrize("rows,vocab,dim", [(5, 300, 40), (90, 131, 72), (600, 4100, 136)])
+def test_rows_without_a_gradient_add_nothing(rows, vocab, dim, t):
+    """Padding of a batch: rows whose token is none of the vocabulary, or whose gradients are 0, whatever they hold."""
+    say("rows without a gradient", rows, vocab, dim, t)
+    g = gen(rows)
+    h, w = rand(g, rows, dim, dtype=t).to(DEV), rand(g, vocab, dim, dtype=t, scale=dim ** -0.5).to(DEV)
+    tok = torch.randint(0, vocab, (rows,), generator=g).to(DEV)
+    gl, ge = rand(g, rows).to(DEV), rand(g, rows, scale=0.1).to(DEV)
+    tok[1], tok[3] = -1, vocab
+    gl[4] = 0.0  # a loss mask
+    ge[[1, 3, 4]] = 0.0
+    h[[1, 3, 4]] = 0.0
+    for entropy in (False, True):
+        def grads():
+            p = rsx.linear_logprobs(h, w, tok)
+            return p, *rsx.linear_logprobs_grad(h, w, tok, p.lse, gl, p.entropy if entropy else None, ge if entropy else None,
+                                                lse_rest=p.lse_rest)
+        h[[1, 3, 4]] = 0.0
+        _, dh, dw = grads()
+        h[1], h[3, 2], h[4] = math.nan, math.inf, -math.inf
+        p, dh2, dw2 = grads()
+        assert torch.isnan(p.lse[1]) and torch.isfinite(dw).all()
+        assert (dh2[[1, 3, 4]] == 0).all()
+        assert torch.equal(dh, dh2) and torch.equal(dw, dw2)
+        h[0, 0] = math.nan  # a row with a gradient shows
+        _, dh3, dw3 = grads()
+        assert torch.isnan(dh3[0]).all() and torch.isnan(dw3).all()
+        h[0, 0] = 0.5
