@@ -539,10 +539,35 @@ struct Parts {
   int count;
 };
 
-// N values as their parts, rounded to nearest each: the rest of an infinity is 0, as the part says it all.
+// Part i of `count` of N values, rounded to nearest, and in v what is left of them.
+// An infinity is the last part's, which is multiplied with first parts alone, and 1 with its
+// sign is the first part: with an infinity in the first part, its products with the
+// other matrix's lower parts, which may be 0 or of the other sign, would be NaN.
+// (fp16's parts are of values within its range.)
+template <class T, int N>
+__device__ __forceinline__ typename Vec<T, N>::type take_part(typename Vec<float, N>::type& v, int i, int count) {
+  auto h = __builtin_convertvector(v, typename Vec<T, N>::type);
+  if (i + 1 >= count) return h;
+  auto back = __builtin_convertvector(h, typename Vec<float, N>::type);
+  if constexpr (__is_same(T, bf16_t)) {
+    float most = 0.0f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) most = fmaxf(most, fabsf(back[e]));
+    if (most == INFINITY) {
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (fabsf(v[e]) == INFINITY) {
+          back[e] = copysignf(i == 0 ? 1.0f : 0.0f, v[e]);
+          h[e] = static_cast<T>(back[e]);
+        }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e) v[e] = fabsf(back[e]) < INFINITY ? v[e] - back[e] : 0.0f;  // the first part of a NaN says it all
+  return h;
+}
 template <class T, int N>
 __device__ __forceinline__ void put_parts(const Parts& p, uint64_t row, uint32_t c, uint32_t n, typename Vec<float, N>::type v) {
-  typedef typename Vec<T, N>::type V;
   const uint64_t at = row * p.ld + c;
   if (p.count == 0 || c >= ((n + 7) & ~7u)) return;
 #pragma unroll
@@ -551,11 +576,7 @@ __device__ __forceinline__ void put_parts(const Parts& p, uint64_t row, uint32_t
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
     if (i >= p.count) break;
-    const V h = __builtin_convertvector(v, V);
-    *reinterpret_cast<V*>(static_cast<T*>(p.part[i]) + at) = h;
-    const auto back = __builtin_convertvector(h, typename Vec<float, N>::type);
-#pragma unroll
-    for (int e = 0; e < N; ++e) v[e] = fabsf(back[e]) < INFINITY ? v[e] - back[e] : 0.0f;
+    *reinterpret_cast<typename Vec<T, N>::type*>(static_cast<T*>(p.part[i]) + at) = take_part<T, N>(v, i, p.count);
   }
 }
 template <class T, int N>

@@ -46,11 +46,7 @@ __global__ __launch_bounds__(256) void copy_parts(const Copies c) {
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
     if (k >= to.count) break;
-    const auto h = __builtin_convertvector(v, typename Vec<T, 8>::type);
-    *reinterpret_cast<typename Vec<T, 8>::type*>(static_cast<T*>(to.part[k]) + row * to.ld + col) = h;
-    const f32x8 back = __builtin_convertvector(h, f32x8);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = fabsf(back[e]) < INFINITY ? v[e] - back[e] : 0.0f;
+    *reinterpret_cast<typename Vec<T, 8>::type*>(static_cast<T*>(to.part[k]) + row * to.ld + col) = take_part<T, 8>(v, k, to.count);
   }
 }
 

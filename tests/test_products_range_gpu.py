@@ -79,3 +79,68 @@ def test_rows_without_a_gradient_add_nothing(rows, vocab, dim, t):
         _, dh3, dw3 = grads()
         assert torch.isnan(dh3[0]).all() and torch.isnan(dw3).all()
         h[0, 0] = 0.5
+
+
+def same_kind(got, ref, what):
+    """NaN, either infinity and numbers in the same places."""
+    got = got.double()
+    assert torch.equal(torch.isnan(got), torch.isnan(ref)), what
+    for inf in (math.inf, -math.inf):
+        assert torch.equal(got == inf, ref == inf), what
+
+
+@pytest.mark.parametrize("rows,dim,hidden", [(4, 72, 88), (70, 136, 40), (300, 264, 520)])
+@pytest.mark.parametrize("where", ["x", "w_gate", "w_down", "dout"])
+def test_fp32_infinities_are_those_of_the_products(rows, dim, hidden, where):
+    """In parts too: no part of a finite value times an infinity may be a NaN or an infinity of the other sign."""
+    say("fp32 infinities", rows, dim, hidden, where)
+    g = gen(rows + 1)
+    host, dy = block(g, rows, dim, hidden, F32), rand(g, rows, dim)
+    x, wg, wu, wd = host
+    at = {"x": x, "w_gate": wg, "w_down": wd, "dout": dy}[where]
+    at[1, 5], at[2, 7] = math.inf, -math.inf
+    x[3, 5] = 0.0  # times an infinity: NaN
+    dev = [m.to(DEV) for m in host]
+    p = rsx.feed_forward(*dev, activation="relu", keep=True)
+    x, wg, wu, wd, dy64 = (m.double() for m in (*host, dy))
+    gate, up = x @ wg.t(), x @ wu.t()
+    same_kind(p.gate.cpu(), gate, "gate")
+    same_kind(p.up.cpu(), up, "up")
+    act = torch.where(gate < 0, 0.0, gate)
+    same_kind(p.out.cpu(), (act * up) @ wd.t(), "out")
+    ds = dy64 @ wd
+    dg, du = ds * up * torch.where(gate.isnan(), gate, (gate > 0).double()), ds * act
+    grads = rsx.feed_forward_grad(dy.to(DEV), *dev, p.gate, p.up, activation="relu")
+    for got, ref, what in zip(grads, (dg @ wg + du @ wu, dg.t() @ x, du.t() @ x, dy64.t() @ (act * up)), ("dx", "dw_gate", "dw_up", "dw_down")):
+        same_kind(got.cpu(), ref, what)
+
+
+@pytest.mark.parametrize("rows,vocab,dim", [(5, 200, 40), (66, 131, 24), (90, 1000, 72), (600, 4100, 136)])
+def test_fp32_masks(rows, vocab, dim):
+    """A weight of minus infinity masks its token, with few rows and with many."""
+    say("fp32 masks", rows, vocab, dim)
+    g = gen(rows + vocab)
+    h, w = rand(g, rows, dim), rand(g, vocab, dim, scale=dim ** -0.5)
+    h[:, 3] = h[:, 3].abs() + 0.1
+    masked = torch.randperm(vocab, generator=g)[:vocab // 3]
+    w[masked, 3] = -math.inf
+    tok = torch.randint(0, vocab, (rows,), generator=g)
+    tok[0] = masked[0]
+    logp = torch.log_softmax(h.double() @ w.double().t(), 1)
+    p = rsx.linear_logprobs(h.to(DEV), w.to(DEV), tok.to(DEV))
+    want = logp.gather(1, tok[:, None])[:, 0]
+    got = p.logprob.cpu().double()
+    assert torch.equal(got == -math.inf, want == -math.inf)
+    some = torch.isfinite(want)
+    # logits of size 1 from sums of `dim` products, six parts' each, with a whole step for every addition
+    assert (got - want)[some].abs().max() < 2.0 ** -23 * (6 * dim + 64) * 4
+    assert torch.isfinite(p.lse).all() and torch.isfinite(p.entropy).all()
+    gl = rand(g, rows)
+    gl[tok == masked[0]] = 0.0
+    _, dw = rsx.linear_logprobs_grad(h.to(DEV), w.to(DEV), tok.to(DEV), p.lse, gl.to(DEV), lse_rest=p.lse_rest, inputs=False)
+    assert torch.isfinite(dw).all()
+    clear = masked[~torch.isin(masked, tok)]
+    assert (dw[clear.to(DEV)] == 0).all()
+    w[:, 3] = -math.inf
+    p = rsx.linear_logprobs(h.to(DEV), w.to(DEV), tok.to(DEV))
+    assert (p.lse == -math.inf).all() and (p.logprob == -math.inf).all() and (p.entropy == 0).all()
