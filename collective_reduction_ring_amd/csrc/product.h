@@ -540,7 +540,8 @@ struct Parts {
 };
 
 // Part i of `count` of N values, rounded to nearest, and in v what is left of them.
-// An infinity is the last part's, which is multiplied with first parts alone, and 1 with its
+// A value that bf16 rounds to infinity has bf16's largest as a part.  An infinity
+// is the last part's, which is multiplied with first parts alone, and 1 with its
 // sign is the first part: with an infinity in the first part, its products with the
 // other matrix's lower parts, which may be 0 or of the other sign, would be NaN.
 // (fp16's parts are of values within its range.)
@@ -556,8 +557,8 @@ __device__ __forceinline__ typename Vec<T, N>::type take_part(typename Vec<float
     if (most == INFINITY) {
 #pragma unroll
       for (int e = 0; e < N; ++e)
-        if (fabsf(v[e]) == INFINITY) {
-          back[e] = copysignf(i == 0 ? 1.0f : 0.0f, v[e]);
+        if (fabsf(back[e]) == INFINITY) {
+          back[e] = copysignf(fabsf(v[e]) < INFINITY ? 0x1.fep127f : i == 0 ? 1.0f : 0.0f, v[e]);
           h[e] = static_cast<T>(back[e]);
         }
     }

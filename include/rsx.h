@@ -534,10 +534,9 @@ rsx_status_t rsx_token_logprobs_grad_rest(const void* logits, size_t stride, rsx
  * its loss, and the orthogonalised update.  Rows, types, aliasing, workspaces
  * and streams as above, with these differences.
  * Sums are held in fp32.  fp32 matrices are multiplied as sums of three bf16
- * values, which hold every bit of values from 2^-100 to bf16's largest; of
- * smaller ones what is below 2^-126 is lost (products of few rows: in fp32).  An
- * infinity gives what it gives in fp32.  Widths (elements of a row but the
- * vocabulary) are below 2^22.
+ * values, which hold every bit of values from 2^-100 on; of smaller ones what is
+ * below 2^-126 is lost (products of few rows: in fp32).  An infinity gives what
+ * it gives in fp32.  Widths (elements of a row but the vocabulary) are below 2^22.
  * Where a 16-bit matrix lies so that its rows are whole 16-byte chunks (address,
  * stride and width multiples of 16 bytes, no stride of 0) it is read in place;
  * from any other a copy is made in the workspace, in every call.  The

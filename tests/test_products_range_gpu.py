@@ -115,6 +115,17 @@ def test_fp32_infinities_are_those_of_the_products(rows, dim, hidden, where):
         same_kind(got.cpu(), ref, what)
 
 
+@pytest.mark.parametrize("rows", [3, 80])
+def test_fp32_values_past_the_largest_bf16_one(rows):
+    dim, hidden = 24, 40
+    x, w = torch.zeros(rows, dim, device=DEV), torch.zeros(hidden, dim, device=DEV)
+    x[:, 3] = torch.finfo(F32).max
+    x[1, 3] = -torch.finfo(F32).max
+    w[:, 3] = 2.0 ** -torch.arange(hidden, device=DEV)
+    p = rsx.feed_forward(x, w, w * 2.0 ** -60, torch.zeros(dim, hidden, device=DEV), activation="relu", keep=True)
+    assert torch.equal(p.gate, x[:, 3:4] * w[:, 3])
+
+
 @pytest.mark.parametrize("rows,vocab,dim", [(5, 200, 40), (66, 131, 24), (90, 1000, 72), (600, 4100, 136)])
 def test_fp32_masks(rows, vocab, dim):
     """A weight of minus infinity masks its token, with few rows and with many."""
