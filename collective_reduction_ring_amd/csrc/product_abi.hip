@@ -215,16 +215,17 @@ rsx_status_t rsx_newton_schulz(const void* x, size_t x_stride, size_t x_matrix, 
   // a matrix's span is in range before it is made of rows and stride: the product may wrap
   if (rows > 1 && (x_stride > kMaxSpan / es / rows || out_stride > kMaxSpan / es / rows)) return RSX_ERR_UNSUPPORTED;
   if (steps < 1 || !(eps >= 0.0f)) return RSX_ERR_INVALID_ARGUMENT;
-  // a stack's matrices do not overlap in what is written
   const bool some = rows != 0 && cols != 0;
-  if (some && batch > 1 && out_matrix < (rows - 1) * out_stride + cols) return RSX_ERR_INVALID_ARGUMENT;
   Areas m;
   if (some) {
     m.bad = x_stride < cols && x_stride != 0;
     m.bad = m.bad || out_stride < cols;
-    // one matrix of a stack is one "row" here
-    m.read(x, batch, (rows - 1) * x_stride + cols, batch > 1 ? x_matrix : (rows - 1) * x_stride + cols, es);
-    m.write(out, batch, (rows - 1) * out_stride + cols, batch > 1 ? out_matrix : (rows - 1) * out_stride + cols, es);
+    // One matrix of a stack is one "row" here; of matrices side by side, one row of all of them.
+    auto beside = [&](size_t stride, size_t each) { return each >= cols && each < (rows - 1) * stride + cols && (batch - 1) * each + cols <= stride; };
+    if (batch > 1 && beside(x_stride, x_matrix)) m.read(x, rows, (batch - 1) * x_matrix + cols, x_stride, es);
+    else m.read(x, batch, (rows - 1) * x_stride + cols, batch > 1 ? x_matrix : (rows - 1) * x_stride + cols, es);
+    if (batch > 1 && beside(out_stride, out_matrix)) m.write(out, rows, (batch - 1) * out_matrix + cols, out_stride, es);
+    else m.write(out, batch, (rows - 1) * out_stride + cols, batch > 1 ? out_matrix : (rows - 1) * out_stride + cols, es);
   }
   m.workspace(workspace, workspace_bytes, rsx_newton_schulz_workspace_size(batch, rows, cols));
   // x has been read before the first value of out is written, so they may be one

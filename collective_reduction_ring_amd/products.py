@@ -237,7 +237,8 @@ def _stack(t, what: str, output: bool = False):
     each = m.stride(0) if batch > 1 else (rows - 1) * stride + cols
     if stride < cols and not (stride == 0 and not output):
         raise ValueError(f"{what}: rows overlap")
-    if each < (rows - 1) * stride + cols and not (each == 0 and not output):
+    beside = each >= cols and (batch - 1) * each + cols <= stride  # side by side in rows of all of them
+    if each < (rows - 1) * stride + cols and not beside and not (each == 0 and not output):
         raise ValueError(f"{what}: matrices overlap")
     return batch, rows, cols, stride, each
 

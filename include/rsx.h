@@ -633,7 +633,8 @@ rsx_status_t rsx_linear_logprobs_grad(const void* hidden, size_t hidden_stride, 
 
 /*
  * Orthogonalised updates by Newton-Schulz products, of a stack of `batch`
- * matrices [rows][cols], x_matrix (out_matrix) elements from one to the next:
+ * matrices [rows][cols], x_matrix (out_matrix) elements from one to the next (one
+ * behind the other, or side by side within a row stride):
  * X = x / (|x| + eps) with the Frobenius norm |x|, then `steps` (at least 1) times
  * A = X X^T, X = a X + (b A + c A A) X; for rows > cols the same of the transpose.
  * out = X, of `type`; out == x with the same strides is allowed.

@@ -6,7 +6,7 @@ import pytest
 
 from test_abi import fake_ptrs
 from test_products import ortho
-from test_steps import A, BF16, F32, UNSUPPORTED
+from test_steps import A, ALIAS, BAD, BF16, F32, UNSUPPORTED
 
 TALL = (1 << 21) + 1
 
@@ -21,3 +21,21 @@ TALL = (1 << 21) + 1
 def test_update_strides_whose_span_leaves_the_range(kw):
     args = dict(rows=TALL, cols=64, xs=64, os=64, xm=0, om=0, batch=1, t=F32, out=A(100), ws=A(200), wb=1 << 40)
     assert ortho(**{**args, **kw}) == UNSUPPORTED
+
+
+HIP = 6  # everything was accepted, and there is no GPU
+
+
+@fake_ptrs
+@pytest.mark.parametrize("kw,want", [
+    # three matrices side by side in rows of 192 or more
+    (dict(xs=192, xm=64), HIP), (dict(os=192, om=64), HIP), (dict(xs=200, xm=66, os=192, om=64), HIP),
+    (dict(xs=192, xm=64, os=192, om=64, out=A(1)), HIP),
+    # rows that meet: the last matrix's with the first one's next, or a matrix's with the next one's
+    (dict(xs=191, xm=64), BAD), (dict(os=191, om=64), BAD), (dict(xs=192, xm=63), BAD), (dict(os=192, om=63), BAD),
+    # an output behind the input's columns, on them, and between its matrices (which is not looked at so closely)
+    (dict(xs=400, xm=64, os=400, om=64, out=A(1) + 192 * 2), HIP), (dict(xs=400, xm=64, os=400, om=64, out=A(1) + 190 * 2), ALIAS),
+    (dict(xs=400, xm=128, os=400, om=128, out=A(1) + 64 * 2), ALIAS), (dict(xs=192, xm=64, ws=A(1)), ALIAS)], ids=str)
+def test_update_of_interleaved_stacks(kw, want):
+    args = dict(batch=3, rows=100, cols=64, xm=6400, om=6400)
+    assert ortho(**{**args, **kw}) == want

@@ -155,3 +155,25 @@ def test_fp32_masks(rows, vocab, dim):
     w[:, 3] = -math.inf
     p = rsx.linear_logprobs(h.to(DEV), w.to(DEV), tok.to(DEV))
     assert (p.lse == -math.inf).all() and (p.logprob == -math.inf).all() and (p.entropy == 0).all()
+
+
+@pytest.mark.parametrize("t", [BF16, F32])
+@pytest.mark.parametrize("rows,cols,batch", [(72, 40, 3), (40, 136, 2), (300, 257, 2)])
+def test_updates_side_by_side(rows, cols, batch, t):
+    """The slices of a fused projection: matrices that lie in the same rows."""
+    say("updates side by side", rows, cols, batch, t)
+    g = gen(rows)
+    x = rand(g, batch, rows, cols, dtype=t, scale=1e-3).to(DEV)
+    want = rsx.newton_schulz(x)
+    wide = torch.full((rows, batch * cols + 5), math.nan, dtype=t, device=DEV)
+    wide[:, 3:3 + batch * cols] = x.transpose(0, 1).reshape(rows, batch * cols)
+    side = wide[:, 3:3 + batch * cols].unflatten(1, (batch, cols)).transpose(0, 1)
+    assert same_bits(rsx.newton_schulz(side), want)
+    other = torch.full_like(wide, math.nan)
+    to = other[:, 1:1 + batch * cols].unflatten(1, (batch, cols)).transpose(0, 1)
+    rsx.newton_schulz(side, to)
+    assert same_bits(to.contiguous(), want) and torch.isnan(other).sum() == 5 * rows
+    rsx.newton_schulz(side, side)
+    assert same_bits(side.contiguous(), want) and torch.isnan(wide).sum() == 5 * rows
+    with pytest.raises(ValueError, match="overlap"):
+        rsx.NewtonSchulz(wide.as_strided((batch, rows, cols), (cols - 1, batch * cols + 5, 1)))
