@@ -4,6 +4,7 @@ Calls with made-up addresses have to be refused before any HIP call.
 """
 import pytest
 
+import product_digits as pd
 from test_abi import fake_ptrs
 from test_products import ortho
 from test_steps import A, ALIAS, BAD, BF16, F32, UNSUPPORTED
@@ -39,3 +40,24 @@ HIP = 6  # everything was accepted, and there is no GPU
 def test_update_of_interleaved_stacks(kw, want):
     args = dict(batch=3, rows=100, cols=64, xm=6400, om=6400)
     assert ortho(**{**args, **kw}) == want
+
+
+def test_the_digits_bounds_find_a_lost_part():
+    """The bounds that the GPU's fp32 products have to meet pass six products of parts, and not five of them."""
+    for rows, dim, hidden, names in pd.BLOCKS:
+        if rows * dim * hidden >= 1 << 27:  # (of the others' shape, and long to multiply here)
+            continue
+        inputs = pd.block_inputs(rows, dim, hidden, names)
+        ref, bound = pd.block(*inputs, names), pd.block_bounds(rows, dim, hidden)
+        for lost in [None] + pd.SEGMENTS[1:] if rows * dim * hidden < 1 << 23 else [None, (2, 0)]:
+            got = pd.block(*inputs, names, [s for s in pd.SEGMENTS if s != lost])
+            for n in names:
+                assert (pd.off(got[n], ref[n]) > bound[n]) == (lost is not None), (rows, dim, hidden, n, lost)
+    for rows, vocab, dim, n in pd.HEADS:
+        if rows * vocab * dim >= 1 << 27:
+            continue
+        inputs = pd.head_inputs(rows, vocab, dim, n)
+        ref, bound = pd.head(*inputs, n), pd.head_bounds(rows, vocab, dim)[n]
+        for lost in [None] + pd.SEGMENTS[1:] if rows * vocab * dim < 1 << 23 else [None, (2, 0)]:
+            got = pd.head(*inputs, n, [s for s in pd.SEGMENTS if s != lost])
+            assert (pd.head_off(n, got, ref) > bound) == (lost is not None), (rows, vocab, dim, n, lost)

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import collective_reduction_ring_amd as rsx
+import product_digits as pd
 from parity_util import say
 from test_products_gpu import block
 from test_steps_gpu import BF16, DEV, F16, F32, gen, rand, same_bits
@@ -177,3 +178,33 @@ def test_updates_side_by_side(rows, cols, batch, t):
     assert same_bits(side.contiguous(), want) and torch.isnan(wide).sum() == 5 * rows
     with pytest.raises(ValueError, match="overlap"):
         rsx.NewtonSchulz(wide.as_strided((batch, rows, cols), (cols - 1, batch * cols + 5, 1)))
+
+
+@pytest.mark.parametrize("rows,dim,hidden,names", pd.BLOCKS)
+def test_fp32_block_keeps_its_digits(rows, dim, hidden, names):
+    say("fp32 digits", rows, dim, hidden, names)
+    inputs = pd.block_inputs(rows, dim, hidden, names)
+    ref, bound = pd.block(*inputs, names), pd.block_bounds(rows, dim, hidden)
+    x, wg, wu, wd, dy, gate, up = (m.to(DEV) for m in inputs)
+    p = rsx.feed_forward(x, wg, wu, wd, activation="relu", keep=True)
+    dx, dg, du, dd = rsx.feed_forward_grad(dy, x, wg, wu, wd, gate, up, activation="relu")
+    got = {"gate": p.gate, "up": p.up, "out": p.out, "dx": dx, "dw_gate": dg, "dw_up": du, "dw_down": dd}
+    for n in names:
+        far = pd.off(got[n], ref[n])
+        print(n, f"{far / pd.U:.2f} of {bound[n] / pd.U:.2f} half steps")
+        assert far <= bound[n], n
+
+
+@pytest.mark.parametrize("rows,vocab,dim,name", pd.HEADS)
+def test_fp32_head_keeps_its_digits(rows, vocab, dim, name):
+    say("fp32 digits", rows, vocab, dim, name)
+    inputs = pd.head_inputs(rows, vocab, dim, name)
+    ref, bound = pd.head(*inputs, name), pd.head_bounds(rows, vocab, dim)[name]
+    h, w, tok, gl, ge = (None if m is None else m.to(DEV) for m in inputs)
+    p = rsx.linear_logprobs(h, w, tok)
+    got = {"logprob": p.logprob}
+    if ge is not None:
+        got["dhidden"], got["dweight"] = rsx.linear_logprobs_grad(h, w, tok, p.lse, gl, p.entropy, ge, lse_rest=p.lse_rest)
+    far = pd.head_off(name, got[name], ref)
+    print(f"{far / pd.U:.2f} of {bound / pd.U:.2f} half steps")
+    assert far <= bound
