@@ -11,9 +11,8 @@
 // transposed in memory.
 //
 // What is rounded: s (and dg, du) to the matrices' type, as the next product's
-// operand (in two parts of it, where the result has few values); in fp32 they are
-// kept whole, as three bf16 parts.  g and u stay fp32 for
-// the gradient: rounded to bf16 as well, they leave the weights' gradients off by
+// operand (s in two parts of it, where the result is narrow); in fp32 they are kept
+// whole, as three bf16 parts.  g and u stay fp32 for the gradient: rounded to bf16 as well, they leave the weights' gradients off by
 // 3.5e-3 (rms) where one rounding of an operand and one of the result leave 2.4e-3;
 // their way through memory costs 3% more time (8192 x 4096 x 11008).
 //
@@ -200,12 +199,16 @@ bool few_form(const FeedForwardArgs& a) { return a.rows <= (a.type == RSX_FLOAT3
 // Bytes of s in the few-row form: fp32, or two parts.
 uint64_t few_product_bytes(const FeedForwardArgs& a) { return (a.rows * copy_ld(a.hidden) * 4 + 255) & ~255ull; }
 
-// Parts of s.  A result of few values has no crowd of roundings to even out what one
-// of s adds to them: below kWhole values s has two parts (rms 1.6e-3 for 2.4e-3 of 5 x
-// 270 bf16, as far off as the rounded result must be).  Everywhere, they would cost 8
-// rows of 4096 64 us for 55.5, whose first operand's reads double, and tiles a third.
-constexpr uint64_t kWhole = 1 << 14;
-int product_parts(const FeedForwardArgs& a) { return a.type == RSX_FLOAT32 ? 3 : a.rows * a.dim < kWhole ? 2 : 1; }
+// Parts of s.  Rounded once to 16 bits, it leaves a bf16 result of any size off by
+// 2.35e-3 (rms), in two parts by 1.66e-3, which is the result's own rounding.  The
+// second part doubles the down product's operations, or the reads of s with few
+// rows: for results narrower than kNarrow 0.2 to 5 us up to 1024 rows and 5 to 11
+// with 8192 (256 x 1024: 7.4 us for 7.2 with one row, 23 for 21, 44 for 33), for wide
+// ones up to a third of the time (1024 x 4096: 258 us for 193 with 8192 rows; 4096 x
+// 11008: 64 for 55.7 with 8, 2120 for 1590).  How many rows a call has plays no part:
+// a row has the same digits in any.
+constexpr uint64_t kNarrow = 512;
+int product_parts(const FeedForwardArgs& a) { return a.type == RSX_FLOAT32 ? 3 : a.dim < kNarrow ? 2 : 1; }
 // Parts of a matrix of `type` as an operand: fp32 is three bf16 values exactly.
 int parts_of(int type) { return type == RSX_FLOAT32 ? 3 : 1; }
 

@@ -558,7 +558,10 @@ typedef enum {
  * Gated feed-forward block: with g = x w_gate^T and u = x w_up^T,
  * out = (act(g) * u) w_down^T.
  * x, out: [rows][dim]; w_gate, w_up: [hidden][dim]; w_down: [dim][hidden].
- * gate, up: [rows][hidden] fp32, dense: g and u for the gradient; or both null.  act(g) * u is rounded to `type` (fp32: kept whole) between the products.
+ * gate, up: [rows][hidden] fp32, dense: g and u for the gradient; or both null.
+ * Between the products act(g) * u is rounded to `type` (fp16: infinite beyond 65504),
+ * or, where dim is below 512, to the sum of two values of it, with which an infinity
+ * in w_down may give a NaN; fp32: kept whole.
  * out overlaps nothing that is read.
  */
 size_t rsx_feed_forward_workspace_size(size_t rows, size_t dim, size_t hidden, rsx_dtype_t type,
@@ -576,8 +579,9 @@ rsx_status_t rsx_feed_forward(const void* x, size_t x_stride, const void* w_gate
  * dx = dg w_gate + du w_up, dw_gate = dg^T x, dw_up = du^T x and
  * dw_down = dout^T (act(gate) * up), the three added to what is there with
  * `accumulate`.  dx may be null, and so may the three dw together.
- * dg, du and act(gate) * up are rounded to `type` (fp32: kept whole).  The dw are
- * of weight_grad_type: `type` or RSX_FLOAT32.
+ * dg, du and act(gate) * up are rounded to `type` (fp32: kept whole; fp16 keeps
+ * nothing below 2^-25 or beyond 65504, so dout is to be scaled to its range).  The
+ * dw are of weight_grad_type: `type` or RSX_FLOAT32.
  */
 size_t rsx_feed_forward_grad_workspace_size(size_t rows, size_t dim, size_t hidden,
                                             rsx_dtype_t type, int copies);

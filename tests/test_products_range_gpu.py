@@ -208,3 +208,26 @@ def test_fp32_head_keeps_its_digits(rows, vocab, dim, name):
     far = pd.head_off(name, got[name], ref)
     print(f"{far / pd.U:.2f} of {bound / pd.U:.2f} half steps")
     assert far <= bound
+
+
+@pytest.mark.parametrize("t", [BF16, F16])
+@pytest.mark.parametrize("dim,hidden", [(4096, 264), (1024, 4100), (264, 520), (40, 5000), (511, 72), (512, 72)])
+def test_a_row_has_the_same_digits_in_any_call(dim, hidden, t):
+    """How an operand is rounded does not depend on how many rows share the call."""
+    say("same digits", dim, hidden, t)
+    g = gen(dim)
+    x, wg, wu, wd = (m.to(DEV) for m in block(g, 300, dim, hidden, t))
+    few = rsx.feed_forward(x[:16], wg, wu, wd).out
+    for rows in (1, 2, 3, 4, 7, 15):
+        assert same_bits(rsx.feed_forward(x[:rows], wg, wu, wd).out, few[:rows]), rows
+    # sums of another order, 64 bits' results of the two rules for s
+    g64, u64, wd64 = x.double() @ wg.double().t(), x.double() @ wu.double().t(), wd.double()
+    s = g64 * torch.sigmoid(g64) * u64
+    whole, once = s @ wd64.t(), s.to(t).double() @ wd64.t()
+    rounding = (whole.to(t).double() - whole).square().mean().sqrt()
+    for rows in (16, 40, 300):
+        off = (rsx.feed_forward(x[:rows], wg, wu, wd).out.double() - whole[:rows]).square().mean().sqrt()
+        apart = (once - whole)[:rows].square().mean().sqrt()
+        # two parts leave the result's rounding, one adds its own; a tenth for what is random in either
+        want = rounding if dim < 512 else torch.hypot(rounding, apart)
+        assert 0.9 * want < off < 1.1 * want, rows
