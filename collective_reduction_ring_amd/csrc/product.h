@@ -539,33 +539,43 @@ struct Parts {
   int count;
 };
 
-// Part i of `count` of N values, rounded to nearest, and in v what is left of them.
+// N values as `count` parts, rounded to nearest each, by f(which, part).
 // A value that bf16 rounds to infinity has bf16's largest as a part.  An infinity
 // is the last part's, which is multiplied with first parts alone, and 1 with its
 // sign is the first part: with an infinity in the first part, its products with the
 // other matrix's lower parts, which may be 0 or of the other sign, would be NaN.
 // (fp16's parts are of values within its range.)
-template <class T, int N>
-__device__ __forceinline__ typename Vec<T, N>::type take_part(typename Vec<float, N>::type& v, int i, int count) {
-  auto h = __builtin_convertvector(v, typename Vec<T, N>::type);
-  if (i + 1 >= count) return h;
-  auto back = __builtin_convertvector(h, typename Vec<float, N>::type);
-  if constexpr (__is_same(T, bf16_t)) {
+template <class T, int N, class F>
+__device__ __forceinline__ void take_parts(typename Vec<float, N>::type v, int count, F f) {
+  typedef typename Vec<T, N>::type V;
+  typedef typename Vec<float, N>::type W;
+  if (__is_same(T, bf16_t) && count > 1) {
     float most = 0.0f;
 #pragma unroll
-    for (int e = 0; e < N; ++e) most = fmaxf(most, fabsf(back[e]));
-    if (most == INFINITY) {
+    for (int e = 0; e < N; ++e) most = fmaxf(most, fabsf(v[e]));
+    if (most >= 0x1.ffp127f) {
+#pragma nounroll
+      for (int i = 0; i < count; ++i) {
+        W back = __builtin_convertvector(__builtin_convertvector(v, V), W);
 #pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (fabsf(back[e]) == INFINITY) {
-          back[e] = copysignf(fabsf(v[e]) < INFINITY ? 0x1.fep127f : i == 0 ? 1.0f : 0.0f, v[e]);
-          h[e] = static_cast<T>(back[e]);
-        }
+        for (int e = 0; e < N; ++e)
+          if (i + 1 < count && fabsf(back[e]) == INFINITY)
+            back[e] = copysignf(fabsf(v[e]) < INFINITY ? 0x1.fep127f : i == 0 ? 1.0f : 0.0f, v[e]);
+        f(i, __builtin_convertvector(back, V));
+        v -= back;
+      }
+      return;
     }
   }
 #pragma unroll
-  for (int e = 0; e < N; ++e) v[e] = fabsf(back[e]) < INFINITY ? v[e] - back[e] : 0.0f;  // the first part of a NaN says it all
-  return h;
+  for (int i = 0; i < 3; ++i) {
+    if (i >= count) break;
+    const V h = __builtin_convertvector(v, V);
+    f(i, h);
+    const W back = __builtin_convertvector(h, W);
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = __is_same(T, bf16_t) || fabsf(back[e]) < INFINITY ? v[e] - back[e] : 0.0f;
+  }
 }
 template <class T, int N>
 __device__ __forceinline__ void put_parts(const Parts& p, uint64_t row, uint32_t c, uint32_t n, typename Vec<float, N>::type v) {
@@ -574,11 +584,9 @@ __device__ __forceinline__ void put_parts(const Parts& p, uint64_t row, uint32_t
 #pragma unroll
   for (int e = 0; e < N; ++e)
     if (c + e >= n) v[e] = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    if (i >= p.count) break;
-    *reinterpret_cast<typename Vec<T, N>::type*>(static_cast<T*>(p.part[i]) + at) = take_part<T, N>(v, i, p.count);
-  }
+  take_parts<T, N>(v, p.count, [&](int i, typename Vec<T, N>::type h) {
+    *reinterpret_cast<typename Vec<T, N>::type*>(static_cast<T*>(i == 0 ? p.part[0] : i == 1 ? p.part[1] : p.part[2]) + at) = h;
+  });
 }
 template <class T, int N>
 __device__ __forceinline__ typename Vec<float, N>::type get_parts(const Parts& p, uint64_t row, uint32_t c) {

@@ -43,11 +43,9 @@ __global__ __launch_bounds__(256) void copy_parts(const Copies c) {
   const uint32_t col = static_cast<uint32_t>(id % groups * kStretch) + threadIdx.x * 8;
   if (col >= to.ld) return;
   f32x8 v = __builtin_convertvector((load_row<S, 8, false>(static_cast<const S*>(from.p) + row * from.ld, col, static_cast<uint32_t>(from.cols))), f32x8);
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    if (k >= to.count) break;
-    *reinterpret_cast<typename Vec<T, 8>::type*>(static_cast<T*>(to.part[k]) + row * to.ld + col) = take_part<T, 8>(v, k, to.count);
-  }
+  take_parts<T, 8>(v, to.count, [&](int k, typename Vec<T, 8>::type h) {
+    *reinterpret_cast<typename Vec<T, 8>::type*>(static_cast<T*>(k == 0 ? to.part[0] : k == 1 ? to.part[1] : to.part[2]) + row * to.ld + col) = h;
+  });
 }
 
 }  // namespace
