@@ -281,11 +281,12 @@ struct Dz {
                                              const f32x4 (&acc)[TILE::TN][N], uint32_t i0, RSX_LDS char* lds) {
     staged<TILE, false, N>(w, acc, i0, lds, [&](uint32_t i, uint32_t c, f32x8 v) {
       if (i >= p.m) return;
-      const Row row(e.row, i);
+      Row row(e.row, i);
       const float f = e.factor[i], by = f == 0.0f ? 0.0f : e.row.scale / f;
+      if (f == 0.0f) row.lse = -INFINITY;  // a row without a gradient, whatever it holds
       const uint64_t hit = row.token >= 0 ? static_cast<uint64_t>(row.token) - e.first : ~0ull;
 #pragma unroll
-      for (int x = 0; x < 8; ++x) v[x] = f == 0.0f ? 0.0f : row.dz(v[x] * e.row.scale, c + x == hit) * by;
+      for (int x = 0; x < 8; ++x) v[x] = row.dz(v[x] * e.row.scale, c + x == hit) * by;
       put_parts<bf16_t, 8>(e.dz, i, c, p.n, v);
     });
   }
