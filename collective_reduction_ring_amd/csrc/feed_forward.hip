@@ -39,8 +39,8 @@ struct Logistic {
   float p, rest;
 };
 __device__ __forceinline__ Logistic logistic(float z) {
-  // exp(-104) is below the smallest number; of a NaN, all of it is NaN (fmaxf would take the number)
-  const float a = -fabsf(z) < -104.0f ? -104.0f : -fabsf(z), t = a * 1.44269504f;
+  // exp(-104) is below the smallest number; the maximum of a NaN is NaN (fmaxf's would be the number)
+  const float a = __builtin_elementwise_maximum(-fabsf(z), -104.0f), t = a * 1.44269504f;
   const float lost = fmaf(a, 1.44269504f, -t) + a * 1.92596299e-8f;  // log2 e is the sum of the two
   const float e = __builtin_amdgcn_exp2f(t), x = fmaf(e, lost * 0.693147181f, e);
   const float large = __builtin_amdgcn_rcpf(1.0f + x), small = x * large;
