@@ -291,8 +291,8 @@ __device__ __forceinline__ Where where_of(const ProductArgs& p, uint32_t t) {
 // where they start, and what waits with them is the matrix instructions behind
 // them (8192^3: 918 us with six of eight loads in one phase, 894 so).
 //
-// What bounds it is the chip's power: the matrix instructions are busy 71% of the
-// time at about 1.75 GHz, and what makes them busier lowers the clock.  8192^3 bf16
+// The matrix instructions are busy 71% of the time at about 1.75 GHz, and what makes
+// them busier lowers the clock (the library's product: 87% at 1.55 GHz).  8192^3 bf16
 // 1220 to 1250 TFLOP/s, whichever side k is on; with long k in the operators 1390 to
 // 1457.  (The library's product: 1517 with k side by side in both, 1383 in one,
 // 1194 in neither.)  Four waves of 128 x 128 each: 1091 TFLOP/s, fewer waves to

@@ -618,7 +618,9 @@ rsx_status_t rsx_linear_logprobs(const void* hidden, size_t hidden_stride, const
  * A row whose token is outside [0, vocab) or whose dlogprob is 0, and whose
  * dentropy is 0 or null, has a gradient of 0 and adds nothing to dweight, whatever
  * its values are: NaN and infinities of a batch's padding stay there.
- * The vocabulary is taken in pieces, of which the logits are multiplied again.
+ * The vocabulary is taken in pieces of 4096 to 2^20 columns, of which the logits
+ * are multiplied again; the workspace has dz of all rows for one of them, 2, 4
+ * (fp16) or 6 (fp32) bytes each.
  * dz is rounded to bf16, each row by itself divided by its token's dz, and the
  * rows of hidden times that to bf16 too (fp16 matrices: either to 16 bits, with the
  * range of fp32; fp32: kept whole).
@@ -642,10 +644,11 @@ rsx_status_t rsx_linear_logprobs_grad(const void* hidden, size_t hidden_stride, 
  * X = x / (|x| + eps) with the Frobenius norm |x|, then `steps` (at least 1) times
  * A = X X^T, X = a X + (b A + c A A) X; for rows > cols the same of the transpose.
  * out = X, of `type`; out == x with the same strides is allowed.
- * X, A and b A + c A A are held to 22 bits and products summed in fp32 (of a
- * bf16 update's last step, the products are of 11 bits); their
- * values may not pass 16 (the singular values of X begin at 1 or less, and stay
- * below 1.3 with the usual coefficients 3.4445, -4.775, 2.0315).
+ * X, A and b A + c A A are held to 22 bits (of an fp32 update whose smaller side
+ * is below 128 to 24), with a least step of 2^-36, and products summed in fp32.  Of
+ * a bf16 update whose smaller side is 256 or more the last of several steps
+ * multiplies 11 bits.  Their values may not pass 16 (the singular values of X begin
+ * at 1 or less, and stay below 1.3 with the usual coefficients 3.4445, -4.775, 2.0315).
  * A matrix of zeros gives zeros if eps > 0.  batch is below 2^16.
  */
 size_t rsx_newton_schulz_workspace_size(size_t batch, size_t rows, size_t cols);
