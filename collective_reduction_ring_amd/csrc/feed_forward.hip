@@ -33,8 +33,9 @@ struct Slope {
 // 1 / (1 + exp(-z)) and the rest to 1, each with all its digits, in some fifteen
 // instructions: the exponential of -|z| by powers of two, with what the argument's
 // rounding took put back, and the hardware's reciprocal (one step off at most).
-// An epilogue has 65536 values a tile: with the library's exponential and divisions
-// the gradient's took longer than half of the tile's products.
+// (8192 x 4096 x 11008: the launches with the two epilogues take 1259 and 756 us, with
+// the library's exponential and divisions 1269 and 779; gelu, with the library's erfc
+// and exponential, 1315 and 803.)
 struct Logistic {
   float p, rest;
 };

@@ -175,7 +175,8 @@ class LinearLogprobsGrad(_Plan):
     """Prepared gradients of ``LinearLogprobs`` for gradients ``dlogprob`` and (with
     ``entropy``) ``dentropy``: ``dhidden`` of hidden's type, ``dweight`` of hidden's
     type or float32, added to what it holds with ``accumulate``; None with
-    ``inputs=False`` or ``weights=False``.  The logits are multiplied again, a piece
+    ``inputs=False`` or ``weights=False``.  A row without a gradient (padding, or
+    masked out of the loss) adds nothing, whatever it holds.  The logits are multiplied again, a piece
     of the vocabulary at a time; ``lse`` and ``lse_rest`` are the forward pass's."""
 
     def __init__(self, hidden, weight, tokens, lse, dlogprob, entropy=None, dentropy=None, dhidden=None, dweight=None,
@@ -248,7 +249,9 @@ class NewtonSchulz(_Plan):
     cols): ``out`` (``update`` itself for in place) is of its type and shape.
     ``steps`` times X = a X + (b A + c A A) X with A = X X^T, from ``update``
     divided by its Frobenius norm (plus ``eps``); the singular values all come
-    near 1."""
+    near 1.  The matrices of a stack may lie side by side in their rows, as the
+    slices of a fused projection do.  No value on the way may pass 16: none does
+    with coefficients that keep the singular values near 1."""
 
     def __init__(self, update, out=None, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps: float = 1e-7):
         batch, rows, cols, us, um = _stack(update, "update")
