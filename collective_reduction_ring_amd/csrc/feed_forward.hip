@@ -11,8 +11,8 @@
 // transposed in memory.
 //
 // What is rounded: s (and dg, du) to the matrices' type, as the next product's
-// operand (s in two parts of it, where the result is narrow); in fp32 they are kept
-// whole, as three bf16 parts.  g and u stay fp32 for the gradient: rounded to bf16 as well, they leave the weights' gradients off by
+// operand (s in two parts of it, where w_down is small); in fp32 they are kept whole,
+// as three bf16 parts.  g and u stay fp32 for the gradient: rounded to bf16 as well, they leave the weights' gradients off by
 // 3.5e-3 (rms) where one rounding of an operand and one of the result leave 2.4e-3;
 // their way through memory costs 3% more time (8192 x 4096 x 11008).
 //
@@ -203,13 +203,14 @@ uint64_t few_product_bytes(const FeedForwardArgs& a) { return (a.rows * copy_ld(
 // Parts of s.  Rounded once to 16 bits, it leaves a bf16 result of any size off by
 // 2.35e-3 (rms), in two parts by 1.66e-3, which is the result's own rounding.  The
 // second part doubles the down product's operations, or the reads of s with few
-// rows: for results narrower than kNarrow 0.2 to 5 us up to 1024 rows and 5 to 11
-// with 8192 (256 x 1024: 7.4 us for 7.2 with one row, 23 for 21, 44 for 33), for wide
-// ones up to a third of the time (1024 x 4096: 258 us for 193 with 8192 rows; 4096 x
-// 11008: 64 for 55.7 with 8, 2120 for 1590).  How many rows a call has plays no part:
-// a row has the same digits in any.
-constexpr uint64_t kNarrow = 512;
-int product_parts(const FeedForwardArgs& a) { return a.type == RSX_FLOAT32 ? 3 : a.dim < kNarrow ? 2 : 1; }
+// rows.  While w_down has fewer than kSmall elements that is 0.5 to 4 us up to 64 rows,
+// 9 at most with 1024 and 16 with 8192 (128 x 512: 6.7, 19.9 and 22.8 us with 1, 1024
+// and 8192 rows for 6.1, 15.6 and 18.0; 24 x 7104: 141 with 8192 for 111); with more it
+// grows with them (256 x 11008: 336 for 220; 4096 x 11008: 64 for 55.7 with 8 rows, 2120
+// for 1590 with 8192).  How many rows a call has plays no part: a row has the same
+// digits in any.
+constexpr uint64_t kSmall = 1 << 18;
+int product_parts(const FeedForwardArgs& a) { return a.type == RSX_FLOAT32 ? 3 : a.dim * a.hidden < kSmall ? 2 : 1; }
 // Parts of a matrix of `type` as an operand: fp32 is three bf16 values exactly.
 int parts_of(int type) { return type == RSX_FLOAT32 ? 3 : 1; }
 

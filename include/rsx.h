@@ -560,8 +560,8 @@ typedef enum {
  * x, out: [rows][dim]; w_gate, w_up: [hidden][dim]; w_down: [dim][hidden].
  * gate, up: [rows][hidden] fp32, dense: g and u for the gradient; or both null.
  * Between the products act(g) * u is rounded to `type` (fp16: infinite beyond 65504),
- * or, where dim is below 512, to the sum of two values of it, with which an infinity
- * in w_down may give a NaN; fp32: kept whole.
+ * or, where w_down has fewer than 2^18 elements, to the sum of two values of it, with
+ * which an infinity in w_down may give a NaN; fp32: kept whole.
  * out overlaps nothing that is read.
  */
 size_t rsx_feed_forward_workspace_size(size_t rows, size_t dim, size_t hidden, rsx_dtype_t type,

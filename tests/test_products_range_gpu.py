@@ -211,7 +211,7 @@ def test_fp32_head_keeps_its_digits(rows, vocab, dim, name):
 
 
 @pytest.mark.parametrize("t", [BF16, F16])
-@pytest.mark.parametrize("dim,hidden", [(4096, 264), (1024, 4100), (264, 520), (40, 5000), (511, 72), (512, 72)])
+@pytest.mark.parametrize("dim,hidden", [(4096, 264), (1024, 4100), (264, 520), (40, 5000), (512, 511), (512, 512)])
 def test_a_row_has_the_same_digits_in_any_call(dim, hidden, t):
     """How an operand is rounded does not depend on how many rows share the call."""
     say("same digits", dim, hidden, t)
@@ -229,5 +229,5 @@ def test_a_row_has_the_same_digits_in_any_call(dim, hidden, t):
         off = (rsx.feed_forward(x[:rows], wg, wu, wd).out.double() - whole[:rows]).square().mean().sqrt()
         apart = (once - whole)[:rows].square().mean().sqrt()
         # two parts leave the result's rounding, one adds its own; a tenth for what is random in either
-        want = rounding if dim < 512 else torch.hypot(rounding, apart)
+        want = rounding if dim * hidden < 1 << 18 else torch.hypot(rounding, apart)
         assert 0.9 * want < off < 1.1 * want, rows
