@@ -11,10 +11,11 @@
 // transposed in memory.
 //
 // What is rounded: s (and dg, du) to the matrices' type, as the next product's
-// operand (s in two parts of it, where w_down is small); in fp32 they are kept whole,
-// as three bf16 parts.  g and u stay fp32 for the gradient: rounded to bf16 as well, they leave the weights' gradients off by
-// 3.5e-3 (rms) where one rounding of an operand and one of the result leave 2.4e-3;
-// their way through memory costs 3% more time (8192 x 4096 x 11008).
+// operand (s in two parts of it, where w_down is small); in fp32 they are kept
+// whole, as three bf16 parts.  g and u stay fp32 for the gradient: rounded to bf16 as
+// well, they leave the weights' gradients off by 3.5e-3 (rms) where one rounding of an
+// operand and one of the result leave 2.4e-3; their way through memory costs 3% more
+// time (8192 x 4096 x 11008).
 //
 // The time is the tile products'.  8192 x 4096 x 11008 bf16: both projections 1240 us
 // (200 of them the writes of g, u and s), down 530 (1410 TFLOP/s), ds 860 (1.26 GB

@@ -618,6 +618,8 @@ rsx_status_t rsx_linear_logprobs(const void* hidden, size_t hidden_stride, const
  * A row whose token is outside [0, vocab) or whose dlogprob is 0, and whose
  * dentropy is 0 or null, has a gradient of 0 and adds nothing to dweight, whatever
  * its values are: NaN and infinities of a batch's padding stay there.
+ * dhidden is a product like any other: an infinity that masks a token in the
+ * forward pass makes it NaN, being multiplied with a dz of 0.
  * The vocabulary is taken in pieces of 4096 to 2^20 columns, of which the logits
  * are multiplied again; the workspace has dz of all rows for one of them, 2, 4
  * (fp16) or 6 (fp32) bytes each.
